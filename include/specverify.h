@@ -68,9 +68,11 @@ enum svf_device_status {
     SVF_DEV_BAD_LENGTH = 8, /* seq_lens[b] < 0 or the sequence overflows its page table */
     SVF_DEV_TIMEOUT = 16,   /* an internal wait gave up (the outputs of b are undefined) */
     SVF_DEV_BAD_PATH = 32,  /* accept_len or path[b] is not a root path in BFS order */
-    SVF_DEV_BAD_CLUSTER = 64 /* a kernel ran without the thread-block cluster it was
+    SVF_DEV_BAD_CLUSTER = 64, /* a kernel ran without the thread-block cluster it was
                                 launched for (e.g. re-launched by a tool that drops the
                                 cluster attribute); it did no work, outputs undefined */
+    SVF_DEV_NO_PAGES = 128,   /* the pool has too few free pages for this sequence */
+    SVF_DEV_BAD_ADAPTER = 256 /* an adapter id outside [-1, number of adapters) */
 };
 
 /* ------------------------------------------------------------------------
@@ -518,6 +520,158 @@ int svf_spec_accept_lmhead(const void *hidden, const void *weight, const float *
                            float *target_logits, int32_t *accept_len, int32_t *path,
                            int32_t *out_tokens, float *ratio, int32_t *lm_status,
                            int32_t *status, svf_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * svf_page_pool_init, svf_page_reserve, svf_page_release -- the page tables
+ * and slot maps of the paged KV cache, kept on the device from the requests'
+ * lengths.
+ *
+ * "EAGLE 演化史", § D.2: every tree node writes its own K/V in the verify pass
+ * and the entries of rejected nodes are rolled back page by page in the paged
+ * cache. A step reserves the tokens of its trees (or of a prompt), writes
+ * their K/V into the slots it was given (svf_rope_kv_write), verifies, commits
+ * (svf_kv_commit) and releases what was rejected; nothing goes through the
+ * host, and every call can be captured in a CUDA graph.
+ *
+ * A pool of num_pages pages is the caller's two arrays:
+ *   free_pages [num_pages] int32   a stack of page ids, free ones first
+ *   pool_state [4] int32           [0] the number of free pages; the others
+ *                                  are zero between calls
+ * svf_page_pool_init makes all pages free (page 0 is handed out first). A
+ * sequence of L tokens holds ceil(L / page_size) pages, at the front of its
+ * row of page_table [B, max_pages]; pages that the caller holds outside any
+ * table are taken off the stack by the caller. Calls on one pool (or one
+ * table) that may overlap on the GPU must be ordered by the caller.
+ *
+ * svf_page_reserve: room for new_lens[b] >= 0 more tokens of every sequence,
+ * whose length is seq_lens[b] (the lengths are not changed). Sequences are
+ * served in order: b gets the ceil((L+n)/page_size) - ceil(L/page_size) pages
+ * that it lacks if the pages asked for by sequences 0..b together are free, or
+ * if it lacks none; a sequence that is not served takes nothing, and its new
+ * page-table entries become -1.
+ *   rows        capacity of the row arrays below. Sequence b's new tokens are
+ *               rows row_offsets[b] .. row_offsets[b] + new_lens[b] - 1
+ *               (row_offsets [B+1] out: the running sum of new_lens, negative
+ *               ones counting as 0)
+ *   depth       [rows] int32, nullable: the depth of each row's tree node
+ *   slots       [rows] int32 out: page * page_size + offset of token L + i of
+ *               its sequence; -1 where the sequence was not served, and for
+ *               rows behind the last sequence
+ *   positions   [rows] int32 out, nullable: L + depth[row] where depth is
+ *               given, else L + i; 0 for rows behind the last sequence
+ *   status      [B] int32 out: SVF_DEV_NO_PAGES; SVF_DEV_BAD_LENGTH (a
+ *               negative length, more tokens than the table's row holds, or a
+ *               sequence with new tokens in a call whose new_lens add up to
+ *               more than rows; then the sequence takes nothing, its slots are
+ *               -1, its positions 0, and its table row stays);
+ *               SVF_DEV_BAD_PAGE (a page of its new tokens has an id outside
+ *               [0, num_pages): the slots in that page are -1)
+ *
+ * svf_page_release: the pages of tokens keep_lens[b] .. old_lens[b] - 1 that
+ * hold none of the first keep_lens[b] tokens go back to the pool, and their
+ * page-table entries become -1. After svf_kv_commit: old = L + N, keep =
+ * new_seq_lens; for a finished request: old = its length, keep = 0. A release
+ * of just what a reserve took restores the stack entry by entry.
+ *   n_released  [B] int32 out: pages given back
+ *   status      [B] int32 out: SVF_DEV_BAD_LENGTH (keep < 0, old < keep, or
+ *               old past the table's row); SVF_DEV_BAD_PAGE (one of the pages
+ *               has an id outside [0, num_pages), or all the pages of the call
+ *               are more than the pool can hold, as when they are given back
+ *               twice). A flagged sequence gives back nothing.
+ * Pages shared by two sequences are the caller's to count: each page must be
+ * in the range of one sequence only.
+ *
+ * Limits: B <= 8192, 1 <= page_size, num_pages * page_size and max_pages *
+ * page_size below 2^31, 1 <= num_pages < 2^30, 0 <= rows < 2^30.
+ * ---------------------------------------------------------------------- */
+int svf_page_pool_init(int32_t *free_pages, int32_t *pool_state, int num_pages,
+                       svf_stream_t stream);
+int svf_page_reserve(int32_t *page_table, int max_pages, int page_size, int32_t *free_pages,
+                     int32_t *pool_state, int num_pages, const int32_t *seq_lens,
+                     const int32_t *new_lens, int B, int rows, const int32_t *depth,
+                     int32_t *slots, int32_t *positions, int32_t *row_offsets, int32_t *status,
+                     svf_stream_t stream);
+int svf_page_release(int32_t *page_table, int max_pages, int page_size, int32_t *free_pages,
+                     int32_t *pool_state, int num_pages, const int32_t *old_lens,
+                     const int32_t *keep_lens, int B, int32_t *n_released, int32_t *status,
+                     svf_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * svf_rope_kv_write -- rotary positions of a step's q and k rows, and their
+ * K/V into the cache: what svf_tree_verify_attn takes (q post-RoPE, the
+ * tree's K/V written at its slots).
+ *
+ * "EAGLE 演化史", § Tree Verification 详解, B: the output of a node equals
+ * running prompt + root->node as an ordinary sequence, so node i stands at
+ * position L_b + depth(i) while its K/V sits at slot L_b + i. With
+ * c_i = rope[pos][i] and s_i = rope[pos][rot/2 + i], i < rot/2, every head of
+ * q and k becomes
+ *   x'_a = x_a c_i - x_b s_i,  x'_b = x_b c_i + x_a s_i,
+ *   (a, b) = (i, i + rot/2), or (2i, 2i + 1) if interleaved != 0,
+ * computed in fp32 and rounded once to dtype; elements from rot on stay.
+ *   q, k, v     [T, Hq, D], [T, Hkv, D], [T, Hkv, D] dtype; rows q_stride,
+ *               k_stride, v_stride elements apart, heads dense (slices of one
+ *               fused projection do)
+ *   rope        [max_pos, rot] float32: the cosines, then the sines
+ *   positions, slots [T] int32: svf_page_reserve's. Slot -1 leaves its row
+ *               out: nothing is read or written for it
+ *   q_out       [T, Hq, D] dtype, dense; may be q itself if q is dense
+ *   k_cache, v_cache  num_slots token rows of [Hkv, D] dtype (a paged cache
+ *               has num_pages * page_size)
+ *   status      [T] int32, may be NULL: SVF_DEV_BAD_PAGE (a slot outside
+ *               [-1, num_slots)), SVF_DEV_BAD_LENGTH (a position outside
+ *               [0, max_pos)). A flagged row's q_out is 0 and its K/V is not
+ *               written.
+ * Two rows with one slot leave either one's K/V there. Hq = 0 (q, q_out NULL)
+ * writes K/V alone.
+ * Limits: T <= 2^24; Hq <= 1024, 1 <= Hkv <= 1024; D <= 512 a multiple of 8
+ * (SVF_BF16) or 4 (SVF_F32); 2 <= rot <= D a multiple of 16 (SVF_BF16) or 8
+ * (SVF_F32); all pointers but positions, slots and status 16-byte aligned and
+ * strides multiples of 16 bytes.
+ * ---------------------------------------------------------------------- */
+int svf_rope_kv_write(const void *q, const void *k, const void *v, long long q_stride,
+                      long long k_stride, long long v_stride, int T, int Hq, int Hkv, int D,
+                      int dtype, const float *rope, int rot, int max_pos, int interleaved,
+                      const int32_t *positions, const int32_t *slots, void *q_out, void *k_cache,
+                      void *v_cache, int num_slots, int32_t *status, svf_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * svf_lora_proj -- a projection shared by all requests, with a low-rank
+ * adapter of its own for each.
+ *
+ * "EAGLE 演化史", § Tree Verification 详解, A: one forward pass of the target
+ * model over all tree nodes; a target served with per-request adapters has
+ *   y[r] = W x[r] + scales[a] * B_a (A_a x[r]),   a = ids[r / rows_per_id],
+ * in each of its projections (a = -1: y[r] = W x[r]). bf16 operands and
+ * results, all sums in fp32 (the inner products A_a x[r] enter the second
+ * product with 16 bits of significand), one rounding at the end.
+ *   x        [R, H] bf16, rows x_stride elements apart       in
+ *   weight   [O, H] bf16                                     in
+ *   lora_a   [adapters, rank, H] bf16                        in
+ *   lora_b   [adapters, O, rank] bf16                        in
+ *            (adapters of a smaller rank are padded with zeros)
+ *   scales   [adapters] float32, NULL: 1                     in
+ *   ids      [R / rows_per_id] int32, in [-1, adapters)      in
+ *   y        [R, O] bf16, rows y_stride elements apart       out
+ *   workspace  device scratch of svf_lora_proj_workspace_size(R, rank) bytes,
+ *            16-byte aligned; nothing in it needs to be kept or zeroed. Calls
+ *            that may overlap on the GPU need workspaces of their own.
+ *   status   [R / rows_per_id] int32 out: SVF_DEV_BAD_ADAPTER (an id outside
+ *            [-1, adapters): the rows of that id are 0); SVF_DEV_TIMEOUT or
+ *            SVF_DEV_BAD_CLUSTER in status[0] if the kernel gave up (y is then
+ *            undefined)
+ * An infinity or NaN in a row of x or in an adapter reaches the rows that use
+ * it and no others.
+ * Limits: 1 <= R <= 2^20, R a multiple of rows_per_id >= 1; H <= 65536 a
+ * multiple of 8; 1 <= O <= 2^20; rank <= 128 a multiple of 8; 1 <= adapters <=
+ * 65536; x, weight, lora_a and lora_b 16-byte aligned, x_stride a multiple of
+ * 8, x_stride >= H and y_stride >= O. y must not overlap an input.
+ * ---------------------------------------------------------------------- */
+size_t svf_lora_proj_workspace_size(int R, int rank);
+int svf_lora_proj(const void *x, long long x_stride, const void *weight, const void *lora_a,
+                  const void *lora_b, const float *scales, const int32_t *ids, int rows_per_id,
+                  int R, int H, int O, int adapters, int rank, void *y, long long y_stride,
+                  void *workspace, size_t workspace_bytes, int32_t *status, svf_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * svf_debug_set_attn_wait_ns -- test hook: the deadline of every internal

@@ -29,6 +29,7 @@ SVF_OK, SVF_ERR_ARG, SVF_ERR_UNSUPPORTED, SVF_ERR_LAUNCH, SVF_ERR_WORKSPACE = 0,
 SVF_ERR_SCRATCH_LIMIT = -5
 SVF_DEV_BAD_PARENT, SVF_DEV_BAD_TOKEN, SVF_DEV_BAD_PAGE, SVF_DEV_BAD_LENGTH, SVF_DEV_TIMEOUT = (
     1, 2, 4, 8, 16)
+SVF_DEV_BAD_PATH, SVF_DEV_BAD_CLUSTER, SVF_DEV_NO_PAGES, SVF_DEV_BAD_ADAPTER = 32, 64, 128, 256
 
 EXPORTED = [
     "svf_tree_mask_build",
@@ -53,6 +54,12 @@ EXPORTED = [
     "svf_eagle2_init",
     "svf_eagle2_expand",
     "svf_eagle2_finalize",
+    "svf_page_pool_init",
+    "svf_page_reserve",
+    "svf_page_release",
+    "svf_rope_kv_write",
+    "svf_lora_proj_workspace_size",
+    "svf_lora_proj",
     "svf_status_string",
     "svf_version",
 ]
@@ -122,6 +129,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.svf_debug_set_attn_splits.restype = I
     lib.svf_debug_set_attn_kernel.argtypes = [I]
     lib.svf_debug_set_attn_kernel.restype = I
+    L = ctypes.c_longlong
+    lib.svf_page_pool_init.argtypes = [P, P, I, P]
+    lib.svf_page_pool_init.restype = I
+    lib.svf_page_reserve.argtypes = [P, I, I, P, P, I, P, P, I, I, P, P, P, P, P, P]
+    lib.svf_page_reserve.restype = I
+    lib.svf_page_release.argtypes = [P, I, I, P, P, I, P, P, I, P, P, P]
+    lib.svf_page_release.restype = I
+    lib.svf_rope_kv_write.argtypes = [P, P, P, L, L, L, I, I, I, I, I, P, I, I, I, P, P, P, P, P,
+                                      I, P, P]
+    lib.svf_rope_kv_write.restype = I
+    lib.svf_lora_proj_workspace_size.argtypes = [I, I]
+    lib.svf_lora_proj_workspace_size.restype = Z
+    lib.svf_lora_proj.argtypes = [P, L, P, P, P, P, P, I, I, I, I, I, I, P, L, P, Z, P, P]
+    lib.svf_lora_proj.restype = I
     lib.svf_status_string.argtypes = [I]
     lib.svf_status_string.restype = ctypes.c_char_p
     lib.svf_version.argtypes = []
@@ -654,6 +675,246 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Te
         _ptr(o["n_freed"]), _ptr(o["status"]), _stream(stream))
     _check(rc, "svf_kv_commit")
     return o
+
+
+# ---------------------------------------------------------------------------
+# The operators around the verify pass: pages, rotary K/V write, projections
+# with per-request adapters. Their calls are short, so each tensor is checked
+# in one expression, and the message is put together only for a bad one.
+# ---------------------------------------------------------------------------
+
+def _device_of(t, name: str) -> int:
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise SpecVerifyError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _bad(t, name: str, dtype, shape, dev: int):
+    if isinstance(t, torch.Tensor) and t.get_device() >= 0 and t.get_device() != dev:
+        raise SpecVerifyError(f"{name} must be on cuda:{dev}, got {t.device}")
+    _dev(t, name, dtype, shape)
+    raise SpecVerifyError(f"{name} is not a usable tensor")
+
+
+def _p(t, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this dtype, shape and device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    _bad(t, name, dtype, shape, dev)
+
+
+def _call(fn, what: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) with ``dev`` current; the default stream is the
+    current one of that device."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, what, dev, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    rc = fn(*args, stream.cuda_stream)
+    if rc != SVF_OK:
+        _check(rc, what)
+
+
+def _out(o: dict, key: str, dtype, shape, like: torch.Tensor, dev: int) -> int:
+    """The address of output ``key``, allocated on first use."""
+    t = o.get(key)
+    if t is None:
+        t = o[key] = torch.empty(shape, dtype=dtype, device=like.device)
+        return t.data_ptr()
+    return _p(t, key, dtype, shape, dev)
+
+
+def _pool(pool: dict, dev: int):
+    free, n = pool["free"], pool["free"].numel()
+    return (_p(free, "pool['free']", torch.int32, (n,), dev),
+            _p(pool["state"], "pool['state']", torch.int32, (4,), dev), n)
+
+
+def page_pool(num_pages: int, device="cuda", stream=None) -> dict:
+    """A pool of ``num_pages`` pages, all free: ``free`` [num_pages] int32 (a
+    stack of page ids) and ``state`` [4] int32 (state[0] free pages)."""
+    if num_pages < 1:
+        raise SpecVerifyError("num_pages must be at least 1")
+    pool = {"free": torch.empty((num_pages,), dtype=torch.int32, device=device),
+            "state": torch.empty((4,), dtype=torch.int32, device=device)}
+    dev = _device_of(pool["free"], "device")
+    free, state, n = _pool(pool, dev)
+    _call(load_library().svf_page_pool_init, "svf_page_pool_init", dev, stream, free, state, n)
+    return pool
+
+
+def page_reserve(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                 new_lens: torch.Tensor, page_size: int, rows: int,
+                 depth: Optional[torch.Tensor] = None, outputs: Optional[dict] = None,
+                 stream=None) -> dict:
+    """Pages and slots for ``new_lens`` [B] more tokens of sequences of
+    ``seq_lens`` [B] tokens (int32), in place in ``page_table`` [B, max_pages]
+    int32 and the pool. ``rows`` is the capacity of the row arrays: sequence
+    b's new tokens are rows row_offsets[b] .. row_offsets[b + 1]. ``depth``
+    (int32, ``rows`` values in any shape, e.g. tree_mask_build's) makes a
+    row's position seq_lens + depth instead of seq_lens + i. Returns device
+    tensors slots [rows], positions [rows], row_offsets [B + 1], status [B]."""
+    lib = _lib or load_library()
+    dev = _device_of(page_table, "page_table")
+    if page_table.dim() != 2:
+        raise SpecVerifyError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    i32 = torch.int32
+    o = outputs if outputs is not None else {}
+    free, state, n = _pool(pool, dev)
+    d = None
+    if depth is not None:
+        if depth.numel() != rows:
+            raise SpecVerifyError("depth must hold one value per row")
+        d = _p(depth, "depth", i32, depth.shape, dev)
+    _call(lib.svf_page_reserve, "svf_page_reserve", dev, stream,
+          _p(page_table, "page_table", i32, (B, max_pages), dev), max_pages, page_size, free,
+          state, n, _p(seq_lens, "seq_lens", i32, (B,), dev),
+          _p(new_lens, "new_lens", i32, (B,), dev), B, rows, d,
+          _out(o, "slots", i32, (rows,), page_table, dev),
+          _out(o, "positions", i32, (rows,), page_table, dev),
+          _out(o, "row_offsets", i32, (B + 1,), page_table, dev),
+          _out(o, "status", i32, (B,), page_table, dev))
+    return o
+
+
+def page_release(pool: dict, page_table: torch.Tensor, old_lens: torch.Tensor,
+                 keep_lens: torch.Tensor, page_size: int, outputs: Optional[dict] = None,
+                 stream=None) -> dict:
+    """Give the pages past the first ``keep_lens`` [B] of ``old_lens`` [B]
+    tokens back to the pool (after kv_commit: seq_lens + N and new_seq_lens;
+    for finished requests keep 0). Returns n_released [B], status [B]."""
+    lib = _lib or load_library()
+    dev = _device_of(page_table, "page_table")
+    if page_table.dim() != 2:
+        raise SpecVerifyError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    i32 = torch.int32
+    o = outputs if outputs is not None else {}
+    free, state, n = _pool(pool, dev)
+    _call(lib.svf_page_release, "svf_page_release", dev, stream,
+          _p(page_table, "page_table", i32, (B, max_pages), dev), max_pages, page_size, free,
+          state, n, _p(old_lens, "old_lens", i32, (B,), dev),
+          _p(keep_lens, "keep_lens", i32, (B,), dev), B,
+          _out(o, "n_released", i32, (B,), page_table, dev),
+          _out(o, "status", i32, (B,), page_table, dev))
+    return o
+
+
+def _rows(t, name: str, dtype, shape, dev: int):
+    """Address and row stride of [T, heads, D] with dense heads."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.shape == shape):
+        _bad(t, name, dtype, shape, dev)
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and shape[2] > 1) or (s1 != shape[2] and shape[1] > 1):
+        raise SpecVerifyError(f"{name} must have dense heads (strides [row, D, 1])")
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1] * shape[2]
+
+
+def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor,
+                  positions: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+                  interleaved: bool = False, status: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions of q and k rows, and the K/V write into the cache.
+
+    q [T, Hq, D], k and v [T, Hkv, D] float32 or bfloat16, heads dense, rows
+    any distance apart (slices of a fused projection); rope [max_pos, rot]
+    float32, cosines then sines; positions, slots [T] int32 (page_reserve's;
+    slot -1 leaves a row out); k_cache, v_cache [num_pages, page_size, Hkv, D].
+    Returns (q_out [T, Hq, D], status [T] int32). Rows that are left out keep
+    what q_out held (a new q_out: undefined)."""
+    lib = _lib or load_library()
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
+        raise SpecVerifyError("q and k must be [T, heads, D], the caches [pages, page_size, Hkv, D]")
+    T, Hq, D = q.shape
+    Hkv, dt = k.shape[1], q.dtype
+    qp, qs = _rows(q, "q", dt, (T, Hq, D), dev)
+    kp, ks = _rows(k, "k", dt, (T, Hkv, D), dev)
+    vp, vs = _rows(v, "v", dt, (T, Hkv, D), dev)
+    if rope.dim() != 2:
+        raise SpecVerifyError("rope must be [max_pos, rot]")
+    max_pos, rot = rope.shape
+    pages, ps = k_cache.shape[:2]
+    cache = (pages, ps, Hkv, D)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+    if status is None:
+        status = torch.empty((T,), dtype=torch.int32, device=q.device)
+    _call(lib.svf_rope_kv_write, "svf_rope_kv_write", dev, stream, qp, kp, vp, qs, ks, vs, T, Hq,
+          Hkv, D, _dtype_code(dt), _p(rope, "rope", torch.float32, (max_pos, rot), dev), rot,
+          max_pos, 1 if interleaved else 0,
+          _p(positions, "positions", torch.int32, (T,), dev),
+          _p(slots, "slots", torch.int32, (T,), dev), _p(q_out, "q_out", dt, (T, Hq, D), dev),
+          _p(k_cache, "k_cache", dt, cache, dev), _p(v_cache, "v_cache", dt, cache, dev),
+          pages * ps, _p(status, "status", torch.int32, (T,), dev))
+    return q_out, status
+
+
+def lora_proj_workspace_size(R: int, rank: int) -> int:
+    return int((_lib or load_library()).svf_lora_proj_workspace_size(R, rank))
+
+
+def lora_proj(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+              ids: torch.Tensor, scales: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None):
+    """out = x weight^T + scales[a] (x lora_a[a]^T) lora_b[a]^T with one adapter
+    a = ids[g] per group of rows (-1: none).
+
+    x [..., H] bfloat16 of R rows (2-D: rows any multiple of 8 elements apart),
+    weight [O, H], lora_a [adapters, rank, H], lora_b [adapters, O, rank]
+    bfloat16; ids [G] int32, group g being the R / G rows from g R / G on
+    (x [B, N, H] with ids [B]: one adapter per request); scales [adapters]
+    float32. Returns (out [..., O] bfloat16, status [G] int32)."""
+    lib = _lib or load_library()
+    dev = _device_of(x, "x")
+    bf = torch.bfloat16
+    if weight.dim() != 2 or lora_a.dim() != 3:
+        raise SpecVerifyError("weight must be [O, H] and lora_a [adapters, rank, H]")
+    O, H = weight.shape
+    adapters, rank = lora_a.shape[:2]
+    if x.dtype is not bf or x.dim() < 1 or x.shape[-1] != H:
+        raise SpecVerifyError("x must be bfloat16 [..., H] with weight's H")
+    if x.is_contiguous():
+        xs = H
+    elif x.dim() == 2 and x.stride(1) == 1:
+        xs = x.stride(0)
+    else:
+        raise SpecVerifyError("x must be contiguous, or 2-D with dense rows")
+    R = x.numel() // H if H > 0 else 0
+    G = ids.shape[0] if ids.dim() == 1 else 0
+    if R > 0 and (G < 1 or R % G):
+        raise SpecVerifyError("ids must be [G] with G dividing the rows of x")
+    shape = x.shape[:-1] + (O,)
+    if out is None:
+        out = torch.empty(shape, dtype=bf, device=x.device)
+    if out.dim() == 2 and out.shape[0] > 1 and not out.is_contiguous():
+        if out.stride(1) != 1 or out.shape != shape or out.dtype is not bf \
+                or out.get_device() != dev:
+            raise SpecVerifyError("out must be bfloat16 [..., O] with dense rows")
+        op, os_ = out.data_ptr(), out.stride(0)
+    else:
+        op, os_ = _p(out, "out", bf, shape, dev), O
+    if status is None:
+        status = torch.empty((G,), dtype=torch.int32, device=x.device)
+    need = R * rank * 4
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise SpecVerifyError("workspace must be a contiguous tensor on x's device")
+    _call(lib.svf_lora_proj, "svf_lora_proj", dev, stream, x.data_ptr(), xs,
+          _p(weight, "weight", bf, (O, H), dev), _p(lora_a, "lora_a", bf, (adapters, rank, H), dev),
+          _p(lora_b, "lora_b", bf, (adapters, O, rank), dev),
+          None if scales is None else _p(scales, "scales", torch.float32, (adapters,), dev),
+          _p(ids, "ids", torch.int32, (G,), dev), R // G if G else 1, R, H, O, adapters, rank,
+          op, os_, workspace.data_ptr(), workspace.nbytes,
+          _p(status, "status", torch.int32, (G,), dev))
+    return out, status
 
 
 # ---------------------------------------------------------------------------

@@ -22,7 +22,8 @@ LIB = os.path.join(OUT, "libspecverify.so")
 SOURCES = ["mask.cu", "attn_simt.cu", "attn_tc.cu", "attn_sk.cu", "accept.cu", "accept_stream.cu",
            "accept_target_stream.cu",
            "accept_noalloc.cu", "accept_target.cu", "eagle2.cu",
-           "kv_commit.cu", "lm_head.cu", "selftest.cu", "api.cu"]
+           "kv_commit.cu", "lm_head.cu", "lora_proj.cu", "lora_shrink.cu", "pages.cu",
+           "rope_kv.cu", "selftest.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "lora.h"
 
 namespace svf {
 
@@ -52,6 +53,8 @@ const char *svf_status_string(int code) {
         case SVF_DEV_TIMEOUT: return "device: an internal wait timed out";
         case SVF_DEV_BAD_PATH: return "device: accepted path is not a root path in BFS order";
         case SVF_DEV_BAD_CLUSTER: return "device: kernel ran without its thread-block cluster";
+        case SVF_DEV_NO_PAGES: return "device: too few free pages in the pool";
+        case SVF_DEV_BAD_ADAPTER: return "device: adapter id outside the adapters";
         default: return "unknown status";
     }
 }
@@ -197,6 +200,152 @@ int svf_debug_set_attn_kernel(int which) {
     if (which < 0 || which > 2) return SVF_ERR_ARG;
     attn_set_kernel(which);
     return SVF_OK;
+}
+
+// What the two calls on a page table and its pool have in common.
+static int page_arg_check(const void *page_table, int max_pages, int page_size,
+                          const void *free_pages, const void *pool_state, int num_pages,
+                          const void *lens_a, const void *lens_b, int B) {
+    if (!page_table || !free_pages || !pool_state || !lens_a || !lens_b) return SVF_ERR_ARG;
+    if (B > kMaxPageSequences || max_pages < 1 || page_size < 1 || num_pages < 1 ||
+        num_pages >= (1 << 30) || (long long)num_pages * page_size > INT_MAX ||
+        (long long)max_pages * page_size > INT_MAX)
+        return SVF_ERR_UNSUPPORTED;
+    return SVF_OK;
+}
+
+int svf_page_pool_init(int32_t *free_pages, int32_t *pool_state, int num_pages,
+                       svf_stream_t stream) {
+    if (num_pages < 0 || !free_pages || !pool_state) return SVF_ERR_ARG;
+    if (num_pages < 1 || num_pages >= (1 << 30)) return SVF_ERR_UNSUPPORTED;
+    cudaError_t e = launch_page_pool_init(free_pages, pool_state, num_pages,
+                                          reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+int svf_page_reserve(int32_t *page_table, int max_pages, int page_size, int32_t *free_pages,
+                     int32_t *pool_state, int num_pages, const int32_t *seq_lens,
+                     const int32_t *new_lens, int B, int rows, const int32_t *depth,
+                     int32_t *slots, int32_t *positions, int32_t *row_offsets, int32_t *status,
+                     svf_stream_t stream) {
+    if (B < 0 || rows < 0) return SVF_ERR_ARG;
+    if (B == 0) return SVF_OK;
+    if ((rows > 0 && !slots) || !row_offsets || !status) return SVF_ERR_ARG;
+    const int rc = page_arg_check(page_table, max_pages, page_size, free_pages, pool_state,
+                                  num_pages, seq_lens, new_lens, B);
+    if (rc != SVF_OK) return rc;
+    if (rows >= (1 << 30) - 1) return SVF_ERR_UNSUPPORTED;
+    const PageReserveArgs a = {page_table, seq_lens, new_lens,  depth,       free_pages,
+                               pool_state, slots,    positions, row_offsets, status,
+                               B,          max_pages, page_size, num_pages,  rows};
+    cudaError_t e = launch_page_reserve(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+int svf_page_release(int32_t *page_table, int max_pages, int page_size, int32_t *free_pages,
+                     int32_t *pool_state, int num_pages, const int32_t *old_lens,
+                     const int32_t *keep_lens, int B, int32_t *n_released, int32_t *status,
+                     svf_stream_t stream) {
+    if (B < 0) return SVF_ERR_ARG;
+    if (B == 0) return SVF_OK;
+    if (!n_released || !status) return SVF_ERR_ARG;
+    const int rc = page_arg_check(page_table, max_pages, page_size, free_pages, pool_state,
+                                  num_pages, old_lens, keep_lens, B);
+    if (rc != SVF_OK) return rc;
+    const PageReleaseArgs a = {page_table, old_lens,   keep_lens, free_pages, pool_state,
+                               n_released, status,     B,         max_pages,  page_size,
+                               num_pages};
+    cudaError_t e = launch_page_release(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+int svf_rope_kv_write(const void *q, const void *k, const void *v, long long q_stride,
+                      long long k_stride, long long v_stride, int T, int Hq, int Hkv, int D,
+                      int dtype, const float *rope, int rot, int max_pos, int interleaved,
+                      const int32_t *positions, const int32_t *slots, void *q_out, void *k_cache,
+                      void *v_cache, int num_slots, int32_t *status, svf_stream_t stream) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || D < 0 || rot < 0 || max_pos < 0 || num_slots < 0)
+        return SVF_ERR_ARG;
+    if (T == 0) return SVF_OK;
+    if ((Hq > 0 && (!q || !q_out)) || !k || !v || !rope || !positions || !slots || !k_cache ||
+        !v_cache)
+        return SVF_ERR_ARG;
+    if (dtype != SVF_F32 && dtype != SVF_BF16) return SVF_ERR_UNSUPPORTED;
+    const int es = dtype == SVF_F32 ? 4 : 2;
+    if (!rope_kv_supported(T, Hq, Hkv, D, rot, es)) return SVF_ERR_UNSUPPORTED;
+    const long long unit = 16 / es;
+    if ((Hq > 0 && (q_stride < (long long)Hq * D || q_stride % unit || !aligned16(q) ||
+                    !aligned16(q_out))) ||
+        k_stride < (long long)Hkv * D || k_stride % unit || v_stride < (long long)Hkv * D ||
+        v_stride % unit || !aligned16(k) || !aligned16(v) || !aligned16(rope) ||
+        !aligned16(k_cache) || !aligned16(v_cache))
+        return SVF_ERR_ARG;
+    RopeKvArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.rope = rope;
+    a.positions = positions;
+    a.slots = slots;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.rot = rot;
+    a.max_pos = max_pos;
+    a.num_slots = num_slots;
+    a.elem_size = es;
+    a.interleaved = interleaved != 0;
+    a.q_out = q_out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.status = status;
+    cudaError_t e = launch_rope_kv(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+size_t svf_lora_proj_workspace_size(int R, int rank) {
+    if (R <= 0 || rank <= 0) return 0;
+    return (size_t)R * (size_t)rank * sizeof(float);
+}
+
+int svf_lora_proj(const void *x, long long x_stride, const void *weight, const void *lora_a,
+                  const void *lora_b, const float *scales, const int32_t *ids, int rows_per_id,
+                  int R, int H, int O, int adapters, int rank, void *y, long long y_stride,
+                  void *workspace, size_t workspace_bytes, int32_t *status, svf_stream_t stream) {
+    if (R < 0 || H < 0 || O < 0 || adapters < 0 || rank < 0) return SVF_ERR_ARG;
+    if (R == 0) return SVF_OK;
+    if (!x || !weight || !lora_a || !lora_b || !ids || !y || !status) return SVF_ERR_ARG;
+    if (rows_per_id < 1 || R % rows_per_id != 0) return SVF_ERR_ARG;
+    if (!lora_proj_supported(R, H, O, adapters, rank)) return SVF_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(lora_a) || !aligned16(lora_b) ||
+        x_stride < H || x_stride % 8 != 0 || y_stride < O)
+        return SVF_ERR_ARG;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < svf_lora_proj_workspace_size(R, rank))
+        return SVF_ERR_WORKSPACE;
+    LoraArgs a;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.weight = weight;
+    a.lora_a = lora_a;
+    a.lora_b = lora_b;
+    a.scales = scales;
+    a.ids = ids;
+    a.rows_per_id = rows_per_id;
+    a.R = R;
+    a.H = H;
+    a.O = O;
+    a.adapters = adapters;
+    a.rank = rank;
+    a.y = y;
+    a.y_stride = y_stride;
+    a.workspace = workspace;
+    a.status = status;
+    return launch_lora_proj(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int svf_lm_head(const void *hidden, const void *weight, int R, int H, int V, float *logits,

@@ -96,6 +96,42 @@ struct KvCommitArgs {
 };
 cudaError_t launch_kv_commit(const KvCommitArgs &a, cudaStream_t stream);
 
+// Page tables and slot maps of the paged cache (pages.cu).
+constexpr int kMaxPageSequences = 8192;
+struct PageReserveArgs {
+    int32_t *page_table;
+    const int32_t *seq_lens, *new_lens, *depth;
+    const int32_t *free_pages;
+    int32_t *pool_state;
+    int32_t *slots, *positions, *row_offsets, *status;
+    int B, max_pages, page_size, num_pages, rows;
+};
+struct PageReleaseArgs {
+    int32_t *page_table;
+    const int32_t *old_lens, *keep_lens;
+    int32_t *free_pages, *pool_state;
+    int32_t *n_released, *status;
+    int B, max_pages, page_size, num_pages;
+};
+cudaError_t launch_page_pool_init(int32_t *free_pages, int32_t *state, int num_pages,
+                                  cudaStream_t stream);
+cudaError_t launch_page_reserve(const PageReserveArgs &a, cudaStream_t stream);
+cudaError_t launch_page_release(const PageReleaseArgs &a, cudaStream_t stream);
+
+// Rotary positions and the K/V write of a step's rows (rope_kv.cu).
+struct RopeKvArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;  // elements between rows
+    const float *rope;
+    const int32_t *positions, *slots;
+    int T, Hq, Hkv, D, rot, max_pos, num_slots, elem_size;
+    bool interleaved;
+    void *q_out, *k_cache, *v_cache;
+    int32_t *status;
+};
+bool rope_kv_supported(int T, int Hq, int Hkv, int D, int rot, int elem_size);
+cudaError_t launch_rope_kv(const RopeKvArgs &a, cudaStream_t stream);
+
 // Arguments of one tree-attention call, shared by both attention kernels.
 struct AttnArgs {
     const void *q;
@@ -172,6 +208,12 @@ cudaError_t launch_accept_stream(const float *target, const float *draft, const 
 bool lm_head_supported(int R, int H, int V);
 int launch_lm_head(const void *hidden, const void *weight, int R, int H, int V, float *logits,
                    int32_t *status, cudaStream_t stream);
+
+// A projection with a low-rank adapter per request (lora_proj.cu). Returns an
+// svf_status.
+struct LoraArgs;
+bool lora_proj_supported(int R, int H, int O, int adapters, int rank);
+int launch_lora_proj(const LoraArgs &a, cudaStream_t stream);
 
 int num_sms();
 
