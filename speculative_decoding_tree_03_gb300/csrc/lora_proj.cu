@@ -32,9 +32,10 @@
 //   warp 0      producer: TMA of W and x blocks, then of B_a blocks;
 //   warp 1      MMA issuer (of the pair's first CTA);
 //   warps 2-5   epilogue (tensor memory -> y);
-//   warps 6-9   adapters: warp 6 lists the tile's distinct adapters; all four
-//               wait for a block's B_a tiles, look them over, and write t's hi
-//               and lo next to them.
+//   warps 6-9   adapters: warp 6 lists the tile's distinct adapters; each of
+//               the four takes the adapter blocks of every fourth stage: waits
+//               for the B_a tiles, looks them over, and writes t's hi and lo
+//               next to them.
 // The t columns come last, so the shared product runs while lora_shrink still
 // does (the launches overlap; only warps 6-9 wait for it).
 //
@@ -44,7 +45,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <map>
 #include <mutex>
+#include <tuple>
 
 #include "common.cuh"
 #include "internal.h"
@@ -58,9 +61,9 @@ constexpr int BK = 64;                  // K per stage: one 128-byte swizzle row
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int MAX_STAGES = 12;
 constexpr int THREADS = 320;
-constexpr int ADAPTER_THREADS = 128;
 constexpr int MAX_BN = 256;
 constexpr int MAX_LIST = 2 * MAX_BN;    // adapter windows of one row tile
+constexpr int HASH = 2 * MAX_BN;        // slots for the distinct adapters of a row tile
 constexpr int SMEM_ONE = 192 * 1024;    // stage ring of a CTA that has its SM alone
 constexpr int SMEM_TWO = 88 * 1024;     // ... that shares its SM with another
 }  // namespace lp
@@ -90,9 +93,13 @@ struct LpShared {
     int ids[2][lp::MAX_BN];     // adapter of each row of the tile; -1 none, -2 a bad id
     int2 list[2][lp::MAX_LIST]; // adapter; first row and row count of its window
     int n_list[2];
-    int nonfinite[2];
+    int nonfinite[2];           // some B_a tile held an infinity or NaN
+    int bad_id[2];              // some row's id is bad
+    // the list's hash table: adapter id and number, and each one's first and last row
+    int hash_id[lp::HASH], hash_no[lp::HASH], span[lp::MAX_BN];
     uint32_t tmem;
     int committed;  // stages whose products were issued
+    uint32_t par_main, par_ext, any_main, any_ext;  // the producer's, at its end
     int abort;
 };
 
@@ -102,24 +109,35 @@ __device__ __forceinline__ bool lp_wait(uint64_t *bar, uint32_t parity, volatile
     return __all_sync(0xffffffffu, ok);
 }
 
-// The same for a barrier that another CTA's threads arrive on.
+// A thread's wait for a barrier that threads of another CTA arrive on.
 __device__ __forceinline__ bool lp_wait_cluster(uint64_t *bar, uint32_t parity,
                                                 volatile int *abort, unsigned long long ns) {
-    bool ok = mbar_try_wait_cluster(bar, parity);
-    if (!ok) {
-        const unsigned long long t0 = globaltimer_ns();
-        for (uint32_t it = 1;; ++it) {
-            if ((ok = mbar_try_wait_cluster(bar, parity))) break;
-            if ((it & 63u) == 0) {
-                if (*abort) break;
-                if (globaltimer_ns() - t0 > ns) {
-                    *abort = 1;
-                    break;
-                }
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > ns) {
+                *abort = 1;
+                return false;
             }
         }
     }
-    return __all_sync(0xffffffffu, ok);
+}
+
+// One lane of a converged warp. tcgen05 and TMA instructions take their
+// operands from uniform registers; under this predicate the compiler knows that
+// one thread runs them and needs no loop over lanes around each (under
+// `lane == 0` every block of K took 0.43 us whatever its size).
+__device__ __forceinline__ bool lp_elect() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // Arrive on a barrier of another CTA of the cluster (an address from cluster_map).
@@ -211,58 +229,91 @@ __device__ __forceinline__ bool bf16_nonfinite2(uint32_t w) {
 
 // The distinct adapters of rows [n0, n0 + BN), in order of first appearance,
 // each with the window of the tile that holds its rows (16 CG rows aligned),
-// in pieces of at most BN / 2 rows. One warp. At most 3 pieces for an adapter
-// of two rows or more and one for the others: 1.5 BN in all.
+// in pieces of at most BN / 2 rows: at most 3 pieces for an adapter of two
+// rows or more and one for the others, 1.5 BN in all. One warp, 32 rows at a
+// time: lanes with the same id are matched, the first of each looks the id up
+// in a hash table in shared memory (about 1 us for 256 rows; looking at the
+// rows one after the other took 0.35 us a row).
 template <int CG>
 __device__ void lp_build_list(const LpParams &p, LpShared *sh, int buf, int n0, int lane) {
     constexpr int G = 16 * CG;
-    int v[lp::MAX_BN / 32];
-    const int chunks = p.BN / 32;
-#pragma unroll
-    for (int c = 0; c < lp::MAX_BN / 32; ++c) {
-        v[c] = -1;
-        if (c < chunks) {
-            const int row = n0 + c * 32 + lane;
-            if (row < p.R) {
-                const int id = p.ids[row / p.per];
-                v[c] = id < -1 || id >= p.adapters ? -2 : id;
-            }
-            sh->ids[buf][c * 32 + lane] = v[c];
-        }
-    }
+    for (int k = lane; k < lp::HASH; k += 32) sh->hash_id[k] = -1;
     __syncwarp();
-    int n = 0;
-    // only the first row of a group can be the first of an adapter
-    int i = 0;
-    while (i < p.BN && n0 + i < p.R) {
-        const int id = sh->ids[buf][i];
-        if (id >= 0) {
-            int first = -1, last = -1;
-#pragma unroll
-            for (int c = 0; c < lp::MAX_BN / 32; ++c) {
-                const unsigned m = __ballot_sync(0xffffffffu, v[c] == id);
-                if (m) {
-                    if (first < 0) first = c * 32 + __ffs(m) - 1;
-                    last = c * 32 + 31 - __clz(m);
-                }
+    int n = 0;  // distinct adapters so far
+    bool any_bad = false;
+    for (int c = 0; c < p.BN; c += 32) {
+        const int row = n0 + c + lane;
+        int id = -1;
+        if (row < p.R) {
+            id = p.ids[row / p.per];
+            if (id < -1 || id >= p.adapters) id = -2;
+        }
+        sh->ids[buf][c + lane] = id;
+        any_bad |= id == -2;
+        const unsigned same = __match_any_sync(0xffffffffu, id);
+        bool fresh = false;
+        int slot = 0;
+        if (id >= 0 && lane == __ffs(same) - 1) {
+            slot = (int)((unsigned)id * 2654435761u >> 23);  // 512 slots
+            while (true) {
+                const int was = atomicCAS(&sh->hash_id[slot], -1, id);
+                fresh = was == -1;
+                if (fresh || was == id) break;
+                slot = (slot + 1) & (lp::HASH - 1);  // at most 256 ids: a slot is free
             }
-            if (first == i) {
-                int w0 = first & ~(G - 1);
-                const int w1 = (last + G) & ~(G - 1);
-                const int most = (p.BN / 2) & ~(G - 1);
-                while (w0 < w1) {
-                    const int len = min(w1 - w0, most);
-                    if (lane == 0) sh->list[buf][n] = make_int2(id, w0 | len << 16);
-                    ++n;
-                    w0 += len;
-                }
+            const int last = c + 31 - __clz(same);
+            if (!fresh) {
+                const int no = sh->hash_no[slot];
+                sh->span[no] = (sh->span[no] & 0xffff) | last << 16;
             }
         }
-        i += p.per - (n0 + i) % p.per;
+        const unsigned m = __ballot_sync(0xffffffffu, fresh);
+        if (fresh) {
+            const int no = n + __popc(m & ((1u << lane) - 1u));
+            sh->hash_no[slot] = no;
+            sh->span[no] = (c + lane) | (c + 31 - __clz(same)) << 16;
+            sh->list[buf][no].x = id;  // spread out to its pieces below
+        }
+        n += __popc(m);
+        __syncwarp();
+    }
+    any_bad = __any_sync(0xffffffffu, any_bad);
+    // the windows, from the last 32 adapters to the first, so that no piece is
+    // written over an adapter that is still to be read
+    const int most = (p.BN / 2) & ~(G - 1);
+    int total = 0;
+    for (int e = lane; e < n; e += 32) {
+        const int w0 = (sh->span[e] & 0xffff) & ~(G - 1), w1 = ((sh->span[e] >> 16) + G) & ~(G - 1);
+        total += (w1 - w0 + most - 1) / most;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    int end = total;
+    for (int e0 = (n - 1) & ~31; e0 >= 0 && n > 0; e0 -= 32) {
+        const int e = e0 + lane;
+        int id = 0, w0 = 0, w1 = 0, pieces = 0;
+        if (e < n) {
+            id = sh->list[buf][e].x;
+            w0 = (sh->span[e] & 0xffff) & ~(G - 1);
+            w1 = ((sh->span[e] >> 16) + G) & ~(G - 1);
+            pieces = (w1 - w0 + most - 1) / most;
+        }
+        int after = pieces;  // pieces of this lane's adapter and the later ones
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_down_sync(0xffffffffu, after, o);
+            if (lane + o < 32) after += v;
+        }
+        __syncwarp();
+        for (int k = 0; k < pieces; ++k, w0 += most)
+            sh->list[buf][end - after + k] = make_int2(id, w0 | min(w1 - w0, most) << 16);
+        end -= __shfl_sync(0xffffffffu, after, 0);
+        __syncwarp();
     }
     if (lane == 0) {
-        sh->n_list[buf] = n;
+        sh->n_list[buf] = total;
         sh->nonfinite[buf] = 0;
+        sh->bad_id[buf] = any_bad;
     }
     __syncwarp();
 }
@@ -279,12 +330,13 @@ __device__ __noinline__ float lp_nonfinite_terms(const LpParams &p, int id, int 
     return v;
 }
 
-// 32 columns of a tile that met non-finite elements of some B_a.
-__device__ __noinline__ void lp_store_patched(const LpParams &p, const int *ids, const uint32_t *r,
-                                              int rows_left, int row0, int o) {
+// 32 columns of a tile whose rows are not 4-byte aligned, or that has bad ids
+// or met non-finite elements of some B_a (patch).
+__device__ __noinline__ void lp_store_checked(const LpParams &p, const int *ids, const uint32_t *r,
+                                              bool patch, int rows_left, int row0, int o) {
     for (int j = 0; j < 32 && j < rows_left; ++j) {
         float v = ids[j] == -2 ? 0.f : __uint_as_float(r[j]);
-        if (ids[j] >= 0) v += lp_nonfinite_terms(p, ids[j], row0 + j, o);
+        if (patch && ids[j] >= 0) v += lp_nonfinite_terms(p, ids[j], row0 + j, o);
         p.y[(long long)(row0 + j) * p.y_stride + o] = __float2bfloat16(v);
     }
 }
@@ -342,7 +394,7 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->bfull[s], 1);
-            mbar_init(&sh->ext[s], 4 * CG);
+            mbar_init(&sh->ext[s], CG);
             mbar_init(&sh->empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -374,7 +426,6 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
     // besides t was complete by then.
     pdl_launch_dependents();
     const uint32_t tmem = sh->tmem;
-    int issued = 0;  // producer: stages loaded
     // A stage's full barrier counts its W and x blocks, its bfull barrier its
     // B_a blocks; who waits for one keeps the parity of its next phase, one
     // bit per stage.
@@ -383,20 +434,17 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        bool ok = true;
-        int i = 0;
-        const int rot = (int)((long long)first_tile * nkb / tile_step) % nkb;
-        for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
-            const int m0 = (tile / p.n_tiles * CG + half) * BM;
-            const int n0 = tile % p.n_tiles * p.BN + half * (p.BN / 2);
-            for (int kb = 0; kb < nkb; ++kb, ++issued) {
-                const int s = issued % S, use = issued / S;
-                // tiles that start together start at different columns
-                const int kc = (kb0 + (kb + rot < nkb ? kb + rot : kb + rot - nkb)) * BK;
-                if (use > 0 && !(ok = lp_wait(&sh->empty[s], (uint32_t)((use - 1) & 1),
-                                              abort_flag, p.wait_ns)))
-                    break;
-                if (lane == 0) {
+        if (lp_elect()) {
+            bool ok = true;
+            int i = 0, s = 0;
+            uint32_t turn = 1;  // parity of the phase that frees stage s
+            const int rot = (int)((long long)first_tile * nkb / tile_step) % nkb;
+            for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
+                const int m0 = (tile / p.n_tiles * CG + half) * BM;
+                const int n0 = tile % p.n_tiles * p.BN + half * (p.BN / 2);
+                int kc = (kb0 + rot) * BK;  // tiles that start together start at different columns
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!(ok = mbar_wait_for(&sh->empty[s], turn, abort_flag, p.wait_ns))) break;
                     if (half == 0)
                         mbar_arrive_expect_tx(&sh->full[s], (uint32_t)(CG * (A_BYTES + b_bytes)));
                     if constexpr (CG == 1) {
@@ -407,117 +455,123 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                         tma_load_2d_pair(sA + s * A_BYTES, &tmw, kc, m0, bar);
                         tma_load_2d_pair(sB + s * b_bytes, &tmx, kc, n0, bar);
                     }
-                }
-                par_main ^= 1u << s;
-                any_main |= 1u << s;
-                __syncwarp();
-            }
-            if (!ok) break;
-            const int buf = i & 1;
-            if (!(ok = lp_wait(&sh->list_full[buf], (uint32_t)(i >> 1 & 1), abort_flag,
-                               p.wait_ns)))
-                break;
-            const int n_list = sh->n_list[buf];
-            const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
-            for (int x = rank; x < blocks; x += p.CK, ++issued) {
-                const int e0 = x / p.kchunks * p.pack, kc = x % p.kchunks;
-                const int ne = min(p.pack, n_list - e0);
-                const int s = issued % S, use = issued / S;
-                if (use > 0 && !(ok = lp_wait(&sh->empty[s], (uint32_t)((use - 1) & 1),
-                                              abort_flag, p.wait_ns)))
-                    break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh->bfull[s], (uint32_t)(ne * tile_bytes));
-                    for (int e = 0; e < ne; ++e)
-                        tma_load_3d(sA + s * A_BYTES + e * tile_bytes, &tmb, kc * BK, m0,
-                                    sh->list[buf][e0 + e].x, &sh->bfull[s]);
-                }
-                par_ext ^= 1u << s;
-                any_ext |= 1u << s;
-                __syncwarp();
-            }
-            if (lane == 0) mbar_arrive(&sh->list_empty[buf]);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        bool ok = true;
-        int it = 0, i = 0;
-        const uint32_t idesc = idesc_bf16_f32(BM * CG, p.BN, false, false);
-        for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
-            const int buf = i & 1, ause = i >> 1;
-            if (half == 0) {
-                if (ause > 0 &&
-                    !(ok = lp_wait_cluster(&sh->acc_empty[buf], (uint32_t)((ause - 1) & 1),
-                                           abort_flag, p.wait_ns)))
-                    break;
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(buf * p.BN);
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = it % S;
-                    if (!(ok = lp_wait(&sh->full[s], par_main >> s & 1u, abort_flag, p.wait_ns)))
-                        break;
                     par_main ^= 1u << s;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t a = smem_u32(sA + s * A_BYTES);
-                        const uint32_t b = smem_u32(sB + s * b_bytes);
-#pragma unroll
-                        for (int k = 0; k < BK / 16; ++k)
-                            lp_mma<CG>(d, smem_desc_sw128(a + k * 32, 16, 1024),
-                                       smem_desc_sw128(b + k * 32, 16, 1024), idesc,
-                                       (kb > 0 || k > 0) ? 1u : 0u);
-                        lp_commit<CG>(&sh->empty[s], pair_mask);
+                    any_main |= 1u << s;
+                    kc = kc + BK == (kb0 + nkb) * BK ? kb0 * BK : kc + BK;
+                    if (++s == S) {
+                        s = 0;
+                        turn ^= 1u;
                     }
-                    __syncwarp();
                 }
                 if (!ok) break;
-            }
-            if (!(ok = lp_wait(&sh->list_full[buf], (uint32_t)(ause & 1), abort_flag, p.wait_ns)))
-                break;
-            if (half == 0) {
-                const uint32_t d = tmem + (uint32_t)(buf * p.BN);
+                const int buf = i & 1;
+                if (!(ok = mbar_wait_for(&sh->list_full[buf], (uint32_t)(i >> 1 & 1), abort_flag,
+                                         p.wait_ns)))
+                    break;
                 const int n_list = sh->n_list[buf];
                 const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
-                const uint32_t slot_bytes = (uint32_t)(b_bytes / 2 / p.pack);
-                for (int x = rank; x < blocks; x += p.CK, ++it) {
-                    const int e0 = x / p.kchunks * p.pack, kc = x % p.kchunks;
+                for (int x = rank; x < blocks; x += p.CK) {
+                    const int e0 = x / p.kchunks * p.pack, kx = x % p.kchunks;
                     const int ne = min(p.pack, n_list - e0);
-                    const int s = it % S;
-                    if (!(ok = lp_wait_cluster(&sh->ext[s], par_ext >> s & 1u, abort_flag,
-                                               p.wait_ns)))
-                        break;
+                    if (!(ok = mbar_wait_for(&sh->empty[s], turn, abort_flag, p.wait_ns))) break;
+                    mbar_arrive_expect_tx(&sh->bfull[s], (uint32_t)(ne * tile_bytes));
+                    for (int e = 0; e < ne; ++e)
+                        tma_load_3d(sA + s * A_BYTES + e * tile_bytes, &tmb, kx * BK, m0,
+                                    sh->list[buf][e0 + e].x, &sh->bfull[s]);
                     par_ext ^= 1u << s;
+                    any_ext |= 1u << s;
+                    if (++s == S) {
+                        s = 0;
+                        turn ^= 1u;
+                    }
+                }
+                mbar_arrive(&sh->list_empty[buf]);
+            }
+            sh->par_main = par_main;
+            sh->par_ext = par_ext;
+            sh->any_main = any_main;
+            sh->any_ext = any_ext;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lp_elect()) {
+            bool ok = true;
+            int i = 0, s = 0, it = 0;
+            const uint32_t idesc = idesc_bf16_f32(BM * CG, p.BN, false, false);
+            const uint64_t desc_a = smem_desc_sw128(smem_u32(sA), 16, 1024);
+            const uint64_t desc_b = smem_desc_sw128(smem_u32(sB), 16, 1024);
+            for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
+                const int buf = i & 1, ause = i >> 1;
+                const uint32_t d = tmem + (uint32_t)(buf * p.BN);
+                if (half == 0) {
+                    if (ause > 0 &&
+                        !(ok = lp_wait_cluster(&sh->acc_empty[buf], (uint32_t)((ause - 1) & 1),
+                                               abort_flag, p.wait_ns)))
+                        break;
                     tc_fence_after();
-                    if (lane == 0) {
+                    for (int kb = 0; kb < nkb; ++kb, ++it) {
+                        if (!(ok = mbar_wait_for(&sh->full[s], par_main >> s & 1u, abort_flag,
+                                                 p.wait_ns)))
+                            break;
+                        par_main ^= 1u << s;
+                        tc_fence_after();
+                        const uint64_t a = desc_a + (uint32_t)(s * (A_BYTES >> 4));
+                        const uint64_t b = desc_b + (uint32_t)(s * (b_bytes >> 4));
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k)
+                            lp_mma<CG>(d, a + 2 * k, b + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                        lp_commit<CG>(&sh->empty[s], pair_mask);
+                        if (++s == S) s = 0;
+                    }
+                    if (!ok) break;
+                }
+                if (!(ok = mbar_wait_for(&sh->list_full[buf], (uint32_t)(ause & 1), abort_flag,
+                                         p.wait_ns)))
+                    break;
+                if (half == 0) {
+                    const int n_list = sh->n_list[buf];
+                    const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
+                    const uint32_t slot_bytes = (uint32_t)(b_bytes / 2 / p.pack);
+                    for (int x = rank; x < blocks; x += p.CK, ++it) {
+                        const int e0 = x / p.kchunks * p.pack, kc = x % p.kchunks;
+                        const int ne = min(p.pack, n_list - e0);
+                        if (!(ok = lp_wait_cluster(&sh->ext[s], par_ext >> s & 1u, abort_flag,
+                                                   p.wait_ns)))
+                            break;
+                        par_ext ^= 1u << s;
+                        tc_fence_after();
                         const int ksteps = (min(p.rank - kc * BK, BK) + 15) / 16;
                         for (int e = 0; e < ne; ++e) {
                             const int w = sh->list[buf][e0 + e].y;
                             const uint32_t dw = d + (uint32_t)(w & 0xffff);
                             const uint32_t idw = idesc_bf16_f32(BM * CG, w >> 16, false, false);
-                            const uint32_t a = smem_u32(sA + s * A_BYTES + e * tile_bytes);
-                            const uint32_t hi = smem_u32(sB + s * b_bytes) + e * slot_bytes;
-                            const uint32_t lo = hi + (uint32_t)b_bytes / 2;
+                            const uint64_t da =
+                                lp_desc(smem_u32(sA + s * A_BYTES + e * tile_bytes), row_bytes);
+                            const uint64_t hi =
+                                lp_desc(smem_u32(sB + s * b_bytes) + e * slot_bytes, row_bytes);
+                            const uint64_t lo = hi + (uint32_t)(b_bytes / 2 >> 4);
                             for (int k = 0; k < ksteps; ++k) {
-                                const uint64_t da = lp_desc(a + k * 32, row_bytes);
-                                lp_mma<CG>(dw, da, lp_desc(hi + k * 32, row_bytes), idw, 1u);
-                                lp_mma<CG>(dw, da, lp_desc(lo + k * 32, row_bytes), idw, 1u);
+                                lp_mma<CG>(dw, da + 2 * k, hi + 2 * k, idw, 1u);
+                                lp_mma<CG>(dw, da + 2 * k, lo + 2 * k, idw, 1u);
                             }
                         }
                         lp_commit<CG>(&sh->empty[s], pair_mask);
+                        if (++s == S) s = 0;
                     }
-                    __syncwarp();
+                    if (!ok) break;
+                    lp_commit<CG>(&sh->acc_full[buf], pair_mask);
                 }
-                if (!ok) break;
-                if (lane == 0) lp_commit<CG>(&sh->acc_full[buf], pair_mask);
+                mbar_arrive(&sh->list_empty[buf]);
             }
-            if (lane == 0) mbar_arrive(&sh->list_empty[buf]);
-            __syncwarp();
+            sh->committed = it;
         }
-        if (lane == 0) sh->committed = it;
+        __syncwarp();
     } else if (warp < 6) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        const bool pairs = (p.y_stride & 1) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 3) == 0;
         bool ok = true;
         int i = 0;
         for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
@@ -530,7 +584,6 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                 break;
             tc_fence_after();
             const int o = m0 + q * 32 + lane;
-            const bool o_ok = o < p.O;
             const bool patch = sh->nonfinite[buf] != 0;
             if (p.CK > 1) {
                 // partial sums into the (now idle) stage ring, [column][128] fp32
@@ -543,27 +596,39 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                     for (int j = 0; j < 32; ++j) part[(c + j) * BM] = __uint_as_float(r[j]);
                 }
             } else {
-                __nv_bfloat16 *col = p.y + o;
+                const bool plain = !patch && !sh->bad_id[buf];
                 for (int c = 0; c < p.BN; c += 32) {
                     uint32_t r[32];
                     tmem_ld32(tmem + lane_base + (uint32_t)(buf * p.BN + c), r);
                     tmem_wait_ld();
                     const int rows_left = p.R - (n0 + c);
-                    if (!o_ok) continue;
-                    if (patch) {
+                    if (!plain || !pairs) {
                         uint32_t v[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = r[j];
-                        lp_store_patched(p, sh->ids[buf] + c, v, rows_left, n0 + c, o);
+                        if (o < p.O)
+                            lp_store_checked(p, sh->ids[buf] + c, v, patch, rows_left, n0 + c, o);
                         continue;
                     }
+                    // two lanes swap a value each, so that a lane stores two
+                    // neighbours of one row: even lanes of row j, odd of j + 1
+                    const int odd = lane & 1;
+                    __nv_bfloat16 *dst =
+                        p.y + (long long)(n0 + c + odd) * p.y_stride + (o - odd);
+                    const bool both = o - odd + 1 < p.O, one = o - odd < p.O;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < rows_left) {
-                            const float v =
-                                sh->ids[buf][c + j] == -2 ? 0.f : __uint_as_float(r[j]);
-                            col[(long long)(n0 + c + j) * p.y_stride] = __float2bfloat16(v);
+                    for (int j = 0; j < 32; j += 2) {
+                        const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]);
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                        const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                        if (j + odd < rows_left) {
+                            if (both)
+                                *reinterpret_cast<uint32_t *>(dst) = w;
+                            else if (one)
+                                *reinterpret_cast<uint16_t *>(dst) = (uint16_t)w;
                         }
+                        dst += 2 * p.y_stride;
+                    }
                 }
             }
             tc_fence_before();
@@ -578,11 +643,11 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
         }
     } else {
         // ------------------------------------------------------------ adapters
-        const int at = tid - (THREADS - ADAPTER_THREADS);
-        // a block's adapters are shared out among 4 / pack warps each
-        const int group = ADAPTER_THREADS / p.pack, e = at / group, ti = at % group;
+        // a stage's adapter blocks are always the same warp's, so that it sees
+        // every phase of the stage's barrier
+        const int w = warp - 6;
         bool ok = true;
-        int it = 0, i = 0;
+        int s = 0, i = 0;
         bool waited = false;
         for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
             const int n0 = tile % p.n_tiles * p.BN;
@@ -601,73 +666,78 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                 pdl_wait();  // t is complete
                 waited = true;
             }
-            it += nkb;
+            s = (s + nkb) % S;
             const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
-            for (int x = rank; x < blocks; x += p.CK, ++it) {
+            for (int x = rank; x < blocks; x += p.CK, s = s + 1 == S ? 0 : s + 1) {
+                if ((s & 3) != w) continue;
                 const int e0 = x / p.kchunks * p.pack, kc = x % p.kchunks;
-                const bool mine = e0 + e < n_list;
-                const int2 entry = sh->list[buf][mine ? e0 + e : e0];
-                // this CTA's rows of the window: all, or its half of them
-                const int rows = (entry.y >> 16) / CG;
-                const int w0 = (entry.y & 0xffff) + half * rows;
+                const int ne = min(p.pack, n_list - e0);
                 const int rc = min(p.rank - kc * BK, BK);  // columns, a multiple of 8
                 const int nch = (rc + 15) / 16 * 2;        // 16-byte chunks of a row of t
-                const int units = mine ? rows * nch : 0;
-                auto load_t = [&](int u, float *f) {
-                    const int row = u / nch, c = u % nch;
+                bool bad = false, landed = false;
+                for (int e = 0; e < ne; ++e) {
+                    const int2 entry = sh->list[buf][e0 + e];
+                    // this CTA's rows of the window: all, or its half of them
+                    const int rows = (entry.y >> 16) / CG;
+                    const int w0 = (entry.y & 0xffff) + half * rows;
+                    // t of the window: hi in the first half of the stage's x
+                    // area, lo in the second; lanes take chunks of rows
+                    uint8_t *hi = sB + s * b_bytes + e * (b_bytes / 2 / p.pack);
+                    uint8_t *lo = hi + b_bytes / 2;
+                    for (int u0 = 0; u0 < rows * nch; u0 += 4 * 32) {
+                        float f[4][8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = 0.f;
-                    if (u < units && c * 8 < rc && sh->ids[buf][w0 + row] == entry.x) {
-                        const float4 *src = reinterpret_cast<const float4 *>(
-                            p.t + (size_t)(n0 + w0 + row) * p.rank + kc * BK + c * 8);
-                        *reinterpret_cast<float4 *>(f) = __ldcg(src);
-                        *reinterpret_cast<float4 *>(f + 4) = __ldcg(src + 1);
+                        for (int v = 0; v < 4; ++v) {
+                            const int u = u0 + v * 32 + lane;
+                            const int row = u / nch, c = u % nch;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) f[v][k] = 0.f;
+                            if (row < rows && c * 8 < rc && sh->ids[buf][w0 + row] == entry.x) {
+                                const float4 *src = reinterpret_cast<const float4 *>(
+                                    p.t + (size_t)(n0 + w0 + row) * p.rank + kc * BK + c * 8);
+                                *reinterpret_cast<float4 *>(f[v]) = __ldcg(src);
+                                *reinterpret_cast<float4 *>(f[v] + 4) = __ldcg(src + 1);
+                            }
+                        }
+                        if (!landed) {  // the stage is this block's: its loads are in
+                            if (!(ok = lp_wait(&sh->bfull[s], par_ext >> s & 1u, abort_flag,
+                                               p.wait_ns)))
+                                break;
+                            par_ext ^= 1u << s;
+                            landed = true;
+                        }
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const int u = u0 + v * 32 + lane;
+                            const int row = u / nch, c = u % nch;
+                            if (row >= rows) break;
+                            uint32_t h[4], l[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                h[k] = pack_bf16x2(f[v][2 * k], f[v][2 * k + 1]);
+                                const float h0 = __uint_as_float(h[k] << 16);
+                                const float h1 = __uint_as_float(h[k] & 0xffff0000u);
+                                // an infinite hi has no remainder
+                                l[k] = pack_bf16x2(isfinite(h0) ? f[v][2 * k] - h0 : 0.f,
+                                                   isfinite(h1) ? f[v][2 * k + 1] - h1 : 0.f);
+                            }
+                            const int off = lp_swizzled(row, c, row_bytes);
+                            *reinterpret_cast<uint4 *>(hi + off) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4 *>(lo + off) =
+                                make_uint4(l[0], l[1], l[2], l[3]);
+                        }
                     }
-                };
-                float f[2][8];
-                load_t(ti, f[0]);
-                load_t(ti + group, f[1]);
-                const int s = it % S;
-                if (!(ok = lp_wait(&sh->bfull[s], par_ext >> s & 1u, abort_flag, p.wait_ns)))
-                    break;
-                par_ext ^= 1u << s;
-                if (mine) {
+                    if (!ok) break;
                     uint8_t *tile_b = sA + s * A_BYTES + e * tile_bytes;
-                    bool bad = false;
-                    for (int row = ti; row < BM; row += group)
+#pragma unroll
+                    for (int u = 0; u < BM / 32; ++u)
                         for (int c = 0; c < rc / 8; ++c)
                             bad |= lp_clean(reinterpret_cast<uint4 *>(
-                                tile_b + lp_swizzled(row, c, row_bytes)));
-                    if (bad) sh->nonfinite[buf] = 1;
+                                tile_b + lp_swizzled(u * 32 + lane, c, row_bytes)));
                 }
-                // t of the window: hi in the first half of the stage's x area,
-                // lo in the second
-                uint8_t *hi = sB + s * b_bytes + e * (b_bytes / 2 / p.pack);
-                uint8_t *lo = hi + b_bytes / 2;
-                for (int u = ti; u < units; u += 2 * group) {
-                    if (u != ti) {
-                        load_t(u, f[0]);
-                        load_t(u + group, f[1]);
-                    }
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        if (u + v * group >= units) break;
-                        uint32_t h[4], l[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            h[k] = pack_bf16x2(f[v][2 * k], f[v][2 * k + 1]);
-                            const float h0 = __uint_as_float(h[k] << 16);
-                            const float h1 = __uint_as_float(h[k] & 0xffff0000u);
-                            // an infinite hi has no remainder
-                            l[k] = pack_bf16x2(isfinite(h0) ? f[v][2 * k] - h0 : 0.f,
-                                               isfinite(h1) ? f[v][2 * k + 1] - h1 : 0.f);
-                        }
-                        const int off = lp_swizzled((u + v * group) / nch, (u + v * group) % nch,
-                                                    row_bytes);
-                        *reinterpret_cast<uint4 *>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4 *>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
-                    }
-                }
+                if (!ok) break;
+                if (bad) sh->nonfinite[buf] = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -701,31 +771,54 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
         int patch = 0;
         for (int k = 0; k < p.CK; ++k)
             patch |= ld_dsmem_s32(cluster_map(&sh->nonfinite[0], (uint32_t)(k * CG + half)));
-        const bool pair = (p.y_stride & 1) == 0 &&
-                          (reinterpret_cast<uintptr_t>(p.y) & 3) == 0;
-        const float *part = reinterpret_cast<const float *>(smem);
-        for (int u = tid; u < (c1 - c0) * (BM / 2); u += THREADS) {
-            const int c = c0 + u / (BM / 2), o2 = u % (BM / 2) * 2;
-            const int row = n0 + c, o = m0 + o2;
-            if (row >= p.R || o >= p.O) continue;
-            float a = 0.f, b = 0.f;
+        const bool quads = (p.y_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 7) == 0;
+        const float *part = reinterpret_cast<const float *>(smem) + lane * 4;
+        const int o = m0 + lane * 4;
+        // a lane takes 4 neighbouring columns of y, a warp a row; 4 rows at a
+        // time, so that their loads from the other CTAs are in flight together
+        for (int r0 = c0 + warp; r0 < c1; r0 += 4 * (THREADS / 32)) {
+            float v[4][4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
             for (int k = 0; k < p.CK; ++k) {
-                const uint32_t src = cluster_map(part + c * BM + o2, (uint32_t)(k * CG + half));
-                a += ld_dsmem_f32(src);
-                b += ld_dsmem_f32(src + 4);
+                const uint32_t src = cluster_map(part, (uint32_t)(k * CG + half));
+                float4 t[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int c = r0 + u * (THREADS / 32);
+                    t[u] = ld_dsmem_v4(src + (uint32_t)(min(c, c1 - 1) * BM * 4));
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    v[u][0] += t[u].x;
+                    v[u][1] += t[u].y;
+                    v[u][2] += t[u].z;
+                    v[u][3] += t[u].w;
+                }
             }
-            const int id = sh->ids[0][c];
-            if (id == -2) a = b = 0.f;
-            if (patch && id >= 0) {
-                a += lp_nonfinite_terms(p, id, row, o);
-                if (o + 1 < p.O) b += lp_nonfinite_terms(p, id, row, o + 1);
-            }
-            __nv_bfloat16 *dst = p.y + (long long)row * p.y_stride + o;
-            if (pair && o + 1 < p.O) {
-                *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(a, b);
-            } else {
-                dst[0] = __float2bfloat16(a);
-                if (o + 1 < p.O) dst[1] = __float2bfloat16(b);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int c = r0 + u * (THREADS / 32), row = n0 + c;
+                if (c >= c1 || row >= p.R || o >= p.O) continue;
+                const int id = sh->ids[0][c];
+                if (id == -2) v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
+                if (patch && id >= 0)
+                    for (int k = 0; k < 4 && o + k < p.O; ++k) {
+                        const float extra = lp_nonfinite_terms(p, id, row, o + k);
+                        if (k == 0) v[u][0] += extra;
+                        if (k == 1) v[u][1] += extra;
+                        if (k == 2) v[u][2] += extra;
+                        if (k == 3) v[u][3] += extra;
+                    }
+                __nv_bfloat16 *dst = p.y + (long long)row * p.y_stride + o;
+                if (quads && o + 3 < p.O) {
+                    *reinterpret_cast<uint2 *>(dst) =
+                        make_uint2(pack_bf16x2(v[u][0], v[u][1]), pack_bf16x2(v[u][2], v[u][3]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (o + k < p.O) dst[k] = __float2bfloat16(v[u][k]);
+                }
             }
         }
     }
@@ -738,10 +831,10 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
     if (*abort_flag && warp == 0 && lane == 0) {
         volatile int never = 0;
         for (int s = 0; s < S; ++s) {
-            if (half == 0 && (any_main >> s & 1u))
-                mbar_wait_for(&sh->full[s], (par_main >> s & 1u) ^ 1u, &never, 20000000ull);
-            if (any_ext >> s & 1u)
-                mbar_wait_for(&sh->bfull[s], (par_ext >> s & 1u) ^ 1u, &never, 20000000ull);
+            if (half == 0 && (sh->any_main >> s & 1u))
+                mbar_wait_for(&sh->full[s], (sh->par_main >> s & 1u) ^ 1u, &never, 20000000ull);
+            if (sh->any_ext >> s & 1u)
+                mbar_wait_for(&sh->bfull[s], (sh->par_ext >> s & 1u) ^ 1u, &never, 20000000ull);
             if (s < sh->committed)
                 mbar_wait_for(&sh->empty[s], (uint32_t)((sh->committed - 1 - s) / S & 1), &never,
                               20000000ull);
@@ -811,6 +904,77 @@ static void lp_stages(LpParams *p, int cg, int budget) {
     if (p->stages > lp::MAX_STAGES) p->stages = lp::MAX_STAGES;
 }
 
+// How a call is cut into tiles.
+struct LpPlan {
+    int cg, BN, n_tiles, tiles, stages, CK;
+    int resident;  // clusters that fit at once
+};
+
+// Rows of x per tile and CTAs (pairs) per tile: the least of a model of the
+// call in ns. A block of K takes a CTA the longest of its products (1900 MHz),
+// its share of what the L2 hands to the SMs (9.5 TB/s measured) and of HBM
+// (6 TB/s), and the latency of a load (1.7 us) over the stages of its ring; a
+// tile begins and ends with about 4 us, and the sum over a cluster takes about
+// 2.5 us.
+static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
+    const int cg = c.R > 64 && c.O > lp::BM ? 2 : 1;
+    const int m_tiles = (c.O + cg * lp::BM - 1) / (cg * lp::BM);
+    auto kern = cg == 2 ? lora_proj_kernel<2> : lora_proj_kernel<1>;
+    const int n_min = (c.R + lp::MAX_BN - 1) / lp::MAX_BN;
+    double least = 0;
+    for (int n = n_min; n <= n_min + 3; ++n) {
+        c.BN = ((c.R + n - 1) / n + 31) / 32 * 32;
+        if (n > n_min && c.BN < 96) break;
+        c.n_tiles = (c.R + c.BN - 1) / c.BN;
+        c.tiles = m_tiles * c.n_tiles;
+        int most = groups < c.adapters ? groups : c.adapters;
+        if (most > c.BN) most = c.BN;
+        const int work = c.kblocks + (most + c.pack - 1) / c.pack * c.kchunks;
+        for (int two = cg == 1 && c.BN <= 64 ? 1 : 0; two >= 0; --two) {
+            lp_stages(&c, cg, two ? lp::SMEM_TWO : lp::SMEM_ONE);
+            const double bytes = lp::A_BYTES + c.BN / cg * 128;
+            for (c.CK = 1; c.CK * cg <= 8 && c.CK <= c.kblocks; ++c.CK) {
+                const int fit = resident_clusters(kern, lp::THREADS, lp_smem(c, cg), c.CK * cg);
+                if (fit < 1) continue;
+                const int waves = (c.tiles + fit - 1) / fit;
+                if (c.CK > 1 && waves > 1) continue;
+                const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
+                double kb = c.BN * 1.05;
+                const double l2 = bytes * ctas / 9500, hbm = lp::A_BYTES * ctas / 6000 / c.n_tiles;
+                if (l2 > kb) kb = l2;
+                if (hbm > kb) kb = hbm;
+                if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
+                const double t =
+                    waves * ((double)work / c.CK * kb + 4000) + (c.CK > 1 ? 2500 : 0);
+                if (least == 0 || t < least) {
+                    least = t;
+                    *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};
+                }
+            }
+        }
+    }
+    return least > 0;
+}
+
+// The plan of a shape on the current device, worked out once.
+static bool lp_plan(const LpParams &p, int groups, LpPlan *plan) {
+    static std::mutex mu;
+    static std::map<std::tuple<int, int, int, int, int, int, int>, LpPlan> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const auto key = std::make_tuple(dev, p.R, p.H, p.O, p.rank, p.adapters, groups);
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) {
+        *plan = it->second;
+        return true;
+    }
+    if (!lp_make_plan(p, groups, plan)) return false;
+    if (cache.size() >= 4096) cache.clear();
+    cache[key] = *plan;
+    return true;
+}
+
 int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     LpParams p;
     p.R = a.R;
@@ -822,55 +986,23 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     p.kblocks = (a.H + lp::BK - 1) / lp::BK;
     p.kchunks = (a.rank + lp::BK - 1) / lp::BK;
     p.pack = a.rank <= 16 ? 4 : a.rank <= 32 ? 2 : 1;
-    const int sms = num_sms();
-    const int cg = a.R > 64 && a.O > lp::BM ? 2 : 1;
-    const int m_tiles = (a.O + cg * lp::BM - 1) / (cg * lp::BM);
-    // rows of x per tile: the fewest waves of tiles over the SMs, each as
-    // long as its rows (and a constant share)
-    const int n_min = (a.R + lp::MAX_BN - 1) / lp::MAX_BN;
-    long long best = 0;
-    for (int n = n_min; n <= n_min + 3; ++n) {
-        const int bn = ((a.R + n - 1) / n + 31) / 32 * 32;
-        const int nt = (a.R + bn - 1) / bn;
-        const long long waves = ((long long)m_tiles * nt * cg + sms - 1) / sms;
-        const long long cost = waves * (bn + 16);
-        if (n == n_min || cost < best) {
-            best = cost;
-            p.BN = bn;
-            p.n_tiles = nt;
-        }
-        if (bn <= 128) break;
+    LpPlan plan;
+    try {
+        if (!lp_plan(p, a.R / a.rows_per_id, &plan)) return SVF_ERR_LAUNCH;
+    } catch (...) {  // no host memory: no exception leaves a C entry
+        return SVF_ERR_LAUNCH;
     }
-    p.tiles = m_tiles * p.n_tiles;
-    lp_stages(&p, cg, cg == 1 && p.BN <= 64 ? lp::SMEM_TWO : lp::SMEM_ONE);
-    const size_t smem = lp_smem(p, cg);
-    // CTAs (pairs) per tile, from the clusters that can be resident at once:
-    // the waves, each as long as a CTA's blocks of K and of adapters, about 8
-    // blocks' time from launch to the first product and to the last store, and
-    // about 4 for the sum over the cluster
+    const int cg = plan.cg;
+    p.BN = plan.BN;
+    p.n_tiles = plan.n_tiles;
+    p.tiles = plan.tiles;
+    p.stages = plan.stages;
+    p.CK = plan.CK;
     auto kern = cg == 2 ? lora_proj_kernel<2> : lora_proj_kernel<1>;
+    const size_t smem = lp_smem(p, cg);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess)
         return SVF_ERR_LAUNCH;
-    const int groups = a.R / a.rows_per_id;
-    int most = groups < a.adapters ? groups : a.adapters;
-    if (most > p.BN) most = p.BN;
-    const int work = p.kblocks + most / p.pack * p.kchunks;
-    double least = 0;
-    int resident = 1;
-    p.CK = 1;
-    for (int c = 1; c * cg <= 8 && c <= p.kblocks; ++c) {
-        int fit = resident_clusters(kern, lp::THREADS, smem, c * cg);
-        if (fit < 1) fit = c == 1 ? sms / cg : 0;
-        if (fit < 1) continue;
-        const double waves = (p.tiles + fit - 1) / fit;
-        const double t = waves * ((double)work / c + 8 + (c > 1 ? 4 : 0));
-        if (c == 1 || t < least) {
-            least = t;
-            p.CK = c;
-            resident = fit;
-        }
-    }
     uint32_t cols = 32;
     while (cols < (uint32_t)(2 * p.BN)) cols <<= 1;
     p.tmem_cols = cols;
@@ -889,7 +1021,7 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
         return SVF_ERR_LAUNCH;
     if (launch_lora_shrink(a, stream) != cudaSuccess) return SVF_ERR_LAUNCH;
     int clusters = p.tiles;
-    if (p.CK == 1 && clusters > resident) clusters = resident;  // persistent
+    if (p.CK == 1 && clusters > plan.resident) clusters = plan.resident;  // persistent
     const int cluster = cg * p.CK;
     if (launch_pdl(kern, dim3((unsigned)(clusters * cluster)), dim3(lp::THREADS), smem, stream,
                    cluster > 1 ? (unsigned)cluster : 0u, tmw, tmx, tmb, p) != cudaSuccess)
