@@ -91,7 +91,7 @@ struct LpShared {
     uint64_t empty[lp::MAX_STAGES];
     uint64_t acc_full[2], acc_empty[2], list_full[2], list_empty[2], ext_done[2];
     int ids[2][lp::MAX_BN];     // adapter of each row of the tile; -1 none, -2 a bad id
-    int2 list[2][lp::MAX_LIST]; // adapter; first row and row count of its window
+    uint32_t list[2][lp::MAX_LIST]; // an adapter's window: lp_window's fields
     int n_list[2];
     int nonfinite[2];           // some B_a tile held an infinity or NaN
     int bad_id[2];              // some row's id is bad
@@ -102,6 +102,15 @@ struct LpShared {
     uint32_t par_main, par_ext, any_main, any_ext;  // the producer's, at its end
     int abort;
 };
+
+// A list entry: the adapter (below 2^16), the first row of its window and its
+// row count, in units of 16 rows.
+__device__ __forceinline__ uint32_t lp_window(int id, int w0, int len) {
+    return (uint32_t)id | (uint32_t)(w0 >> 4) << 16 | (uint32_t)(len >> 4) << 24;
+}
+__device__ __forceinline__ int lp_adapter(uint32_t w) { return (int)(w & 0xffffu); }
+__device__ __forceinline__ int lp_first(uint32_t w) { return (int)(w >> 16 & 0xffu) << 4; }
+__device__ __forceinline__ int lp_rows(uint32_t w) { return (int)(w >> 24) << 4; }
 
 __device__ __forceinline__ bool lp_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
                                         unsigned long long ns) {
@@ -223,10 +232,6 @@ __device__ __forceinline__ int lp_swizzled(int row, int c, int row_bytes) {
     return row * row_bytes + ((c ^ ((row >> sh) & (row_bytes / 16 - 1))) << 4);
 }
 
-__device__ __forceinline__ bool bf16_nonfinite2(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
 // The distinct adapters of rows [n0, n0 + BN), in order of first appearance,
 // each with the window of the tile that holds its rows (16 CG rows aligned),
 // in pieces of at most BN / 2 rows: at most 3 pieces for an adapter of two
@@ -272,7 +277,7 @@ __device__ void lp_build_list(const LpParams &p, LpShared *sh, int buf, int n0, 
             const int no = n + __popc(m & ((1u << lane) - 1u));
             sh->hash_no[slot] = no;
             sh->span[no] = (c + lane) | (c + 31 - __clz(same)) << 16;
-            sh->list[buf][no].x = id;  // spread out to its pieces below
+            sh->list[buf][no] = (uint32_t)id;  // spread out to its pieces below
         }
         n += __popc(m);
         __syncwarp();
@@ -293,7 +298,7 @@ __device__ void lp_build_list(const LpParams &p, LpShared *sh, int buf, int n0, 
         const int e = e0 + lane;
         int id = 0, w0 = 0, w1 = 0, pieces = 0;
         if (e < n) {
-            id = sh->list[buf][e].x;
+            id = (int)sh->list[buf][e];
             w0 = (sh->span[e] & 0xffff) & ~(G - 1);
             w1 = ((sh->span[e] >> 16) + G) & ~(G - 1);
             pieces = (w1 - w0 + most - 1) / most;
@@ -306,7 +311,7 @@ __device__ void lp_build_list(const LpParams &p, LpShared *sh, int buf, int n0, 
         }
         __syncwarp();
         for (int k = 0; k < pieces; ++k, w0 += most)
-            sh->list[buf][end - after + k] = make_int2(id, w0 | min(w1 - w0, most) << 16);
+            sh->list[buf][end - after + k] = lp_window(id, w0, min(w1 - w0, most));
         end -= __shfl_sync(0xffffffffu, after, 0);
         __syncwarp();
     }
@@ -330,8 +335,8 @@ __device__ __noinline__ float lp_nonfinite_terms(const LpParams &p, int id, int 
     return v;
 }
 
-// 32 columns of a tile whose rows are not 4-byte aligned, or that has bad ids
-// or met non-finite elements of some B_a (patch).
+// 32 columns of a tile that has bad ids or met non-finite elements of some B_a
+// (patch).
 __device__ __noinline__ void lp_store_checked(const LpParams &p, const int *ids, const uint32_t *r,
                                               bool patch, int rows_left, int row0, int o) {
     for (int j = 0; j < 32 && j < rows_left; ++j) {
@@ -341,12 +346,14 @@ __device__ __noinline__ void lp_store_checked(const LpParams &p, const int *ids,
     }
 }
 
-// Replaces the non-finite elements of 8 bf16 values by zero; true if there were any.
-__device__ __forceinline__ bool lp_clean(uint4 *at) {
+// acc + 0 * v on pairs of bf16.
+__device__ __forceinline__ void add_zero_times(uint32_t &acc, uint32_t v) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v), "r"(0u));
+}
+
+// Replaces the non-finite elements of 8 bf16 values by zero.
+__device__ __forceinline__ void lp_clean(uint4 *at) {
     const uint4 b = *at;
-    if (!(bf16_nonfinite2(b.x) | bf16_nonfinite2(b.y) | bf16_nonfinite2(b.z) |
-          bf16_nonfinite2(b.w)))
-        return false;
     uint32_t wd[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -354,11 +361,100 @@ __device__ __forceinline__ bool lp_clean(uint4 *at) {
         if ((wd[k] & 0x7f800000u) == 0x7f800000u) wd[k] &= 0xffffu;
     }
     *at = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+}
+
+// One block of up to PACK adapters in a stage: B_a's tiles (brought by TMA) and
+// t's, which are written here.
+struct LpBlock {
+    LpShared *sh;
+    int buf, e0, kc;  // list, its first entry, 64-column block
+    int n0, half;     // first row of the tile; which half of a window is this CTA's
+    uint8_t *tiles_b, *area_t;
+    uint64_t *bar;
+    uint32_t parity;
+};
+
+// One warp. The lanes are shared out among the block's adapters; a lane takes
+// 4 chunks of t (8 columns of a row) at a time, the first ones before it waits
+// for the stage. False if the wait gave up.
+template <int CG, int PACK>
+__device__ __forceinline__ bool lp_adapter_block(const LpParams &p, const LpBlock &b, int lane) {
+    constexpr int ROW = 128 / PACK, NCH = ROW / 16;  // bytes and chunks of a row
+    constexpr int GL = 32 / PACK;                    // lanes of an adapter
+    const LpShared *sh = b.sh;
+    const int n_list = sh->n_list[b.buf];
+    const int ne = min(PACK, n_list - b.e0);
+    const int e = lane / GL, li = lane % GL;
+    const uint32_t w = sh->list[b.buf][min(b.e0 + e, n_list - 1)];
+    // this CTA's rows of the window: all, or its half of them
+    const int rows = lp_rows(w) / CG;
+    const int w0 = lp_first(w) + b.half * rows;
+    const int id = lp_adapter(w);
+    const int units = e < ne ? rows * NCH : 0;
+    const int rounds = ((int)__reduce_max_sync(0xffffffffu, (unsigned)units) + 4 * GL - 1) / (4 * GL);
+    const int rc = p.rank - b.kc * lp::BK;  // columns left
+    // hi in the first half of the stage's x area, lo in the second
+    const int area = p.BN / CG * 64;
+    uint8_t *hi = b.area_t + e * (area / PACK);
+    const int *ids = sh->ids[b.buf] + w0;
+    const float *src = p.t + (size_t)(b.n0 + w0) * p.rank + b.kc * lp::BK;
+    for (int g = 0; g < rounds; ++g) {
+        float f[4][8];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int u = (g * 4 + v) * GL + li;
+            const int row = u / NCH, c = u % NCH;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[v][k] = 0.f;
+            if (u < units && c * 8 < rc && ids[row] == id) {
+                const float4 *at = reinterpret_cast<const float4 *>(src + row * p.rank + c * 8);
+                *reinterpret_cast<float4 *>(f[v]) = __ldcg(at);
+                *reinterpret_cast<float4 *>(f[v] + 4) = __ldcg(at + 1);
+            }
+        }
+        // the stage is this block's once its loads are in
+        if (g == 0 && !lp_wait(b.bar, b.parity, &b.sh->abort, p.wait_ns)) return false;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int u = (g * 4 + v) * GL + li;
+            if (u >= units) break;
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h[k] = pack_bf16x2(f[v][2 * k], f[v][2 * k + 1]);
+                const float h0 = __uint_as_float(h[k] << 16);
+                const float h1 = __uint_as_float(h[k] & 0xffff0000u);
+                // an infinite hi has no remainder
+                l[k] = pack_bf16x2(isfinite(h0) ? f[v][2 * k] - h0 : 0.f,
+                                   isfinite(h1) ? f[v][2 * k + 1] - h1 : 0.f);
+            }
+            uint8_t *to = hi + lp_swizzled(u / NCH, u % NCH, ROW);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(to + area) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    }
+    // B_a: 0 times an infinity or NaN is NaN, and stays in the sum
+    uint4 *tiles = reinterpret_cast<uint4 *>(b.tiles_b);
+    uint32_t seen = 0;
+    for (int k = 0; k < ne * (lp::BM * NCH / 32); k += 8) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint4 v = tiles[(k + u) * 32 + lane];
+            add_zero_times(seen, v.x);
+            add_zero_times(seen, v.y);
+            add_zero_times(seen, v.z);
+            add_zero_times(seen, v.w);
+        }
+    }
+    if (__any_sync(0xffffffffu, (seen & 0x7fff7fffu) != 0)) {
+        for (int k = lane; k < ne * lp::BM * NCH; k += 32) lp_clean(tiles + k);
+        b.sh->nonfinite[b.buf] = 1;
+    }
     return true;
 }
 
 template <int CG>
-__global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
+__global__ void __launch_bounds__(lp::THREADS, 2)
     lora_proj_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
                      const __grid_constant__ CUtensorMap tmb, LpParams p) {
     using namespace lp;
@@ -477,7 +573,7 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                     mbar_arrive_expect_tx(&sh->bfull[s], (uint32_t)(ne * tile_bytes));
                     for (int e = 0; e < ne; ++e)
                         tma_load_3d(sA + s * A_BYTES + e * tile_bytes, &tmb, kx * BK, m0,
-                                    sh->list[buf][e0 + e].x, &sh->bfull[s]);
+                                    lp_adapter(sh->list[buf][e0 + e]), &sh->bfull[s]);
                     par_ext ^= 1u << s;
                     any_ext |= 1u << s;
                     if (++s == S) {
@@ -543,9 +639,9 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                         tc_fence_after();
                         const int ksteps = (min(p.rank - kc * BK, BK) + 15) / 16;
                         for (int e = 0; e < ne; ++e) {
-                            const int w = sh->list[buf][e0 + e].y;
-                            const uint32_t dw = d + (uint32_t)(w & 0xffff);
-                            const uint32_t idw = idesc_bf16_f32(BM * CG, w >> 16, false, false);
+                            const uint32_t w = sh->list[buf][e0 + e];
+                            const uint32_t dw = d + (uint32_t)lp_first(w);
+                            const uint32_t idw = idesc_bf16_f32(BM * CG, lp_rows(w), false, false);
                             const uint64_t da =
                                 lp_desc(smem_u32(sA + s * A_BYTES + e * tile_bytes), row_bytes);
                             const uint64_t hi =
@@ -602,7 +698,18 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                     tmem_ld32(tmem + lane_base + (uint32_t)(buf * p.BN + c), r);
                     tmem_wait_ld();
                     const int rows_left = p.R - (n0 + c);
-                    if (!plain || !pairs) {
+                    if (plain && !pairs) {
+                        __nv_bfloat16 *to = p.y + (long long)(n0 + c) * p.y_stride + o;
+                        if (o < p.O) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                if (j < rows_left) *to = __float2bfloat16(__uint_as_float(r[j]));
+                                to += p.y_stride;
+                            }
+                        }
+                        continue;
+                    }
+                    if (!plain) {
                         uint32_t v[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = r[j];
@@ -616,6 +723,17 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                     __nv_bfloat16 *dst =
                         p.y + (long long)(n0 + c + odd) * p.y_stride + (o - odd);
                     const bool both = o - odd + 1 < p.O, one = o - odd < p.O;
+                    if (rows_left >= 32 && m0 + q * 32 + 32 <= p.O) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]);
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                            *reinterpret_cast<uint32_t *>(dst) =
+                                odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                            dst += 2 * p.y_stride;
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]);
@@ -670,74 +788,15 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
             const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
             for (int x = rank; x < blocks; x += p.CK, s = s + 1 == S ? 0 : s + 1) {
                 if ((s & 3) != w) continue;
-                const int e0 = x / p.kchunks * p.pack, kc = x % p.kchunks;
-                const int ne = min(p.pack, n_list - e0);
-                const int rc = min(p.rank - kc * BK, BK);  // columns, a multiple of 8
-                const int nch = (rc + 15) / 16 * 2;        // 16-byte chunks of a row of t
-                bool bad = false, landed = false;
-                for (int e = 0; e < ne; ++e) {
-                    const int2 entry = sh->list[buf][e0 + e];
-                    // this CTA's rows of the window: all, or its half of them
-                    const int rows = (entry.y >> 16) / CG;
-                    const int w0 = (entry.y & 0xffff) + half * rows;
-                    // t of the window: hi in the first half of the stage's x
-                    // area, lo in the second; lanes take chunks of rows
-                    uint8_t *hi = sB + s * b_bytes + e * (b_bytes / 2 / p.pack);
-                    uint8_t *lo = hi + b_bytes / 2;
-                    for (int u0 = 0; u0 < rows * nch; u0 += 4 * 32) {
-                        float f[4][8];
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const int u = u0 + v * 32 + lane;
-                            const int row = u / nch, c = u % nch;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) f[v][k] = 0.f;
-                            if (row < rows && c * 8 < rc && sh->ids[buf][w0 + row] == entry.x) {
-                                const float4 *src = reinterpret_cast<const float4 *>(
-                                    p.t + (size_t)(n0 + w0 + row) * p.rank + kc * BK + c * 8);
-                                *reinterpret_cast<float4 *>(f[v]) = __ldcg(src);
-                                *reinterpret_cast<float4 *>(f[v] + 4) = __ldcg(src + 1);
-                            }
-                        }
-                        if (!landed) {  // the stage is this block's: its loads are in
-                            if (!(ok = lp_wait(&sh->bfull[s], par_ext >> s & 1u, abort_flag,
-                                               p.wait_ns)))
-                                break;
-                            par_ext ^= 1u << s;
-                            landed = true;
-                        }
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const int u = u0 + v * 32 + lane;
-                            const int row = u / nch, c = u % nch;
-                            if (row >= rows) break;
-                            uint32_t h[4], l[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                h[k] = pack_bf16x2(f[v][2 * k], f[v][2 * k + 1]);
-                                const float h0 = __uint_as_float(h[k] << 16);
-                                const float h1 = __uint_as_float(h[k] & 0xffff0000u);
-                                // an infinite hi has no remainder
-                                l[k] = pack_bf16x2(isfinite(h0) ? f[v][2 * k] - h0 : 0.f,
-                                                   isfinite(h1) ? f[v][2 * k + 1] - h1 : 0.f);
-                            }
-                            const int off = lp_swizzled(row, c, row_bytes);
-                            *reinterpret_cast<uint4 *>(hi + off) =
-                                make_uint4(h[0], h[1], h[2], h[3]);
-                            *reinterpret_cast<uint4 *>(lo + off) =
-                                make_uint4(l[0], l[1], l[2], l[3]);
-                        }
-                    }
-                    if (!ok) break;
-                    uint8_t *tile_b = sA + s * A_BYTES + e * tile_bytes;
-#pragma unroll
-                    for (int u = 0; u < BM / 32; ++u)
-                        for (int c = 0; c < rc / 8; ++c)
-                            bad |= lp_clean(reinterpret_cast<uint4 *>(
-                                tile_b + lp_swizzled(u * 32 + lane, c, row_bytes)));
-                }
+                const int e0 = p.kchunks == 1 ? x * p.pack : x / p.kchunks;
+                const int kc = p.kchunks == 1 ? 0 : x % p.kchunks;
+                const LpBlock b = {sh, buf, e0, kc, n0, half, sA + s * A_BYTES, sB + s * b_bytes,
+                                   &sh->bfull[s], par_ext >> s & 1u};
+                ok = p.pack == 4   ? lp_adapter_block<CG, 4>(p, b, lane)
+                     : p.pack == 2 ? lp_adapter_block<CG, 2>(p, b, lane)
+                                   : lp_adapter_block<CG, 1>(p, b, lane);
                 if (!ok) break;
-                if (bad) sh->nonfinite[buf] = 1;
+                par_ext ^= 1u << s;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -767,15 +826,18 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
         cluster_wait();
         const int m0 = (first_tile / p.n_tiles * CG + half) * BM;
         const int n0 = first_tile % p.n_tiles * p.BN;
-        const int c0 = p.BN * rank / p.CK, c1 = p.BN * (rank + 1) / p.CK;
+        const int cols = min(p.BN, p.R - n0);
+        const int c0 = cols * rank / p.CK, c1 = cols * (rank + 1) / p.CK;
         int patch = 0;
         for (int k = 0; k < p.CK; ++k)
             patch |= ld_dsmem_s32(cluster_map(&sh->nonfinite[0], (uint32_t)(k * CG + half)));
         const bool quads = (p.y_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 7) == 0;
-        const float *part = reinterpret_cast<const float *>(smem) + lane * 4;
-        const int o = m0 + lane * 4;
-        // a lane takes 4 neighbouring columns of y, a warp a row; 4 rows at a
-        // time, so that their loads from the other CTAs are in flight together
+        // a warp takes a row of y, a lane 4 neighbouring columns of it (where
+        // rows are 8-byte aligned, else every 32nd); 4 rows at a time, so that
+        // their loads from the other CTAs are in flight together
+        const int at = quads ? lane * 4 : lane, step = quads ? 1 : 32;
+        const float *part = reinterpret_cast<const float *>(smem) + at;
+        const int o = m0 + at;
         for (int r0 = c0 + warp; r0 < c1; r0 += 4 * (THREADS / 32)) {
             float v[4][4];
 #pragma unroll
@@ -786,7 +848,15 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int c = r0 + u * (THREADS / 32);
-                    t[u] = ld_dsmem_v4(src + (uint32_t)(min(c, c1 - 1) * BM * 4));
+                    const uint32_t from = src + (uint32_t)(min(c, c1 - 1) * BM * 4);
+                    if (quads) {
+                        t[u] = ld_dsmem_v4(from);
+                    } else {
+                        t[u].x = ld_dsmem_f32(from);
+                        t[u].y = ld_dsmem_f32(from + 128);
+                        t[u].z = ld_dsmem_f32(from + 256);
+                        t[u].w = ld_dsmem_f32(from + 384);
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -799,17 +869,15 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int c = r0 + u * (THREADS / 32), row = n0 + c;
-                if (c >= c1 || row >= p.R || o >= p.O) continue;
+                if (c >= c1 || o >= p.O) continue;
                 const int id = sh->ids[0][c];
                 if (id == -2) v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
-                if (patch && id >= 0)
-                    for (int k = 0; k < 4 && o + k < p.O; ++k) {
-                        const float extra = lp_nonfinite_terms(p, id, row, o + k);
-                        if (k == 0) v[u][0] += extra;
-                        if (k == 1) v[u][1] += extra;
-                        if (k == 2) v[u][2] += extra;
-                        if (k == 3) v[u][3] += extra;
-                    }
+                if (patch && id >= 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (o + k * step < p.O)
+                            v[u][k] += lp_nonfinite_terms(p, id, row, o + k * step);
+                }
                 __nv_bfloat16 *dst = p.y + (long long)row * p.y_stride + o;
                 if (quads && o + 3 < p.O) {
                     *reinterpret_cast<uint2 *>(dst) =
@@ -817,7 +885,7 @@ __global__ void __launch_bounds__(lp::THREADS, CG == 1 ? 2 : 1)
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (o + k < p.O) dst[k] = __float2bfloat16(v[u][k]);
+                        if (o + k * step < p.O) dst[k * step] = __float2bfloat16(v[u][k]);
                 }
             }
         }
@@ -1004,7 +1072,7 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
         cudaSuccess)
         return SVF_ERR_LAUNCH;
     uint32_t cols = 32;
-    while (cols < (uint32_t)(2 * p.BN)) cols <<= 1;
+    while (cols < (uint32_t)((p.CK > 1 ? 1 : 2) * p.BN)) cols <<= 1;
     p.tmem_cols = cols;
     p.wait_ns = kWaitDeadlineNs;
     p.t = static_cast<const float *>(a.workspace);

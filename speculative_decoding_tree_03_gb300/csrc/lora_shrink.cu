@@ -13,7 +13,7 @@
 // through shared memory and tensor memory for N = rank columns.
 //
 // A CTA takes a block of 16 rows and one of the distinct adapters in it; its
-// 8 warps, and the KS CTAs of its cluster, share the 64-wide blocks of K. The
+// 4 warps, and the KS CTAs of its cluster, share the 64-wide blocks of K. The
 // warps' sums meet in shared memory, the CTAs' over distributed shared memory,
 // in a fixed order. Rows of other adapters in the block are not stored, so an
 // infinity or NaN in one request's adapter or hidden state stays with it.
@@ -25,7 +25,7 @@ namespace svf {
 
 namespace {
 
-constexpr int kShrinkWarps = 8;
+constexpr int kShrinkWarps = 4;
 constexpr int kShrinkThreads = 32 * kShrinkWarps;
 constexpr int kShrinkRows = 16;
 
@@ -41,7 +41,7 @@ struct ShrinkArgs {
 };
 
 __device__ __forceinline__ void mma_bf16(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -54,7 +54,7 @@ __device__ __forceinline__ uint4 ld16(const __nv_bfloat16 *p, bool ok) {
 
 // NT: 8-row tiles of A that a CTA takes (rank in groups of 8 NT)
 template <int NT>
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(ShrinkArgs p) {
+__global__ void __launch_bounds__(kShrinkThreads, 5) lora_shrink_kernel(ShrinkArgs p) {
     __shared__ float s_acc[kShrinkWarps][kShrinkRows][NT * 8];
     __shared__ int s_ids[kShrinkRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(ShrinkArgs 
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll 2
         for (int kc = ks * kShrinkWarps + warp; kc < kchunks; kc += p.KS * kShrinkWarps) {
             const int k = kc * 64 + q * 16;
             const bool ok0 = k < p.H, ok1 = k + 8 < p.H;
@@ -182,16 +183,16 @@ cudaError_t launch_nt(ShrinkArgs p, cudaStream_t stream) {
     const int groups = (p.R + p.per - 1) / p.per;
     if (most > groups) most = groups;
     if (most > kShrinkRows) most = kShrinkRows;
-    const int sms = num_sms();
-    // one CTA per adapter of a block while that stays within a few waves;
-    // then up to 8 CTAs (a cluster) over K while the GPU is not full and each
-    // warp still has a 64-wide block of its own
+    // One CTA per adapter of a block, up to two CTAs per SM, so that the CTAs
+    // of the projection kernel find room beside them and start at once; then
+    // up to 8 CTAs (a cluster) over K while the two per SM are not used up and
+    // each warp still has a 64-wide block of its own.
+    const long long room = 2ll * num_sms();
     int slots = most;
-    while (slots > 1 && (long long)blocks * slots * p.ngroups > 8ll * sms) slots = (slots + 1) / 2;
+    while (slots > 1 && (long long)blocks * slots * p.ngroups > room) slots = (slots + 1) / 2;
     const int kchunks = (p.H + 63) / 64;
     int KS = 1;
-    while (KS < 8 && (long long)blocks * slots * p.ngroups * KS < 2ll * sms &&
-           KS * kShrinkWarps < kchunks)
+    while (KS < 8 && 2ll * KS * blocks * slots * p.ngroups <= room && KS * kShrinkWarps < kchunks)
         KS *= 2;
     p.slots = slots;
     p.KS = KS;
@@ -217,8 +218,7 @@ cudaError_t launch_lora_shrink(const LoraArgs &a, cudaStream_t stream) {
     p.per = a.rows_per_id;
     if (a.rank <= 8) return launch_nt<1>(p, stream);
     if (a.rank <= 16) return launch_nt<2>(p, stream);
-    if (a.rank <= 32) return launch_nt<4>(p, stream);
-    return launch_nt<8>(p, stream);
+    return launch_nt<4>(p, stream);
 }
 
 }  // namespace svf
