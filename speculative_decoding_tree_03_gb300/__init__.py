@@ -902,9 +902,8 @@ def lora_proj(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, lora_
         op, os_ = _p(out, "out", bf, shape, dev), O
     if status is None:
         status = torch.empty((G,), dtype=torch.int32, device=x.device)
-    need = R * rank * 4
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+        workspace = torch.empty((lora_proj_workspace_size(R, rank),), dtype=torch.uint8, device=x.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise SpecVerifyError("workspace must be a contiguous tensor on x's device")
     _call(lib.svf_lora_proj, "svf_lora_proj", dev, stream, x.data_ptr(), xs,

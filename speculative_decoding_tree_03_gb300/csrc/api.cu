@@ -309,7 +309,7 @@ int svf_rope_kv_write(const void *q, const void *k, const void *v, long long q_s
 
 size_t svf_lora_proj_workspace_size(int R, int rank) {
     if (R <= 0 || rank <= 0) return 0;
-    return (size_t)R * (size_t)rank * sizeof(float);
+    return (size_t)R * (size_t)rank * 4;  // two bf16 terms of each inner product
 }
 
 int svf_lora_proj(const void *x, long long x_stride, const void *weight, const void *lora_a,

@@ -17,7 +17,7 @@ struct LoraArgs {
     int rows_per_id, R, H, O, adapters, rank;
     void *y;             // [R, O] bf16, rows y_stride elements apart
     long long y_stride;
-    void *workspace;     // t [R, rank] fp32
+    void *workspace;     // t [2, R, rank] bf16: hi + lo
     int32_t *status;     // [R / rows_per_id]
 };
 

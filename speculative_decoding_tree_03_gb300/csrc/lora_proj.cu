@@ -2,12 +2,11 @@
 //     y[r] = W x[r] + s_a B_a (A_a x[r]),   a = ids[r / rows_per_id]
 // (a = -1: y[r] = W x[r]), bf16 operands and result, fp32 sums.
 //
-// lora_shrink.cu leaves t[r] = s_a A_a x[r] in fp32. Here the rest is ONE
-// matrix product with a longer inner axis: to the H columns of x and W come,
+// lora_shrink.cu leaves t[r] = s_a A_a x[r]. Here the rest is ONE matrix product with a longer inner axis: to the H columns of x and W come,
 // for every distinct adapter a of the row tile, rank columns that hold t on
 // the rows of a (zero on the others) and B_a. So the adapters ride in the same
 // tensor-memory accumulator as the shared product, and y is written once.
-//   - t enters as two bf16 terms, hi + lo (16 bits of significand, error
+//   - t is kept as two bf16 terms, hi + lo (16 bits of significand, error
 //     2^-16 of t): one rounding to bf16 would add an error as large as the
 //     result's own when the adapter's part dominates.
 //   - A product of a zero of t with an infinity or NaN of another request's
@@ -29,15 +28,14 @@
 // would be what bounds it; the pair brings 32 KB each. CG = 1 serves few rows
 // (bound by the bytes of W), where two CTAs per SM keep more loads in flight.
 // Roles of a CTA (320 threads):
-//   warp 0      producer: TMA of W and x blocks, then of B_a blocks;
+//   warp 0      producer: TMA of W and x blocks, then of B_a and t blocks;
 //   warp 1      MMA issuer (of the pair's first CTA);
 //   warps 2-5   epilogue (tensor memory -> y);
 //   warps 6-9   adapters: warp 6 lists the tile's distinct adapters; each of
-//               the four takes the adapter blocks of every fourth stage: waits
-//               for the B_a tiles, looks them over, and writes t's hi and lo
-//               next to them.
+//               the four takes the adapter blocks of every fourth stage: looks
+//               over their B_a and clears the rows of t that are not a's.
 // The t columns come last, so the shared product runs while lora_shrink still
-// does (the launches overlap; only warps 6-9 wait for it).
+// does (the launches overlap; only the producer waits for it, before t).
 //
 // Few rows leave too few tiles for the SMs: CK CTAs (or pairs) of a cluster
 // then share a tile, each with an equal part of K and every CK-th adapter
@@ -75,7 +73,7 @@ struct LpParams {
     int pack;       // adapters of one block: 4, 2 or 1
     uint32_t tmem_cols;
     unsigned long long wait_ns;
-    const float *t;
+    const __nv_bfloat16 *t;  // [hi and lo, R, rank]
     const int32_t *ids;
     const __nv_bfloat16 *lora_b;
     __nv_bfloat16 *y;
@@ -326,11 +324,11 @@ __device__ void lp_build_list(const LpParams &p, LpShared *sh, int buf, int n0, 
 // The terms of non-finite elements of the row's own B_a, from memory.
 __device__ __noinline__ float lp_nonfinite_terms(const LpParams &p, int id, int row, int o) {
     const __nv_bfloat16 *b = p.lora_b + ((size_t)id * p.O + o) * (size_t)p.rank;
-    const float *t = p.t + (size_t)row * p.rank;
+    const __nv_bfloat16 *hi = p.t + (size_t)row * p.rank, *lo = hi + (size_t)p.R * p.rank;
     float v = 0.f;
     for (int j = 0; j < p.rank; ++j) {
         const float f = __bfloat162float(b[j]);
-        if (!isfinite(f)) v += __ldcg(t + j) * f;
+        if (!isfinite(f)) v += (__bfloat162float(hi[j]) + __bfloat162float(lo[j])) * f;
     }
     return v;
 }
@@ -363,100 +361,54 @@ __device__ __forceinline__ void lp_clean(uint4 *at) {
     *at = make_uint4(wd[0], wd[1], wd[2], wd[3]);
 }
 
-// One block of up to PACK adapters in a stage: B_a's tiles (brought by TMA) and
-// t's, which are written here.
-struct LpBlock {
-    LpShared *sh;
-    int buf, e0, kc;  // list, its first entry, 64-column block
-    int n0, half;     // first row of the tile; which half of a window is this CTA's
-    uint8_t *tiles_b, *area_t;
-    uint64_t *bar;
-    uint32_t parity;
-};
-
-// One warp. The lanes are shared out among the block's adapters; a lane takes
-// 4 chunks of t (8 columns of a row) at a time, the first ones before it waits
-// for the stage. False if the wait gave up.
+// A landed adapter block of up to PACK adapters (list entries from e0 on), by
+// one warp: t's rows of other adapters become zero, non-finite elements of B_a
+// are looked for. True if there were any; they are zero then.
 template <int CG, int PACK>
-__device__ __forceinline__ bool lp_adapter_block(const LpParams &p, const LpBlock &b, int lane) {
+__device__ __forceinline__ bool lp_check_block(const LpShared *sh, int buf, int e0, int half,
+                                               int area, uint8_t *tiles_b, uint8_t *hi, int lane) {
     constexpr int ROW = 128 / PACK, NCH = ROW / 16;  // bytes and chunks of a row
-    constexpr int GL = 32 / PACK;                    // lanes of an adapter
-    const LpShared *sh = b.sh;
-    const int n_list = sh->n_list[b.buf];
-    const int ne = min(PACK, n_list - b.e0);
-    const int e = lane / GL, li = lane % GL;
-    const uint32_t w = sh->list[b.buf][min(b.e0 + e, n_list - 1)];
-    // this CTA's rows of the window: all, or its half of them
-    const int rows = lp_rows(w) / CG;
-    const int w0 = lp_first(w) + b.half * rows;
-    const int id = lp_adapter(w);
-    const int units = e < ne ? rows * NCH : 0;
-    const int rounds = ((int)__reduce_max_sync(0xffffffffu, (unsigned)units) + 4 * GL - 1) / (4 * GL);
-    const int rc = p.rank - b.kc * lp::BK;  // columns left
-    // hi in the first half of the stage's x area, lo in the second
-    const int area = p.BN / CG * 64;
-    uint8_t *hi = b.area_t + e * (area / PACK);
-    const int *ids = sh->ids[b.buf] + w0;
-    const float *src = p.t + (size_t)(b.n0 + w0) * p.rank + b.kc * lp::BK;
-    for (int g = 0; g < rounds; ++g) {
-        float f[4][8];
+    const int ne = min(PACK, sh->n_list[buf] - e0);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int u = (g * 4 + v) * GL + li;
-            const int row = u / NCH, c = u % NCH;
+    for (int e = 0; e < PACK; ++e) {
+        if (e >= ne) break;
+        const uint32_t w = sh->list[buf][e0 + e];
+        // this CTA's rows of the window: all, or its half of them
+        const int rows = lp_rows(w) / CG;
+        const int *ids = sh->ids[buf] + lp_first(w) + half * rows;
+        for (int row = lane; row < rows; row += 32)
+            if (ids[row] != lp_adapter(w)) {
+                uint4 *at = reinterpret_cast<uint4 *>(hi + e * (area / PACK) + row * ROW);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[v][k] = 0.f;
-            if (u < units && c * 8 < rc && ids[row] == id) {
-                const float4 *at = reinterpret_cast<const float4 *>(src + row * p.rank + c * 8);
-                *reinterpret_cast<float4 *>(f[v]) = __ldcg(at);
-                *reinterpret_cast<float4 *>(f[v] + 4) = __ldcg(at + 1);
+                for (int c = 0; c < NCH; ++c)
+                    at[c] = at[area / 16 + c] = make_uint4(0, 0, 0, 0);
             }
-        }
-        // the stage is this block's once its loads are in
-        if (g == 0 && !lp_wait(b.bar, b.parity, &b.sh->abort, p.wait_ns)) return false;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int u = (g * 4 + v) * GL + li;
-            if (u >= units) break;
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h[k] = pack_bf16x2(f[v][2 * k], f[v][2 * k + 1]);
-                const float h0 = __uint_as_float(h[k] << 16);
-                const float h1 = __uint_as_float(h[k] & 0xffff0000u);
-                // an infinite hi has no remainder
-                l[k] = pack_bf16x2(isfinite(h0) ? f[v][2 * k] - h0 : 0.f,
-                                   isfinite(h1) ? f[v][2 * k + 1] - h1 : 0.f);
-            }
-            uint8_t *to = hi + lp_swizzled(u / NCH, u % NCH, ROW);
-            *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(to + area) = make_uint4(l[0], l[1], l[2], l[3]);
-        }
     }
-    // B_a: 0 times an infinity or NaN is NaN, and stays in the sum
-    uint4 *tiles = reinterpret_cast<uint4 *>(b.tiles_b);
+    // 0 times an infinity or NaN is NaN, and stays in the sum
+    uint4 *tiles = reinterpret_cast<uint4 *>(tiles_b) + lane;
     uint32_t seen = 0;
-    for (int k = 0; k < ne * (lp::BM * NCH / 32); k += 8) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const uint4 v = tiles[(k + u) * 32 + lane];
+    for (int e = 0; e < PACK; ++e) {
+        if (e >= ne) break;
+#pragma unroll 8
+        for (int k = 0; k < lp::BM * NCH / 32; ++k) {
+            const uint4 v = tiles[e * lp::BM * NCH + k * 32];
             add_zero_times(seen, v.x);
             add_zero_times(seen, v.y);
             add_zero_times(seen, v.z);
             add_zero_times(seen, v.w);
         }
     }
-    if (__any_sync(0xffffffffu, (seen & 0x7fff7fffu) != 0)) {
-        for (int k = lane; k < ne * lp::BM * NCH; k += 32) lp_clean(tiles + k);
-        b.sh->nonfinite[b.buf] = 1;
-    }
+    if (!__any_sync(0xffffffffu, (seen & 0x7fff7fffu) != 0)) return false;
+    for (int k = 0; k < ne * lp::BM * NCH; k += 32) lp_clean(tiles + k);
     return true;
 }
 
 template <int CG>
 __global__ void __launch_bounds__(lp::THREADS, 2)
     lora_proj_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
-                     const __grid_constant__ CUtensorMap tmb, LpParams p) {
+                     const __grid_constant__ CUtensorMap tmb, const __grid_constant__ CUtensorMap tmt,
+                     LpParams p) {
     using namespace lp;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -508,6 +460,7 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
         tma_prefetch_desc(&tmw);
         tma_prefetch_desc(&tmx);
         tma_prefetch_desc(&tmb);
+        tma_prefetch_desc(&tmt);
     }
     if (warp == 1) lp_tmem_alloc<CG>(&sh->tmem, p.tmem_cols);
     tc_fence_before();
@@ -517,10 +470,10 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
         cluster_arrive();
         cluster_wait();
     }
-    // Only t waits for the kernel before this one (warps 6-9 below): that
+    // Only t waits for the kernel before this one (in the producer): that
     // kernel lets this one start after its own wait, so what this call reads
     // besides t was complete by then.
-    pdl_launch_dependents();
+    if (p.CK > 1) pdl_launch_dependents();
     const uint32_t tmem = sh->tmem;
     // A stage's full barrier counts its W and x blocks, its bfull barrier its
     // B_a blocks; who waits for one keeps the parity of its next phase, one
@@ -533,6 +486,7 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
         if (lp_elect()) {
             bool ok = true;
             int i = 0, s = 0;
+            bool waited = false;
             uint32_t turn = 1;  // parity of the phase that frees stage s
             const int rot = (int)((long long)first_tile * nkb / tile_step) % nkb;
             for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
@@ -564,16 +518,37 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                 if (!(ok = mbar_wait_for(&sh->list_full[buf], (uint32_t)(i >> 1 & 1), abort_flag,
                                          p.wait_ns)))
                     break;
+                if (!waited) {
+                    pdl_wait();  // t is complete
+                    asm volatile("fence.proxy.async.global;" ::: "memory");
+                    waited = true;
+                }
                 const int n_list = sh->n_list[buf];
                 const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
                 for (int x = rank; x < blocks; x += p.CK) {
                     const int e0 = x / p.kchunks * p.pack, kx = x % p.kchunks;
                     const int ne = min(p.pack, n_list - e0);
                     if (!(ok = mbar_wait_for(&sh->empty[s], turn, abort_flag, p.wait_ns))) break;
-                    mbar_arrive_expect_tx(&sh->bfull[s], (uint32_t)(ne * tile_bytes));
+                    int bytes = 0;
                     for (int e = 0; e < ne; ++e)
+                        bytes += tile_bytes + 2 * lp_rows(sh->list[buf][e0 + e]) / CG * row_bytes;
+                    mbar_arrive_expect_tx(&sh->bfull[s], (uint32_t)bytes);
+                    for (int e = 0; e < ne; ++e) {
+                        const uint32_t w = sh->list[buf][e0 + e];
                         tma_load_3d(sA + s * A_BYTES + e * tile_bytes, &tmb, kx * BK, m0,
-                                    lp_adapter(sh->list[buf][e0 + e]), &sh->bfull[s]);
+                                    lp_adapter(w), &sh->bfull[s]);
+                        // t of this CTA's rows of the window: hi in the first
+                        // half of the stage's x area, lo in the second
+                        const int rows = lp_rows(w) / CG;
+                        const int r0 = tile % p.n_tiles * p.BN + lp_first(w) + half * rows;
+                        uint8_t *hi = sB + s * b_bytes + e * (b_bytes / 2 / p.pack);
+                        for (int r = 0; r < rows; r += 16) {
+                            tma_load_3d(hi + r * row_bytes, &tmt, kx * BK, r0 + r, 0,
+                                        &sh->bfull[s]);
+                            tma_load_3d(hi + b_bytes / 2 + r * row_bytes, &tmt, kx * BK, r0 + r, 1,
+                                        &sh->bfull[s]);
+                        }
+                    }
                     par_ext ^= 1u << s;
                     any_ext |= 1u << s;
                     if (++s == S) {
@@ -583,6 +558,7 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                 }
                 mbar_arrive(&sh->list_empty[buf]);
             }
+            if (!waited) pdl_wait();  // this grid ends after the one before it
             sh->par_main = par_main;
             sh->par_ext = par_ext;
             sh->any_main = any_main;
@@ -766,7 +742,6 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
         const int w = warp - 6;
         bool ok = true;
         int s = 0, i = 0;
-        bool waited = false;
         for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
             const int n0 = tile % p.n_tiles * p.BN;
             const int buf = i & 1, ause = i >> 1;
@@ -779,24 +754,21 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
             }
             if (!(ok = lp_wait(&sh->list_full[buf], (uint32_t)(ause & 1), abort_flag, p.wait_ns)))
                 break;
-            const int n_list = sh->n_list[buf];
-            if (!waited) {
-                pdl_wait();  // t is complete
-                waited = true;
-            }
             s = (s + nkb) % S;
+            const int n_list = sh->n_list[buf];
             const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
             for (int x = rank; x < blocks; x += p.CK, s = s + 1 == S ? 0 : s + 1) {
                 if ((s & 3) != w) continue;
-                const int e0 = p.kchunks == 1 ? x * p.pack : x / p.kchunks;
-                const int kc = p.kchunks == 1 ? 0 : x % p.kchunks;
-                const LpBlock b = {sh, buf, e0, kc, n0, half, sA + s * A_BYTES, sB + s * b_bytes,
-                                   &sh->bfull[s], par_ext >> s & 1u};
-                ok = p.pack == 4   ? lp_adapter_block<CG, 4>(p, b, lane)
-                     : p.pack == 2 ? lp_adapter_block<CG, 2>(p, b, lane)
-                                   : lp_adapter_block<CG, 1>(p, b, lane);
-                if (!ok) break;
+                if (!(ok = lp_wait(&sh->bfull[s], par_ext >> s & 1u, abort_flag, p.wait_ns))) break;
                 par_ext ^= 1u << s;
+                const int e0 = p.kchunks == 1 ? x * p.pack : x / p.kchunks;
+                uint8_t *tb = sA + s * A_BYTES, *hi = sB + s * b_bytes;
+                const bool bad =
+                    p.pack == 4 ? lp_check_block<CG, 4>(sh, buf, e0, half, b_bytes / 2, tb, hi, lane)
+                    : p.pack == 2
+                        ? lp_check_block<CG, 2>(sh, buf, e0, half, b_bytes / 2, tb, hi, lane)
+                        : lp_check_block<CG, 1>(sh, buf, e0, half, b_bytes / 2, tb, hi, lane);
+                if (bad) sh->nonfinite[buf] = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -806,13 +778,13 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                         mbar_arrive_cluster(cluster_map(&sh->ext[s], (uint32_t)lead));
                 }
             }
+            if (!ok) break;
             if (lane == 0) {
                 mbar_arrive(&sh->ext_done[buf]);
                 mbar_arrive(&sh->list_empty[buf]);
             }
             __syncwarp();
         }
-        if (!waited) pdl_wait();
     }
 
     tc_fence_before();
@@ -1075,24 +1047,26 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     while (cols < (uint32_t)((p.CK > 1 ? 1 : 2) * p.BN)) cols <<= 1;
     p.tmem_cols = cols;
     p.wait_ns = kWaitDeadlineNs;
-    p.t = static_cast<const float *>(a.workspace);
+    p.t = static_cast<const __nv_bfloat16 *>(a.workspace);
     p.ids = a.ids;
     p.lora_b = static_cast<const __nv_bfloat16 *>(a.lora_b);
     p.y = static_cast<__nv_bfloat16 *>(a.y);
     p.y_stride = a.y_stride;
     p.status = a.status;
-    CUtensorMap tmw, tmx, tmb;
+    CUtensorMap tmw, tmx, tmb, tmt;
     if (!lp_map(&tmw, a.weight, 2, 1, a.O, a.H, a.H, 0, 64, lp::BM) ||
         !lp_map(&tmx, a.x, 2, 1, a.R, a.H, a.x_stride, 0, 64, p.BN / cg) ||
         !lp_map(&tmb, a.lora_b, 3, a.adapters, a.O, a.rank, a.rank, (long long)a.O * a.rank,
-                64 / p.pack, lp::BM))
+                64 / p.pack, lp::BM) ||
+        !lp_map(&tmt, a.workspace, 3, 2, a.R, a.rank, a.rank, (long long)a.R * a.rank, 64 / p.pack,
+                16))
         return SVF_ERR_LAUNCH;
     if (launch_lora_shrink(a, stream) != cudaSuccess) return SVF_ERR_LAUNCH;
     int clusters = p.tiles;
     if (p.CK == 1 && clusters > plan.resident) clusters = plan.resident;  // persistent
     const int cluster = cg * p.CK;
     if (launch_pdl(kern, dim3((unsigned)(clusters * cluster)), dim3(lp::THREADS), smem, stream,
-                   cluster > 1 ? (unsigned)cluster : 0u, tmw, tmx, tmb, p) != cudaSuccess)
+                   cluster > 1 ? (unsigned)cluster : 0u, tmw, tmx, tmb, tmt, p) != cudaSuccess)
         return SVF_ERR_LAUNCH;
     return SVF_OK;
 }

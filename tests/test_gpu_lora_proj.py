@@ -138,7 +138,7 @@ def test_strided_rows_and_what_lies_beside_them(sv, O, cols):
     wide[:, 8:136] = c["x"]
     c["x"] = wide[:, 8:136]
     buf = torch.full((R + 2, cols), 7.0, dtype=torch.bfloat16, device="cuda")
-    ws = torch.full((R * 8,), float("nan"), device="cuda")
+    ws = torch.full((sv.lora_proj_workspace_size(R, 8) // 4,), float("nan"), device="cuda")
     out = buf[1:R + 1, 2:2 + O]
     y, bound = reference(c)
     got, _ = sv.lora_proj(**c, out=out, workspace=ws)
