@@ -69,8 +69,8 @@ constexpr int SMEM_TWO = 88 * 1024;     // ... that shares its SM with another
 struct LpParams {
     int R, H, O, rank, adapters, per;
     int BN, CK, n_tiles, tiles, kblocks, stages;
-    int kchunks;    // 64-column blocks of one adapter (rank > 64: 2)
-    int pack;       // adapters of one block: 4, 2 or 1
+    int kchunks;    // 64-column blocks of one adapter: 1, or 2 (rank > 64)
+    int lpack;      // log2 of the adapters of one block: 2, 1 or 0 (0 when kchunks is 2)
     uint32_t tmem_cols;
     unsigned long long wait_ns;
     const __nv_bfloat16 *t;  // [hi and lo, R, rank]
@@ -376,30 +376,28 @@ __device__ __forceinline__ bool lp_check_block(const LpShared *sh, int buf, int 
         // this CTA's rows of the window: all, or its half of them
         const int rows = lp_rows(w) / CG;
         const int *ids = sh->ids[buf] + lp_first(w) + half * rows;
-        for (int row = lane; row < rows; row += 32)
-            if (ids[row] != lp_adapter(w)) {
-                uint4 *at = reinterpret_cast<uint4 *>(hi + e * (area / PACK) + row * ROW);
-#pragma unroll
-                for (int c = 0; c < NCH; ++c)
-                    at[c] = at[area / 16 + c] = make_uint4(0, 0, 0, 0);
-            }
+        uint4 *at = reinterpret_cast<uint4 *>(hi + e * (area / PACK));
+        for (int u = lane; u < rows * NCH; u += 32)
+            if (ids[u / NCH] != lp_adapter(w))
+                at[u] = at[area / 16 + u] = make_uint4(0, 0, 0, 0);
     }
     // 0 times an infinity or NaN is NaN, and stays in the sum
     uint4 *tiles = reinterpret_cast<uint4 *>(tiles_b) + lane;
-    uint32_t seen = 0;
+    uint32_t seen[4] = {0, 0, 0, 0};
+    for (int k = 0; k < ne * lp::BM * NCH; k += 8 * 32) {
+        uint4 v[8];
 #pragma unroll
-    for (int e = 0; e < PACK; ++e) {
-        if (e >= ne) break;
-#pragma unroll 8
-        for (int k = 0; k < lp::BM * NCH / 32; ++k) {
-            const uint4 v = tiles[e * lp::BM * NCH + k * 32];
-            add_zero_times(seen, v.x);
-            add_zero_times(seen, v.y);
-            add_zero_times(seen, v.z);
-            add_zero_times(seen, v.w);
+        for (int u = 0; u < 8; ++u) v[u] = tiles[k + u * 32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            add_zero_times(seen[0], v[u].x);
+            add_zero_times(seen[1], v[u].y);
+            add_zero_times(seen[2], v[u].z);
+            add_zero_times(seen[3], v[u].w);
         }
     }
-    if (!__any_sync(0xffffffffu, (seen & 0x7fff7fffu) != 0)) return false;
+    if (!__any_sync(0xffffffffu, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7fff7fffu) != 0))
+        return false;
     for (int k = 0; k < ne * lp::BM * NCH; k += 32) lp_clean(tiles + k);
     return true;
 }
@@ -436,7 +434,9 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
     const int first_tile = blockIdx.x / cluster, tile_step = gridDim.x / cluster;
     const int kb0 = (int)((long long)p.kblocks * rank / p.CK);
     const int nkb = (int)((long long)p.kblocks * (rank + 1) / p.CK) - kb0;
-    const int row_bytes = 128 / p.pack, tile_bytes = BM * row_bytes;
+    const int row_bytes = 128 >> p.lpack, tile_bytes = BM * row_bytes;
+    const int pack = 1 << p.lpack, deep = p.kchunks - 1;
+    const int area = b_bytes / 2;  // of a stage's x area: t's hi, then lo
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -524,10 +524,11 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                     waited = true;
                 }
                 const int n_list = sh->n_list[buf];
-                const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
+                const int blocks = ((n_list + pack - 1) >> p.lpack) << deep;
+                const int row0 = tile % p.n_tiles * p.BN;
                 for (int x = rank; x < blocks; x += p.CK) {
-                    const int e0 = x / p.kchunks * p.pack, kx = x % p.kchunks;
-                    const int ne = min(p.pack, n_list - e0);
+                    const int e0 = (x >> deep) << p.lpack, kx = x & deep;
+                    const int ne = min(pack, n_list - e0);
                     if (!(ok = mbar_wait_for(&sh->empty[s], turn, abort_flag, p.wait_ns))) break;
                     int bytes = 0;
                     for (int e = 0; e < ne; ++e)
@@ -540,12 +541,12 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                         // t of this CTA's rows of the window: hi in the first
                         // half of the stage's x area, lo in the second
                         const int rows = lp_rows(w) / CG;
-                        const int r0 = tile % p.n_tiles * p.BN + lp_first(w) + half * rows;
-                        uint8_t *hi = sB + s * b_bytes + e * (b_bytes / 2 / p.pack);
+                        const int r0 = row0 + lp_first(w) + half * rows;
+                        uint8_t *hi = sB + s * b_bytes + e * (area >> p.lpack);
                         for (int r = 0; r < rows; r += 16) {
                             tma_load_3d(hi + r * row_bytes, &tmt, kx * BK, r0 + r, 0,
                                         &sh->bfull[s]);
-                            tma_load_3d(hi + b_bytes / 2 + r * row_bytes, &tmt, kx * BK, r0 + r, 1,
+                            tma_load_3d(hi + area + r * row_bytes, &tmt, kx * BK, r0 + r, 1,
                                         &sh->bfull[s]);
                         }
                     }
@@ -603,26 +604,26 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                     break;
                 if (half == 0) {
                     const int n_list = sh->n_list[buf];
-                    const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
-                    const uint32_t slot_bytes = (uint32_t)(b_bytes / 2 / p.pack);
+                    const int blocks = ((n_list + pack - 1) >> p.lpack) << deep;
+                    const uint64_t ext_a = lp_desc(smem_u32(sA), row_bytes);
+                    const uint64_t ext_t = lp_desc(smem_u32(sB), row_bytes);
                     for (int x = rank; x < blocks; x += p.CK, ++it) {
-                        const int e0 = x / p.kchunks * p.pack, kc = x % p.kchunks;
-                        const int ne = min(p.pack, n_list - e0);
+                        const int e0 = (x >> deep) << p.lpack;
+                        const int ne = min(pack, n_list - e0);
                         if (!(ok = lp_wait_cluster(&sh->ext[s], par_ext >> s & 1u, abort_flag,
                                                    p.wait_ns)))
                             break;
                         par_ext ^= 1u << s;
                         tc_fence_after();
-                        const int ksteps = (min(p.rank - kc * BK, BK) + 15) / 16;
+                        const int ksteps = (min(p.rank - (x & deep) * BK, BK) + 15) >> 4;
                         for (int e = 0; e < ne; ++e) {
                             const uint32_t w = sh->list[buf][e0 + e];
                             const uint32_t dw = d + (uint32_t)lp_first(w);
                             const uint32_t idw = idesc_bf16_f32(BM * CG, lp_rows(w), false, false);
-                            const uint64_t da =
-                                lp_desc(smem_u32(sA + s * A_BYTES + e * tile_bytes), row_bytes);
+                            const uint64_t da = ext_a + (uint32_t)((s * A_BYTES + e * tile_bytes) >> 4);
                             const uint64_t hi =
-                                lp_desc(smem_u32(sB + s * b_bytes) + e * slot_bytes, row_bytes);
-                            const uint64_t lo = hi + (uint32_t)(b_bytes / 2 >> 4);
+                                ext_t + (uint32_t)((s * b_bytes + e * (area >> p.lpack)) >> 4);
+                            const uint64_t lo = hi + (uint32_t)(area >> 4);
                             for (int k = 0; k < ksteps; ++k) {
                                 lp_mma<CG>(dw, da + 2 * k, hi + 2 * k, idw, 1u);
                                 lp_mma<CG>(dw, da + 2 * k, lo + 2 * k, idw, 1u);
@@ -756,18 +757,17 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                 break;
             s = (s + nkb) % S;
             const int n_list = sh->n_list[buf];
-            const int blocks = (n_list + p.pack - 1) / p.pack * p.kchunks;
+            const int blocks = ((n_list + pack - 1) >> p.lpack) << deep;
             for (int x = rank; x < blocks; x += p.CK, s = s + 1 == S ? 0 : s + 1) {
                 if ((s & 3) != w) continue;
                 if (!(ok = lp_wait(&sh->bfull[s], par_ext >> s & 1u, abort_flag, p.wait_ns))) break;
                 par_ext ^= 1u << s;
-                const int e0 = p.kchunks == 1 ? x * p.pack : x / p.kchunks;
+                const int e0 = (x >> deep) << p.lpack;
                 uint8_t *tb = sA + s * A_BYTES, *hi = sB + s * b_bytes;
                 const bool bad =
-                    p.pack == 4 ? lp_check_block<CG, 4>(sh, buf, e0, half, b_bytes / 2, tb, hi, lane)
-                    : p.pack == 2
-                        ? lp_check_block<CG, 2>(sh, buf, e0, half, b_bytes / 2, tb, hi, lane)
-                        : lp_check_block<CG, 1>(sh, buf, e0, half, b_bytes / 2, tb, hi, lane);
+                    p.lpack == 2   ? lp_check_block<CG, 4>(sh, buf, e0, half, area, tb, hi, lane)
+                    : p.lpack == 1 ? lp_check_block<CG, 2>(sh, buf, e0, half, area, tb, hi, lane)
+                                   : lp_check_block<CG, 1>(sh, buf, e0, half, area, tb, hi, lane);
                 if (bad) sh->nonfinite[buf] = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -820,8 +820,11 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int c = r0 + u * (THREADS / 32);
-                    const uint32_t from = src + (uint32_t)(min(c, c1 - 1) * BM * 4);
-                    if (quads) {
+                    const int off = min(c, c1 - 1) * BM;
+                    const uint32_t from = src + (uint32_t)(off * 4);
+                    if (quads && k == rank) {
+                        t[u] = *reinterpret_cast<const float4 *>(part + off);
+                    } else if (quads) {
                         t[u] = ld_dsmem_v4(from);
                     } else {
                         t[u].x = ld_dsmem_f32(from);
@@ -952,43 +955,51 @@ struct LpPlan {
 
 // Rows of x per tile and CTAs (pairs) per tile: the least of a model of the
 // call in ns. A block of K takes a CTA the longest of its products (1900 MHz),
-// its share of what the L2 hands to the SMs (9.5 TB/s measured) and of HBM
-// (6 TB/s), and the latency of a load (1.7 us) over the stages of its ring; a
+// its share of what the L2 hands to the SMs (9.5 TB/s measured, 100 GB/s to
+// one) and of HBM (6 TB/s), and the latency of a load (1.7 us) over the stages of its ring; a
 // tile begins and ends with about 4 us, and the sum over a cluster takes about
 // 2.5 us.
 static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
-    const int cg = c.R > 64 && c.O > lp::BM ? 2 : 1;
-    const int m_tiles = (c.O + cg * lp::BM - 1) / (cg * lp::BM);
-    auto kern = cg == 2 ? lora_proj_kernel<2> : lora_proj_kernel<1>;
-    const int n_min = (c.R + lp::MAX_BN - 1) / lp::MAX_BN;
     double least = 0;
-    for (int n = n_min; n <= n_min + 3; ++n) {
-        c.BN = ((c.R + n - 1) / n + 31) / 32 * 32;
-        if (n > n_min && c.BN < 96) break;
-        c.n_tiles = (c.R + c.BN - 1) / c.BN;
-        c.tiles = m_tiles * c.n_tiles;
-        int most = groups < c.adapters ? groups : c.adapters;
-        if (most > c.BN) most = c.BN;
-        const int work = c.kblocks + (most + c.pack - 1) / c.pack * c.kchunks;
-        for (int two = cg == 1 && c.BN <= 64 ? 1 : 0; two >= 0; --two) {
-            lp_stages(&c, cg, two ? lp::SMEM_TWO : lp::SMEM_ONE);
-            const double bytes = lp::A_BYTES + c.BN / cg * 128;
-            for (c.CK = 1; c.CK * cg <= 8 && c.CK <= c.kblocks; ++c.CK) {
-                const int fit = resident_clusters(kern, lp::THREADS, lp_smem(c, cg), c.CK * cg);
-                if (fit < 1) continue;
-                const int waves = (c.tiles + fit - 1) / fit;
-                if (c.CK > 1 && waves > 1) continue;
-                const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
-                double kb = c.BN * 1.05;
-                const double l2 = bytes * ctas / 9500, hbm = lp::A_BYTES * ctas / 6000 / c.n_tiles;
-                if (l2 > kb) kb = l2;
-                if (hbm > kb) kb = hbm;
-                if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
-                const double t =
-                    waves * ((double)work / c.CK * kb + 4000) + (c.CK > 1 ? 2500 : 0);
-                if (least == 0 || t < least) {
-                    least = t;
-                    *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};
+    for (int cg = 1; cg <= 2; ++cg) {
+        if (cg == 2 && (c.R <= 64 || c.O <= lp::BM)) break;
+        auto kern = cg == 2 ? lora_proj_kernel<2> : lora_proj_kernel<1>;
+        // one CTA alone takes more than 64 rows of x only where W has no second
+        // tile for a pair
+        const int widest = cg == 1 && c.O > lp::BM ? 64 : lp::MAX_BN;
+        const int m_tiles = (c.O + cg * lp::BM - 1) / (cg * lp::BM);
+        const int n_min = (c.R + widest - 1) / widest;
+        for (int n = n_min; n <= n_min + (cg == 2 ? 3 : 0) && n <= 512; ++n) {
+            c.BN = ((c.R + n - 1) / n + 31) / 32 * 32;
+            if (n > n_min && c.BN < 96) break;
+            c.n_tiles = (c.R + c.BN - 1) / c.BN;
+            c.tiles = m_tiles * c.n_tiles;
+            int most = groups < c.adapters ? groups : c.adapters;
+            if (most > c.BN) most = c.BN;
+            const int work = c.kblocks + (((most - 1) >> c.lpack) + 1) * c.kchunks;
+            for (int two = cg == 1 && c.BN <= 64 ? 1 : 0; two >= 0; --two) {
+                lp_stages(&c, cg, two ? lp::SMEM_TWO : lp::SMEM_ONE);
+                const double bytes = lp::A_BYTES + c.BN / cg * 128;
+                for (c.CK = 1; c.CK * cg <= 8 && c.CK <= c.kblocks; ++c.CK) {
+                    const int fit = resident_clusters(kern, lp::THREADS, lp_smem(c, cg), c.CK * cg);
+                    if (fit < 1) continue;
+                    const int waves = (c.tiles + fit - 1) / fit;
+                    if (c.CK > 1 && waves > 1) continue;
+                    const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
+                    double kb = c.BN * 1.05;
+                    const double l2 = bytes * ctas / 9500;
+                    const double hbm = lp::A_BYTES * ctas / 6000 / c.n_tiles;
+                    const double sm = bytes * (two ? ctas / num_sms() : 1) / 100;
+                    if (l2 > kb) kb = l2;
+                    if (hbm > kb) kb = hbm;
+                    if (sm > kb) kb = sm;
+                    if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
+                    const double t =
+                        waves * ((double)work / c.CK * kb + 4000) + (c.CK > 1 ? 2500 : 0);
+                    if (least == 0 || t < least) {
+                        least = t;
+                        *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};
+                    }
                 }
             }
         }
@@ -1025,7 +1036,7 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     p.per = a.rows_per_id;
     p.kblocks = (a.H + lp::BK - 1) / lp::BK;
     p.kchunks = (a.rank + lp::BK - 1) / lp::BK;
-    p.pack = a.rank <= 16 ? 4 : a.rank <= 32 ? 2 : 1;
+    p.lpack = a.rank <= 16 ? 2 : a.rank <= 32 ? 1 : 0;
     LpPlan plan;
     try {
         if (!lp_plan(p, a.R / a.rows_per_id, &plan)) return SVF_ERR_LAUNCH;
@@ -1057,8 +1068,8 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     if (!lp_map(&tmw, a.weight, 2, 1, a.O, a.H, a.H, 0, 64, lp::BM) ||
         !lp_map(&tmx, a.x, 2, 1, a.R, a.H, a.x_stride, 0, 64, p.BN / cg) ||
         !lp_map(&tmb, a.lora_b, 3, a.adapters, a.O, a.rank, a.rank, (long long)a.O * a.rank,
-                64 / p.pack, lp::BM) ||
-        !lp_map(&tmt, a.workspace, 3, 2, a.R, a.rank, a.rank, (long long)a.R * a.rank, 64 / p.pack,
+                64 >> p.lpack, lp::BM) ||
+        !lp_map(&tmt, a.workspace, 3, 2, a.R, a.rank, a.rank, (long long)a.R * a.rank, 64 >> p.lpack,
                 16))
         return SVF_ERR_LAUNCH;
     if (launch_lora_shrink(a, stream) != cudaSuccess) return SVF_ERR_LAUNCH;
