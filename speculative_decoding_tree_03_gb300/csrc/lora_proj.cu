@@ -366,7 +366,7 @@ __device__ __forceinline__ void lp_clean(uint4 *at) {
 // are looked for. True if there were any; they are zero then.
 template <int CG, int PACK>
 __device__ __forceinline__ bool lp_check_block(const LpShared *sh, int buf, int e0, int half,
-                                               int area, uint8_t *tiles_b, uint8_t *hi, int lane) {
+                                               int slot, uint8_t *tiles_b, uint8_t *hi, int lane) {
     constexpr int ROW = 128 / PACK, NCH = ROW / 16;  // bytes and chunks of a row
     const int ne = min(PACK, sh->n_list[buf] - e0);
 #pragma unroll
@@ -376,10 +376,11 @@ __device__ __forceinline__ bool lp_check_block(const LpShared *sh, int buf, int 
         // this CTA's rows of the window: all, or its half of them
         const int rows = lp_rows(w) / CG;
         const int *ids = sh->ids[buf] + lp_first(w) + half * rows;
-        uint4 *at = reinterpret_cast<uint4 *>(hi + e * (area / PACK));
+        uint4 *at = reinterpret_cast<uint4 *>(hi + e * slot);
+        const int lo = (rows == 16 ? 16 * ROW : slot / 2) / 16;
         for (int u = lane; u < rows * NCH; u += 32)
             if (ids[u / NCH] != lp_adapter(w))
-                at[u] = at[area / 16 + u] = make_uint4(0, 0, 0, 0);
+                at[u] = at[lo + u] = make_uint4(0, 0, 0, 0);
     }
     // 0 times an infinity or NaN is NaN, and stays in the sum
     uint4 *tiles = reinterpret_cast<uint4 *>(tiles_b) + lane;
@@ -403,10 +404,10 @@ __device__ __forceinline__ bool lp_check_block(const LpShared *sh, int buf, int 
 }
 
 template <int CG>
-__global__ void __launch_bounds__(lp::THREADS, 2)
+__global__ void __maxnreg__(80)
     lora_proj_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
                      const __grid_constant__ CUtensorMap tmb, const __grid_constant__ CUtensorMap tmt,
-                     LpParams p) {
+                     const __grid_constant__ CUtensorMap tmt2, LpParams p) {
     using namespace lp;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -436,7 +437,10 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
     const int nkb = (int)((long long)p.kblocks * (rank + 1) / p.CK) - kb0;
     const int row_bytes = 128 >> p.lpack, tile_bytes = BM * row_bytes;
     const int pack = 1 << p.lpack, deep = p.kchunks - 1;
-    const int area = b_bytes / 2;  // of a stage's x area: t's hi, then lo
+    // A stage's x area is shared out among the block's adapters; each part
+    // holds the rows of t's hi, and from its middle on those of lo (16 rows:
+    // from behind the hi rows on, so that one box brings both).
+    const int slot = b_bytes >> p.lpack;
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -461,6 +465,7 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
         tma_prefetch_desc(&tmx);
         tma_prefetch_desc(&tmb);
         tma_prefetch_desc(&tmt);
+        tma_prefetch_desc(&tmt2);
     }
     if (warp == 1) lp_tmem_alloc<CG>(&sh->tmem, p.tmem_cols);
     tc_fence_before();
@@ -538,16 +543,19 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                         const uint32_t w = sh->list[buf][e0 + e];
                         tma_load_3d(sA + s * A_BYTES + e * tile_bytes, &tmb, kx * BK, m0,
                                     lp_adapter(w), &sh->bfull[s]);
-                        // t of this CTA's rows of the window: hi in the first
-                        // half of the stage's x area, lo in the second
+                        // t of this CTA's rows of the window
                         const int rows = lp_rows(w) / CG;
                         const int r0 = row0 + lp_first(w) + half * rows;
-                        uint8_t *hi = sB + s * b_bytes + e * (area >> p.lpack);
-                        for (int r = 0; r < rows; r += 16) {
-                            tma_load_3d(hi + r * row_bytes, &tmt, kx * BK, r0 + r, 0,
-                                        &sh->bfull[s]);
-                            tma_load_3d(hi + area + r * row_bytes, &tmt, kx * BK, r0 + r, 1,
-                                        &sh->bfull[s]);
+                        uint8_t *hi = sB + s * b_bytes + e * slot;
+                        if (rows == 16) {
+                            tma_load_3d(hi, &tmt2, kx * BK, r0, 0, &sh->bfull[s]);
+                        } else {
+                            for (int r = 0; r < rows; r += 16) {
+                                tma_load_3d(hi + r * row_bytes, &tmt, kx * BK, r0 + r, 0,
+                                            &sh->bfull[s]);
+                                tma_load_3d(hi + slot / 2 + r * row_bytes, &tmt, kx * BK, r0 + r,
+                                            1, &sh->bfull[s]);
+                            }
                         }
                     }
                     par_ext ^= 1u << s;
@@ -621,9 +629,9 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                             const uint32_t dw = d + (uint32_t)lp_first(w);
                             const uint32_t idw = idesc_bf16_f32(BM * CG, lp_rows(w), false, false);
                             const uint64_t da = ext_a + (uint32_t)((s * A_BYTES + e * tile_bytes) >> 4);
-                            const uint64_t hi =
-                                ext_t + (uint32_t)((s * b_bytes + e * (area >> p.lpack)) >> 4);
-                            const uint64_t lo = hi + (uint32_t)(area >> 4);
+                            const uint64_t hi = ext_t + (uint32_t)((s * b_bytes + e * slot) >> 4);
+                            const int lo_off = lp_rows(w) == 16 * CG ? 16 * row_bytes : slot / 2;
+                            const uint64_t lo = hi + (uint32_t)(lo_off >> 4);
                             for (int k = 0; k < ksteps; ++k) {
                                 lp_mma<CG>(dw, da + 2 * k, hi + 2 * k, idw, 1u);
                                 lp_mma<CG>(dw, da + 2 * k, lo + 2 * k, idw, 1u);
@@ -765,9 +773,9 @@ __global__ void __launch_bounds__(lp::THREADS, 2)
                 const int e0 = (x >> deep) << p.lpack;
                 uint8_t *tb = sA + s * A_BYTES, *hi = sB + s * b_bytes;
                 const bool bad =
-                    p.lpack == 2   ? lp_check_block<CG, 4>(sh, buf, e0, half, area, tb, hi, lane)
-                    : p.lpack == 1 ? lp_check_block<CG, 2>(sh, buf, e0, half, area, tb, hi, lane)
-                                   : lp_check_block<CG, 1>(sh, buf, e0, half, area, tb, hi, lane);
+                    p.lpack == 2   ? lp_check_block<CG, 4>(sh, buf, e0, half, slot, tb, hi, lane)
+                    : p.lpack == 1 ? lp_check_block<CG, 2>(sh, buf, e0, half, slot, tb, hi, lane)
+                                   : lp_check_block<CG, 1>(sh, buf, e0, half, slot, tb, hi, lane);
                 if (bad) sh->nonfinite[buf] = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -913,15 +921,15 @@ static PFN_cuTensorMapEncodeTiled_v12000 lp_encoder() {
 
 // [planes, rows, cols] bf16 with the given strides (elements); boxes of
 // box_cols columns (32, 64 or 128 bytes, swizzled over as many) x box_rows
-// rows of one plane. dims == 2: one plane.
+// rows x box_planes planes. dims == 2: one plane.
 static bool lp_map(CUtensorMap *map, const void *base, int dims, long long planes, long long rows,
                    long long cols, long long row_stride, long long plane_stride, int box_cols,
-                   int box_rows) {
+                   int box_rows, int box_planes = 1) {
     auto enc = lp_encoder();
     if (!enc) return false;
     cuuint64_t d[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, (cuuint64_t)plane_stride * 2};
-    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), d,
                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1064,20 +1072,22 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     p.y = static_cast<__nv_bfloat16 *>(a.y);
     p.y_stride = a.y_stride;
     p.status = a.status;
-    CUtensorMap tmw, tmx, tmb, tmt;
+    CUtensorMap tmw, tmx, tmb, tmt, tmt2;
     if (!lp_map(&tmw, a.weight, 2, 1, a.O, a.H, a.H, 0, 64, lp::BM) ||
         !lp_map(&tmx, a.x, 2, 1, a.R, a.H, a.x_stride, 0, 64, p.BN / cg) ||
         !lp_map(&tmb, a.lora_b, 3, a.adapters, a.O, a.rank, a.rank, (long long)a.O * a.rank,
                 64 >> p.lpack, lp::BM) ||
         !lp_map(&tmt, a.workspace, 3, 2, a.R, a.rank, a.rank, (long long)a.R * a.rank, 64 >> p.lpack,
-                16))
+                16) ||
+        !lp_map(&tmt2, a.workspace, 3, 2, a.R, a.rank, a.rank, (long long)a.R * a.rank,
+                64 >> p.lpack, 16, 2))
         return SVF_ERR_LAUNCH;
     if (launch_lora_shrink(a, stream) != cudaSuccess) return SVF_ERR_LAUNCH;
     int clusters = p.tiles;
     if (p.CK == 1 && clusters > plan.resident) clusters = plan.resident;  // persistent
     const int cluster = cg * p.CK;
     if (launch_pdl(kern, dim3((unsigned)(clusters * cluster)), dim3(lp::THREADS), smem, stream,
-                   cluster > 1 ? (unsigned)cluster : 0u, tmw, tmx, tmb, tmt, p) != cudaSuccess)
+                   cluster > 1 ? (unsigned)cluster : 0u, tmw, tmx, tmb, tmt, tmt2, p) != cudaSuccess)
         return SVF_ERR_LAUNCH;
     return SVF_OK;
 }

@@ -15,12 +15,12 @@
 // memory and tensor memory for N = rank columns.
 //
 // A CTA takes a block of 16 MT rows and one of the distinct adapters in it; its
-// 6 warps, and the KS CTAs of its cluster, share the 32-wide blocks of K. The
+// 4 warps, and the KS CTAs of its cluster, share the 32-wide blocks of K. The
 // warps' sums meet in shared memory, the CTAs' over distributed shared memory,
 // in a fixed order. Rows of other adapters in the block are not stored, so an infinity or NaN
 // in one request's adapter or hidden state stays with it.
 //
-// The kernel is small (192 threads, 104 registers, where possible one CTA per SM), so that
+// The kernel is small (128 threads of 128 registers, two CTAs per SM), so that
 // the CTAs of the projection kernel start beside it: its first product needs
 // no t. They are let go once this kernel's first loads are under way, which
 // would otherwise queue behind the projection's.
@@ -32,7 +32,7 @@ namespace svf {
 
 namespace {
 
-constexpr int kShrinkWarps = 6;
+constexpr int kShrinkWarps = 4;
 constexpr int kShrinkThreads = 32 * kShrinkWarps;
 
 struct ShrinkArgs {
@@ -61,7 +61,7 @@ __device__ __forceinline__ uint4 ld16(const __nv_bfloat16 *p, bool ok) {
 // MT: 16-row tiles of x of a block; NT: 8-row tiles of A that a CTA takes
 // (rank in groups of 8 NT)
 template <int MT, int NT, int DEPTH>
-__global__ void __maxnreg__(104) lora_shrink_kernel(ShrinkArgs p) {
+__global__ void __maxnreg__(128) lora_shrink_kernel(ShrinkArgs p) {
     constexpr int ROWS = 16 * MT;
     __shared__ float s_acc[kShrinkWarps][ROWS][NT * 8];
     __shared__ int s_ids[32];
@@ -216,13 +216,13 @@ cudaError_t launch_tiled(ShrinkArgs p, cudaStream_t stream) {
     const int groups = p.R / p.per;
     if (most > groups) most = groups;
     if (most > rows) most = rows;
-    // One CTA per SM, so that the projection's CTAs fit beside them, while
-    // what is read is small; four where it would take longer than the
+    // Two CTAs per SM, so that the projection's CTAs fit beside them, while
+    // what is read is small; six where it would take longer than the
     // projection's first products (then the sooner it is over the better).
     // Where there are fewer blocks than that, an adapter of a block each.
     const int used = groups < p.adapters ? groups : p.adapters;
     const double bytes = 2.0 * p.H * (p.R + (double)used * p.rank);
-    const long long room = bytes > 16e6 ? 4ll * num_sms() : num_sms();
+    const long long room = (bytes > 16e6 ? 6ll : 2ll) * num_sms();
     int slots = most;
     while (slots > 1 && (long long)blocks * slots * p.ngroups > room) slots = (slots + 1) / 2;
     p.slots = slots;
