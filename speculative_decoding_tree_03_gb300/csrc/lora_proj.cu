@@ -26,7 +26,7 @@
 // the first one issues the products for both. One CTA alone would have to
 // bring 48 KB into shared memory per 128 x 256 x 64 block, and shared memory
 // would be what bounds it; the pair brings 32 KB each. CG = 1 serves few rows
-// (bound by the bytes of W), where two CTAs per SM keep more loads in flight.
+// (bound by the bytes of W).
 // Roles of a CTA (320 threads):
 //   warp 0      producer: TMA of W and x blocks, then of B_a and t blocks;
 //   warp 1      MMA issuer (of the pair's first CTA);
@@ -62,8 +62,7 @@ constexpr int THREADS = 320;
 constexpr int MAX_BN = 256;
 constexpr int MAX_LIST = 2 * MAX_BN;    // adapter windows of one row tile
 constexpr int HASH = 2 * MAX_BN;        // slots for the distinct adapters of a row tile
-constexpr int SMEM_ONE = 192 * 1024;    // stage ring of a CTA that has its SM alone
-constexpr int SMEM_TWO = 88 * 1024;     // ... that shares its SM with another
+constexpr int SMEM_BUDGET = 192 * 1024; // stage ring; leaves lora_shrink room beside it
 }  // namespace lp
 
 struct LpParams {
@@ -828,7 +827,8 @@ __global__ void __maxnreg__(80)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int c = r0 + u * (THREADS / 32);
-                    const int off = min(c, c1 - 1) * BM;
+                    if (c >= c1) break;
+                    const int off = c * BM;
                     const uint32_t from = src + (uint32_t)(off * 4);
                     if (quads && k == rank) {
                         t[u] = *reinterpret_cast<const float4 *>(part + off);
@@ -843,6 +843,7 @@ __global__ void __maxnreg__(80)
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
+                    if (r0 + u * (THREADS / 32) >= c1) break;
                     v[u][0] += t[u].x;
                     v[u][1] += t[u].y;
                     v[u][2] += t[u].z;
@@ -950,8 +951,8 @@ static size_t lp_smem(const LpParams &p, int cg) {
     return 1024 + (size_t)p.stages * (lp::A_BYTES + p.BN / cg * 128) + sizeof(LpShared);
 }
 
-static void lp_stages(LpParams *p, int cg, int budget) {
-    p->stages = budget / (lp::A_BYTES + p->BN / cg * 128);
+static void lp_stages(LpParams *p, int cg) {
+    p->stages = lp::SMEM_BUDGET / (lp::A_BYTES + p->BN / cg * 128);
     if (p->stages > lp::MAX_STAGES) p->stages = lp::MAX_STAGES;
 }
 
@@ -961,12 +962,13 @@ struct LpPlan {
     int resident;  // clusters that fit at once
 };
 
-// Rows of x per tile and CTAs (pairs) per tile: the least of a model of the
-// call in ns. A block of K takes a CTA the longest of its products (1900 MHz),
-// its share of what the L2 hands to the SMs (9.5 TB/s measured, 100 GB/s to
-// one) and of HBM (6 TB/s), and the latency of a load (1.7 us) over the stages of its ring; a
-// tile begins and ends with about 4 us, and the sum over a cluster takes about
-// 2.5 us.
+// Tiles of one CTA or a pair, rows of x per tile and CTAs (pairs) per tile: the
+// least of a model of the call in ns. A block of K takes a CTA the longest of
+// its products (1900 MHz), its share of what the L2 hands to the SMs (19 TB/s
+// measured, 130 GB/s to one) and of HBM (6 TB/s), and the latency of a load
+// (1.7 us) over the stages of its ring; an adapter block about 0.6 us. A tile
+// begins with about 3.5 us and ends with its stores (12 ns a row of x), or with
+// the sum over the cluster (20 ns a row).
 static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
     double least = 0;
     for (int cg = 1; cg <= 2; ++cg) {
@@ -982,32 +984,30 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
             if (n > n_min && c.BN < 96) break;
             c.n_tiles = (c.R + c.BN - 1) / c.BN;
             c.tiles = m_tiles * c.n_tiles;
+            lp_stages(&c, cg);
             int most = groups < c.adapters ? groups : c.adapters;
             if (most > c.BN) most = c.BN;
-            const int work = c.kblocks + (((most - 1) >> c.lpack) + 1) * c.kchunks;
-            for (int two = cg == 1 && c.BN <= 64 ? 1 : 0; two >= 0; --two) {
-                lp_stages(&c, cg, two ? lp::SMEM_TWO : lp::SMEM_ONE);
-                const double bytes = lp::A_BYTES + c.BN / cg * 128;
-                for (c.CK = 1; c.CK * cg <= 8 && c.CK <= c.kblocks; ++c.CK) {
-                    const int fit = resident_clusters(kern, lp::THREADS, lp_smem(c, cg), c.CK * cg);
-                    if (fit < 1) continue;
-                    const int waves = (c.tiles + fit - 1) / fit;
-                    if (c.CK > 1 && waves > 1) continue;
-                    const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
-                    double kb = c.BN * 1.05;
-                    const double l2 = bytes * ctas / 9500;
-                    const double hbm = lp::A_BYTES * ctas / 6000 / c.n_tiles;
-                    const double sm = bytes * (two ? ctas / num_sms() : 1) / 100;
-                    if (l2 > kb) kb = l2;
-                    if (hbm > kb) kb = hbm;
-                    if (sm > kb) kb = sm;
-                    if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
-                    const double t =
-                        waves * ((double)work / c.CK * kb + 4000) + (c.CK > 1 ? 2500 : 0);
-                    if (least == 0 || t < least) {
-                        least = t;
-                        *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};
-                    }
+            const int blocks = (((most - 1) >> c.lpack) + 1) * c.kchunks;
+            const double bytes = lp::A_BYTES + c.BN / cg * 128;
+            for (c.CK = 1; c.CK * cg <= 8 && c.CK <= c.kblocks; ++c.CK) {
+                const int fit = resident_clusters(kern, lp::THREADS, lp_smem(c, cg), c.CK * cg);
+                if (fit < 1) continue;
+                const int waves = (c.tiles + fit - 1) / fit;
+                if (c.CK > 1 && waves > 1) continue;
+                const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
+                double kb = c.BN * 1.05;
+                const double l2 = bytes * ctas / 19000, sm = bytes / 130;
+                const double hbm = lp::A_BYTES * ctas / 6000 / c.n_tiles;
+                if (l2 > kb) kb = l2;
+                if (sm > kb) kb = sm;
+                if (hbm > kb) kb = hbm;
+                if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
+                const double t =
+                    waves * ((c.kblocks * kb + blocks * 600.0) / c.CK + 3500) +
+                    (c.CK > 1 ? 1500 + 20.0 * c.BN : 12.0 * c.BN);
+                if (least == 0 || t < least) {
+                    least = t;
+                    *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};
                 }
             }
         }
