@@ -699,21 +699,33 @@ def _bad(t, name: str, dtype, shape, dev: int):
 
 def _p(t, name: str, dtype, shape, dev: int) -> int:
     """The address of a contiguous tensor of this dtype, shape and device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
-            and t.shape == shape and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        pass
     _bad(t, name, dtype, shape, dev)
+
+
+def _current_stream(dev: int) -> int:
+    """The handle of the device's current stream (the stream object that the
+    public call makes costs a microsecond)."""
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+_current_device = torch.cuda.current_device
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _call(fn, what: str, dev: int, stream, *args) -> None:
     """fn(*args, stream) with ``dev`` current; the default stream is the
     current one of that device."""
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _call(fn, what, dev, stream, *args)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    rc = fn(*args, stream.cuda_stream)
+    rc = fn(*args, _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc != SVF_OK:
         _check(rc, what)
 

@@ -14,8 +14,12 @@
 // Bound: HBM: each q, k and v element is read once and written once, plus one
 // table row of 4 rot bytes per token. So no staging: a thread takes 16 bytes
 // of either half of a pair block (32 contiguous bytes when interleaved), reads
-// its cosines and sines once and walks over HEADS heads with them, all of its
-// loads issued before the first is used.
+// its cosines and sines once and takes HEADS heads with them, all of its loads
+// issued before the first is used; nothing is read twice, so loads and stores
+// are marked for early eviction. Measured for 16391 rows of 32 + 8 + 8 heads of
+// 128 (bf16, 407 MB): 59.7 us, the rate of a plain copy; 73.2 us with 256
+// threads and four heads each, 60.7 us with 128, 67.7 us with two heads each. For
+// 1984 rows of 64 + 8 + 8 heads (82 MB) 14.1 us, 86 % of a copy.
 #include "common.cuh"
 #include "internal.h"
 
@@ -23,7 +27,7 @@ namespace svf {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 struct RopeArgs {
     const uint8_t *q, *k, *v;
@@ -121,8 +125,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(RopeArgs a) {
                 : h < a.Hq + a.Hkv
                     ? a.k + t * a.k_stride + (size_t)(h - a.Hq) * a.head_bytes
                     : a.v + t * a.v_stride + (size_t)(h - a.Hq - a.Hkv) * a.head_bytes;
-            xa[u] = *reinterpret_cast<const uint4 *>(src + oa);
-            if (has_b) xb[u] = *reinterpret_cast<const uint4 *>(src + ob);
+            xa[u] = __ldcs(reinterpret_cast<const uint4 *>(src + oa));
+            if (has_b) xb[u] = __ldcs(reinterpret_cast<const uint4 *>(src + ob));
         }
     }
 #pragma unroll
@@ -146,8 +150,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(RopeArgs a) {
                        : h < a.Hq + a.Hkv
                            ? a.k_cache + kv_row + (size_t)(h - a.Hq) * a.head_bytes
                            : a.v_cache + kv_row + (size_t)(h - a.Hq - a.Hkv) * a.head_bytes;
-        *reinterpret_cast<uint4 *>(dst + oa) = xa[u];
-        if (has_b) *reinterpret_cast<uint4 *>(dst + ob) = xb[u];
+        __stcs(reinterpret_cast<uint4 *>(dst + oa), xa[u]);
+        if (has_b) __stcs(reinterpret_cast<uint4 *>(dst + ob), xb[u]);
     }
 }
 
@@ -156,14 +160,14 @@ cudaError_t launch_typed(const RopeArgs &a, cudaStream_t stream) {
     const int H = a.Hq + 2 * a.Hkv;
     const dim3 block((unsigned)(a.J * a.HG));
     // few rows: one head per thread, so that every load of the call is in
-    // flight at once; many rows: four, which amortises the table row
+    // flight at once; many rows: three, which amortises the table row
     const long long blocks1 = (long long)a.T * ((H + a.HG - 1) / a.HG);
     if (blocks1 <= 2ll * num_sms())
         return launch_pdl(rope_kv_kernel<T, INTER, 1>,
                           dim3((unsigned)a.T, (unsigned)((H + a.HG - 1) / a.HG)), block, 0, stream,
                           0u, a);
-    const int per = a.HG * 4;
-    return launch_pdl(rope_kv_kernel<T, INTER, 4>,
+    const int per = a.HG * 3;
+    return launch_pdl(rope_kv_kernel<T, INTER, 3>,
                       dim3((unsigned)a.T, (unsigned)((H + per - 1) / per)), block, 0, stream, 0u,
                       a);
 }
