@@ -679,8 +679,9 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Te
 
 # ---------------------------------------------------------------------------
 # The operators around the verify pass: pages, rotary K/V write, projections
-# with per-request adapters. Their calls are short, so each tensor is checked
-# in one expression, and the message is put together only for a bad one.
+# with per-request adapters. Their calls are short, so a call's tensors are
+# checked in one expression; where it is false, each is checked by itself for
+# the message.
 # ---------------------------------------------------------------------------
 
 def _device_of(t, name: str) -> int:
@@ -699,12 +700,9 @@ def _bad(t, name: str, dtype, shape, dev: int):
 
 def _p(t, name: str, dtype, shape, dev: int) -> int:
     """The address of a contiguous tensor of this dtype, shape and device."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except (AttributeError, TypeError):
-        pass
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
     _bad(t, name, dtype, shape, dev)
 
 
@@ -730,19 +728,13 @@ def _call(fn, what: str, dev: int, stream, *args) -> None:
         _check(rc, what)
 
 
-def _out(o: dict, key: str, dtype, shape, like: torch.Tensor, dev: int) -> int:
-    """The address of output ``key``, allocated on first use."""
-    t = o.get(key)
-    if t is None:
-        t = o[key] = torch.empty(shape, dtype=dtype, device=like.device)
-        return t.data_ptr()
-    return _p(t, key, dtype, shape, dev)
-
-
-def _pool(pool: dict, dev: int):
-    free, n = pool["free"], pool["free"].numel()
-    return (_p(free, "pool['free']", torch.int32, (n,), dev),
-            _p(pool["state"], "pool['state']", torch.int32, (4,), dev), n)
+def _outs(o: dict, dtype, like: torch.Tensor, dev: int, **shapes) -> None:
+    """Allocate the outputs that ``o`` lacks, check the ones that it has."""
+    for key, shape in shapes.items():
+        if o.get(key) is None:
+            o[key] = torch.empty(shape, dtype=dtype, device=like.device)
+        else:
+            _p(o[key], key, dtype, shape, dev)
 
 
 def page_pool(num_pages: int, device="cuda", stream=None) -> dict:
@@ -752,10 +744,38 @@ def page_pool(num_pages: int, device="cuda", stream=None) -> dict:
         raise SpecVerifyError("num_pages must be at least 1")
     pool = {"free": torch.empty((num_pages,), dtype=torch.int32, device=device),
             "state": torch.empty((4,), dtype=torch.int32, device=device)}
-    dev = _device_of(pool["free"], "device")
-    free, state, n = _pool(pool, dev)
-    _call(load_library().svf_page_pool_init, "svf_page_pool_init", dev, stream, free, state, n)
+    free, state = pool["free"], pool["state"]
+    _call(load_library().svf_page_pool_init, "svf_page_pool_init", _device_of(free, "device"),
+          stream, free.data_ptr(), state.data_ptr(), num_pages)
     return pool
+
+
+def _page_args(pool: dict, page_table, lens_a, name_a: str, lens_b, name_b: str):
+    """Check what the two calls on a pool and a table share; (dev, B, max_pages)."""
+    dev = _device_of(page_table, "page_table")
+    if page_table.dim() != 2:
+        raise SpecVerifyError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    free, state, i32, row = pool["free"], pool["state"], torch.int32, (B,)
+    try:
+        fine = (page_table.dtype is i32 and page_table.is_contiguous()
+                and free.dtype is i32 and free.get_device() == dev and free.dim() == 1
+                and free.is_contiguous()
+                and state.dtype is i32 and state.get_device() == dev and state.shape == (4,)
+                and state.is_contiguous()
+                and lens_a.dtype is i32 and lens_a.get_device() == dev and lens_a.shape == row
+                and lens_a.is_contiguous()
+                and lens_b.dtype is i32 and lens_b.get_device() == dev and lens_b.shape == row
+                and lens_b.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _p(page_table, "page_table", i32, (B, max_pages), dev)
+        _p(free, "pool['free']", i32, (free.numel(),), dev)
+        _p(state, "pool['state']", i32, (4,), dev)
+        _p(lens_a, name_a, i32, row, dev)
+        _p(lens_b, name_b, i32, row, dev)
+    return dev, B, max_pages
 
 
 def page_reserve(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -770,26 +790,38 @@ def page_reserve(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor,
     row's position seq_lens + depth instead of seq_lens + i. Returns device
     tensors slots [rows], positions [rows], row_offsets [B + 1], status [B]."""
     lib = _lib or load_library()
-    dev = _device_of(page_table, "page_table")
-    if page_table.dim() != 2:
-        raise SpecVerifyError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
-    i32 = torch.int32
+    dev, B, max_pages = _page_args(pool, page_table, seq_lens, "seq_lens", new_lens, "new_lens")
+    free, i32 = pool["free"], torch.int32
     o = outputs if outputs is not None else {}
-    free, state, n = _pool(pool, dev)
+    try:
+        slots, positions, offsets, status = (o["slots"], o["positions"], o["row_offsets"],
+                                             o["status"])
+        fine = (slots.dtype is i32 and slots.get_device() == dev and slots.shape == (rows,)
+                and slots.is_contiguous()
+                and positions.dtype is i32 and positions.get_device() == dev
+                and positions.shape == (rows,) and positions.is_contiguous()
+                and offsets.dtype is i32 and offsets.get_device() == dev
+                and offsets.shape == (B + 1,) and offsets.is_contiguous()
+                and status.dtype is i32 and status.get_device() == dev
+                and status.shape == (B,) and status.is_contiguous())
+    except (KeyError, AttributeError):
+        fine = False
+    if not fine:
+        if rows < 0:
+            raise SpecVerifyError("rows must not be negative")
+        _outs(o, i32, page_table, dev, slots=(rows,), positions=(rows,), row_offsets=(B + 1,),
+              status=(B,))
+        slots, positions, offsets, status = (o["slots"], o["positions"], o["row_offsets"],
+                                             o["status"])
     d = None
     if depth is not None:
         if depth.numel() != rows:
             raise SpecVerifyError("depth must hold one value per row")
         d = _p(depth, "depth", i32, depth.shape, dev)
-    _call(lib.svf_page_reserve, "svf_page_reserve", dev, stream,
-          _p(page_table, "page_table", i32, (B, max_pages), dev), max_pages, page_size, free,
-          state, n, _p(seq_lens, "seq_lens", i32, (B,), dev),
-          _p(new_lens, "new_lens", i32, (B,), dev), B, rows, d,
-          _out(o, "slots", i32, (rows,), page_table, dev),
-          _out(o, "positions", i32, (rows,), page_table, dev),
-          _out(o, "row_offsets", i32, (B + 1,), page_table, dev),
-          _out(o, "status", i32, (B,), page_table, dev))
+    _call(lib.svf_page_reserve, "svf_page_reserve", dev, stream, page_table.data_ptr(), max_pages,
+          page_size, free.data_ptr(), pool["state"].data_ptr(), free.numel(), seq_lens.data_ptr(),
+          new_lens.data_ptr(), B, rows, d, slots.data_ptr(), positions.data_ptr(),
+          offsets.data_ptr(), status.data_ptr())
     return o
 
 
@@ -800,31 +832,35 @@ def page_release(pool: dict, page_table: torch.Tensor, old_lens: torch.Tensor,
     tokens back to the pool (after kv_commit: seq_lens + N and new_seq_lens;
     for finished requests keep 0). Returns n_released [B], status [B]."""
     lib = _lib or load_library()
-    dev = _device_of(page_table, "page_table")
-    if page_table.dim() != 2:
-        raise SpecVerifyError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
-    i32 = torch.int32
+    dev, B, max_pages = _page_args(pool, page_table, old_lens, "old_lens", keep_lens, "keep_lens")
+    free, i32 = pool["free"], torch.int32
     o = outputs if outputs is not None else {}
-    free, state, n = _pool(pool, dev)
-    _call(lib.svf_page_release, "svf_page_release", dev, stream,
-          _p(page_table, "page_table", i32, (B, max_pages), dev), max_pages, page_size, free,
-          state, n, _p(old_lens, "old_lens", i32, (B,), dev),
-          _p(keep_lens, "keep_lens", i32, (B,), dev), B,
-          _out(o, "n_released", i32, (B,), page_table, dev),
-          _out(o, "status", i32, (B,), page_table, dev))
+    try:
+        n_released, status = o["n_released"], o["status"]
+        fine = (n_released.dtype is i32 and n_released.get_device() == dev
+                and n_released.shape == (B,) and n_released.is_contiguous()
+                and status.dtype is i32 and status.get_device() == dev
+                and status.shape == (B,) and status.is_contiguous())
+    except (KeyError, AttributeError):
+        fine = False
+    if not fine:
+        _outs(o, i32, page_table, dev, n_released=(B,), status=(B,))
+        n_released, status = o["n_released"], o["status"]
+    _call(lib.svf_page_release, "svf_page_release", dev, stream, page_table.data_ptr(), max_pages,
+          page_size, free.data_ptr(), pool["state"].data_ptr(), free.numel(), old_lens.data_ptr(),
+          keep_lens.data_ptr(), B, n_released.data_ptr(), status.data_ptr())
     return o
 
 
-def _rows(t, name: str, dtype, shape, dev: int):
-    """Address and row stride of [T, heads, D] with dense heads."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
-            and t.shape == shape):
+def _row_stride(t, name: str, dtype, shape, dev: int) -> int:
+    """Elements between the rows of [T, heads, D] with dense heads."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev):
         _bad(t, name, dtype, shape, dev)
     s0, s1, s2 = t.stride()
     if (s2 != 1 and shape[2] > 1) or (s1 != shape[2] and shape[1] > 1):
         raise SpecVerifyError(f"{name} must have dense heads (strides [row, D, 1])")
-    return t.data_ptr(), s0 if shape[0] > 1 else shape[1] * shape[2]
+    return s0 if shape[0] > 1 else shape[1] * shape[2]
 
 
 def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor,
@@ -841,29 +877,47 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch
     what q_out held (a new q_out: undefined)."""
     lib = _lib or load_library()
     dev = _device_of(q, "q")
-    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
-        raise SpecVerifyError("q and k must be [T, heads, D], the caches [pages, page_size, Hkv, D]")
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4 or rope.dim() != 2:
+        raise SpecVerifyError("q and k must be [T, heads, D], the caches [pages, page_size, Hkv, "
+                              "D], rope [max_pos, rot]")
     T, Hq, D = q.shape
-    Hkv, dt = k.shape[1], q.dtype
-    qp, qs = _rows(q, "q", dt, (T, Hq, D), dev)
-    kp, ks = _rows(k, "k", dt, (T, Hkv, D), dev)
-    vp, vs = _rows(v, "v", dt, (T, Hkv, D), dev)
-    if rope.dim() != 2:
-        raise SpecVerifyError("rope must be [max_pos, rot]")
+    Hkv, dt, i32 = k.shape[1], q.dtype, torch.int32
+    qs, ks, vs = (_row_stride(q, "q", dt, (T, Hq, D), dev), _row_stride(k, "k", dt, (T, Hkv, D), dev),
+                  _row_stride(v, "v", dt, (T, Hkv, D), dev))
     max_pos, rot = rope.shape
     pages, ps = k_cache.shape[:2]
-    cache = (pages, ps, Hkv, D)
+    cache, row = (pages, ps, Hkv, D), (T,)
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
     if status is None:
-        status = torch.empty((T,), dtype=torch.int32, device=q.device)
-    _call(lib.svf_rope_kv_write, "svf_rope_kv_write", dev, stream, qp, kp, vp, qs, ks, vs, T, Hq,
-          Hkv, D, _dtype_code(dt), _p(rope, "rope", torch.float32, (max_pos, rot), dev), rot,
-          max_pos, 1 if interleaved else 0,
-          _p(positions, "positions", torch.int32, (T,), dev),
-          _p(slots, "slots", torch.int32, (T,), dev), _p(q_out, "q_out", dt, (T, Hq, D), dev),
-          _p(k_cache, "k_cache", dt, cache, dev), _p(v_cache, "v_cache", dt, cache, dev),
-          pages * ps, _p(status, "status", torch.int32, (T,), dev))
+        status = torch.empty(row, dtype=i32, device=q.device)
+    try:
+        fine = (rope.dtype is torch.float32 and rope.get_device() == dev and rope.is_contiguous()
+                and positions.dtype is i32 and positions.get_device() == dev
+                and positions.shape == row and positions.is_contiguous()
+                and slots.dtype is i32 and slots.get_device() == dev and slots.shape == row
+                and slots.is_contiguous()
+                and q_out.dtype is dt and q_out.get_device() == dev and q_out.shape == (T, Hq, D)
+                and q_out.is_contiguous()
+                and k_cache.dtype is dt and k_cache.get_device() == dev
+                and k_cache.shape == cache and k_cache.is_contiguous()
+                and v_cache.dtype is dt and v_cache.get_device() == dev
+                and v_cache.shape == cache and v_cache.is_contiguous()
+                and status.dtype is i32 and status.get_device() == dev and status.shape == row
+                and status.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        for t, name, dtype, shape in (
+                (rope, "rope", torch.float32, (max_pos, rot)), (positions, "positions", i32, row),
+                (slots, "slots", i32, row), (q_out, "q_out", dt, (T, Hq, D)),
+                (k_cache, "k_cache", dt, cache), (v_cache, "v_cache", dt, cache),
+                (status, "status", i32, row)):
+            _p(t, name, dtype, shape, dev)
+    _call(lib.svf_rope_kv_write, "svf_rope_kv_write", dev, stream, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), qs, ks, vs, T, Hq, Hkv, D, _dtype_code(dt), rope.data_ptr(), rot, max_pos,
+          1 if interleaved else 0, positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), pages * ps, status.data_ptr())
     return q_out, status
 
 
@@ -912,19 +966,40 @@ def lora_proj(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, lora_
         op, os_ = out.data_ptr(), out.stride(0)
     else:
         op, os_ = _p(out, "out", bf, shape, dev), O
+    i32 = torch.int32
     if status is None:
-        status = torch.empty((G,), dtype=torch.int32, device=x.device)
+        status = torch.empty((G,), dtype=i32, device=x.device)
     if workspace is None:
-        workspace = torch.empty((lora_proj_workspace_size(R, rank),), dtype=torch.uint8, device=x.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        workspace = torch.empty((lora_proj_workspace_size(R, rank),), dtype=torch.uint8,
+                                device=x.device)
+    try:
+        fine = (weight.dtype is bf and weight.get_device() == dev and weight.is_contiguous()
+                and lora_a.dtype is bf and lora_a.get_device() == dev
+                and lora_a.shape[2] == H and lora_a.is_contiguous()
+                and lora_b.dtype is bf and lora_b.get_device() == dev
+                and lora_b.shape == (adapters, O, rank) and lora_b.is_contiguous()
+                and ids.dtype is i32 and ids.get_device() == dev and ids.is_contiguous()
+                and (scales is None
+                     or (scales.dtype is torch.float32 and scales.get_device() == dev
+                         and scales.shape == (adapters,) and scales.is_contiguous()))
+                and status.dtype is i32 and status.get_device() == dev and status.shape == (G,)
+                and status.is_contiguous()
+                and workspace.get_device() == dev and workspace.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _p(weight, "weight", bf, (O, H), dev)
+        _p(lora_a, "lora_a", bf, (adapters, rank, H), dev)
+        _p(lora_b, "lora_b", bf, (adapters, O, rank), dev)
+        _p(ids, "ids", i32, (G,), dev)
+        if scales is not None:
+            _p(scales, "scales", torch.float32, (adapters,), dev)
+        _p(status, "status", i32, (G,), dev)
         raise SpecVerifyError("workspace must be a contiguous tensor on x's device")
-    _call(lib.svf_lora_proj, "svf_lora_proj", dev, stream, x.data_ptr(), xs,
-          _p(weight, "weight", bf, (O, H), dev), _p(lora_a, "lora_a", bf, (adapters, rank, H), dev),
-          _p(lora_b, "lora_b", bf, (adapters, O, rank), dev),
-          None if scales is None else _p(scales, "scales", torch.float32, (adapters,), dev),
-          _p(ids, "ids", torch.int32, (G,), dev), R // G if G else 1, R, H, O, adapters, rank,
-          op, os_, workspace.data_ptr(), workspace.nbytes,
-          _p(status, "status", torch.int32, (G,), dev))
+    _call(lib.svf_lora_proj, "svf_lora_proj", dev, stream, x.data_ptr(), xs, weight.data_ptr(),
+          lora_a.data_ptr(), lora_b.data_ptr(), None if scales is None else scales.data_ptr(),
+          ids.data_ptr(), R // G if G else 1, R, H, O, adapters, rank, op, os_,
+          workspace.data_ptr(), workspace.nbytes, status.data_ptr())
     return out, status
 
 
