@@ -658,11 +658,11 @@ int svf_rope_kv_write(const void *q, const void *k, const void *v, long long q_s
  *            that may overlap on the GPU need workspaces of their own.
  *   status   [R / rows_per_id] int32 out: SVF_DEV_BAD_ADAPTER (an id outside
  *            [-1, adapters): the rows of that id are 0); SVF_DEV_TIMEOUT or
- *            SVF_DEV_BAD_CLUSTER in status[0] if the kernel gave up (y is then
+ *            SVF_DEV_BAD_CLUSTER in status[0] if a kernel gave up (y is then
  *            undefined)
  * An infinity or NaN in a row of x or in an adapter reaches the rows that use
  * it and no others.
- * Limits: 1 <= R <= 2^20, R a multiple of rows_per_id >= 1; H <= 65536 a
+ * Limits: 1 <= R <= 2^17, R a multiple of rows_per_id >= 1; H <= 65536 a
  * multiple of 8; 1 <= O <= 2^20; rank <= 128 a multiple of 8; 1 <= adapters <=
  * 65536; x, weight, lora_a and lora_b 16-byte aligned, x_stride a multiple of
  * 8, x_stride >= H and y_stride >= O. y must not overlap an input.

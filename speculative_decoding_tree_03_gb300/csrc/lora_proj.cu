@@ -2,10 +2,11 @@
 //     y[r] = W x[r] + s_a B_a (A_a x[r]),   a = ids[r / rows_per_id]
 // (a = -1: y[r] = W x[r]), bf16 operands and result, fp32 sums.
 //
-// lora_shrink.cu leaves t[r] = s_a A_a x[r]. Here the rest is ONE matrix product with a longer inner axis: to the H columns of x and W come,
-// for every distinct adapter a of the row tile, rank columns that hold t on
-// the rows of a (zero on the others) and B_a. So the adapters ride in the same
-// tensor-memory accumulator as the shared product, and y is written once.
+// lora_shrink.cu leaves t[r] = s_a A_a x[r]. Here the rest is ONE matrix product
+// with a longer inner axis: to the H columns of x and W come, for every
+// distinct adapter a of the row tile, rank columns that hold t on the rows of a
+// (zero on the others) and B_a. So the adapters ride in the same tensor-memory
+// accumulator as the shared product, and y is written once.
 //   - t is kept as two bf16 terms, hi + lo (16 bits of significand, error
 //     2^-16 of t): one rounding to bf16 would add an error as large as the
 //     result's own when the adapter's part dominates.
@@ -15,9 +16,9 @@
 //     terms are added to the rows of a alone, in the epilogue.
 //   - The tensor-core work of an adapter is confined to the window of the tile
 //     that holds its rows (the MMA's N: steps of 16 rows, of 32 for a pair of
-//     CTAs), and a 64-column
-//     block carries as many adapters as fit: 4 of rank <= 16 (tiles of 32-byte
-//     rows), 2 of rank <= 32 (64 bytes), else one (128 bytes).
+//     CTAs), and a 64-column block carries as many adapters as fit: 4 of rank
+//     <= 16 (tiles of 32-byte rows), 2 of rank <= 32 (64 bytes), else one (128
+//     bytes).
 //
 // W's rows are the MMA's M axis (128 per CTA), the rows of x its N axis (tiles
 // of BN <= 256), K in blocks of 64 staged by TMA with 128-byte swizzle.
@@ -40,6 +41,20 @@
 // Few rows leave too few tiles for the SMs: CK CTAs (or pairs) of a cluster
 // then share a tile, each with an equal part of K and every CK-th adapter
 // block, and their sums meet over distributed shared memory in a fixed order.
+//
+// Bound and measured (graph replays, three sets of inputs in turn): 1984 rows,
+// 8192 -> 10240, 24 adapters of rank 16: the tensor cores, 200-206 us = 1.62 to
+// 1.67 PFLOP/s, 97 % of the measured sustained rate of a library product under
+// the power cap (341 us with one CTA per tile and lane-predicated issue). Few
+// rows: HBM and the call's own latency: one row, 4096 -> 6144: 16.1 us, of which
+// W streams for 7 (50 MB at 7 TB/s), 3.3 pass from the first launch to this
+// kernel's start, 2.5 to the first product, 3.3 in the cluster's sum and exit.
+// Tried and dropped: adapter blocks spread among the last blocks of K (70B-shaped
+// batch 222 against 200 us: their checks and the products share shared memory's
+// bandwidth), a slot of their own for them (203 against 202), one polling lane
+// per warp (one row 19.2 against 18.3), two CTAs per SM (19.8 against 16.9),
+// B_a brought before t is there (24.1 against 24.3 for 64 requests, 28.1 against
+// 27.4 for the EAGLE-2 batch).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -942,7 +957,7 @@ static bool lp_map(CUtensorMap *map, const void *base, int dims, long long plane
 }
 
 bool lora_proj_supported(int R, int H, int O, int adapters, int rank) {
-    return R >= 1 && R <= (1 << 20) && H >= 8 && H % 8 == 0 && H <= (1 << 16) && O >= 1 &&
+    return R >= 1 && R <= (1 << 17) && H >= 8 && H % 8 == 0 && H <= (1 << 16) && O >= 1 &&
            O <= (1 << 20) && adapters >= 1 && adapters <= (1 << 16) && rank >= 8 &&
            rank % 8 == 0 && rank <= 128;
 }
@@ -950,6 +965,9 @@ bool lora_proj_supported(int R, int H, int O, int adapters, int rank) {
 static size_t lp_smem(const LpParams &p, int cg) {
     return 1024 + (size_t)p.stages * (lp::A_BYTES + p.BN / cg * 128) + sizeof(LpShared);
 }
+
+// The limit that every call sets, so that calls of several host threads agree.
+static constexpr size_t kLpMaxSmem = 1024 + lp::SMEM_BUDGET + sizeof(LpShared);
 
 static void lp_stages(LpParams *p, int cg) {
     p->stages = lp::SMEM_BUDGET / (lp::A_BYTES + p->BN / cg * 128);
@@ -990,7 +1008,7 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
             const int blocks = (((most - 1) >> c.lpack) + 1) * c.kchunks;
             const double bytes = lp::A_BYTES + c.BN / cg * 128;
             for (c.CK = 1; c.CK * cg <= 8 && c.CK <= c.kblocks; ++c.CK) {
-                const int fit = resident_clusters(kern, lp::THREADS, lp_smem(c, cg), c.CK * cg);
+                const int fit = resident_clusters(kern, lp::THREADS, kLpMaxSmem, c.CK * cg);
                 if (fit < 1) continue;
                 const int waves = (c.tiles + fit - 1) / fit;
                 if (c.CK > 1 && waves > 1) continue;
@@ -1059,7 +1077,7 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     p.CK = plan.CK;
     auto kern = cg == 2 ? lora_proj_kernel<2> : lora_proj_kernel<1>;
     const size_t smem = lp_smem(p, cg);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLpMaxSmem) !=
         cudaSuccess)
         return SVF_ERR_LAUNCH;
     uint32_t cols = 32;

@@ -110,13 +110,13 @@ def test_lora_proj_argument_checks(lib):
         assert call(**kw) == ARG, kw
     assert call(R=0, x=None) == OK
     for kw in (dict(H=60), dict(H=0), dict(H=65544), dict(O=0), dict(n=0), dict(n=65537),
-               dict(rank=0), dict(rank=12), dict(rank=136), dict(R=(1 << 20) + 2)):
+               dict(rank=0), dict(rank=12), dict(rank=136), dict(R=(1 << 17) + 2)):
         assert call(**kw) == UNSUPPORTED, kw
     for kw in (dict(ws=None), dict(wsb=4 * 16 * 4 - 1), dict(ws=Q)):
         assert call(**kw) == WORKSPACE, kw
     assert lib.svf_lora_proj_workspace_size(4, 16) == 256
     assert lib.svf_lora_proj_workspace_size(0, 16) == 0
-    assert lib.svf_lora_proj_workspace_size(1 << 20, 128) == (1 << 20) * 512  # past 32 bits of count
+    assert lib.svf_lora_proj_workspace_size(1 << 17, 128) == 1 << 26
 
 
 def test_status_strings(sv):
