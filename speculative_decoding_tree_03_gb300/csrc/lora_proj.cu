@@ -101,6 +101,7 @@ struct LpShared {
     uint64_t bfull[lp::MAX_STAGES];  // a block of B_a has landed
     uint64_t ext[lp::MAX_STAGES];    // ... is looked over, and t stands next to it (first CTA)
     uint64_t empty[lp::MAX_STAGES];
+    uint64_t recv;                   // the other CTAs' sums of this CTA's rows of y
     uint64_t acc_full[2], acc_empty[2], list_full[2], list_empty[2], ext_done[2];
     int ids[2][lp::MAX_BN];     // adapter of each row of the tile; -1 none, -2 a bad id
     uint32_t list[2][lp::MAX_LIST]; // an adapter's window: lp_window's fields
@@ -165,6 +166,17 @@ __device__ __forceinline__ bool lp_elect() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
                  : "memory");
+}
+
+// A bulk copy from this CTA's shared memory to the same object `dst` of CTA `to`
+// of the cluster, whose bytes count on that CTA's `bar`.
+__device__ __forceinline__ void bulk_copy_peer(void *dst, const void *src, uint32_t bytes,
+                                               uint64_t *bar, uint32_t to) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+        "[%3];" ::"r"(cluster_map(dst, to)),
+        "r"(smem_u32(src)), "r"(bytes), "r"(cluster_map(bar, to))
+        : "memory");
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -238,12 +250,6 @@ __device__ __forceinline__ uint64_t lp_desc(uint32_t start, uint32_t row_bytes) 
     d |= layout << 61;
     return d;
 }
-// Byte offset of 16-byte chunk c of row `row` in such a tile.
-__device__ __forceinline__ int lp_swizzled(int row, int c, int row_bytes) {
-    const int sh = row_bytes == 128 ? 0 : row_bytes == 64 ? 1 : 2;
-    return row * row_bytes + ((c ^ ((row >> sh) & (row_bytes / 16 - 1))) << 4);
-}
-
 // The distinct adapters of rows [n0, n0 + BN), in order of first appearance,
 // each with the window of the tile that holds its rows (16 CG rows aligned),
 // in pieces of at most BN / 2 rows: at most 3 pieces for an adapter of two
@@ -470,6 +476,7 @@ __global__ void __maxnreg__(80)
             mbar_init(&sh->list_empty[a], 10);  // warps 0, 1, 2-5, 6-9
             mbar_init(&sh->ext_done[a], 4);
         }
+        mbar_init(&sh->recv, 1);
         sh->committed = 0;
         sh->abort = 0;
         mbar_fence_init();
@@ -492,7 +499,7 @@ __global__ void __maxnreg__(80)
     // Only t waits for the kernel before this one (in the producer): that
     // kernel lets this one start after its own wait, so what this call reads
     // besides t was complete by then.
-    if (p.CK > 1) pdl_launch_dependents();
+    if (tile_step >= p.tiles) pdl_launch_dependents();  // one tile each
     const uint32_t tmem = sh->tmem;
     // A stage's full barrier counts its W and x blocks, its bfull barrier its
     // B_a blocks; who waits for one keeps the parity of its next phase, one
@@ -690,6 +697,7 @@ __global__ void __maxnreg__(80)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) part[(c + j) * BM] = __uint_as_float(r[j]);
                 }
+                fence_proxy_async_smem();  // the bulk copies below read them
             } else {
                 const bool plain = !patch && !sh->bad_id[buf];
                 for (int c = 0; c < p.BN; c += 32) {
@@ -815,77 +823,68 @@ __global__ void __maxnreg__(80)
     if (p.CK > 1) {
         // ------------------------------------------------------------ cluster sum
         // Each CTA adds up an equal part of the tile's columns (rows of y)
-        // from the CK partial tiles of its rows of W, in order of K.
+        // from the CK partial tiles of its rows of W, in order of K. The parts
+        // move by bulk copies from shared memory to shared memory, one per
+        // pair of CTAs, behind the receiver's own partial tile (128 rows of y
+        // of a tile of 256, two CTAs: loads from the other CTA's shared memory
+        // took 4.5 us, at 7 bytes a cycle).
         cluster_arrive();
         cluster_wait();
         const int m0 = (first_tile / p.n_tiles * CG + half) * BM;
         const int n0 = first_tile % p.n_tiles * p.BN;
         const int cols = min(p.BN, p.R - n0);
         const int c0 = cols * rank / p.CK, c1 = cols * (rank + 1) / p.CK;
+        const int most = (p.BN + p.CK - 1) / p.CK;
+        float *part = reinterpret_cast<float *>(smem), *recv = part + p.BN * BM;
+        if (tid == 0) {
+            mbar_arrive_expect_tx(&sh->recv, (uint32_t)((p.CK - 1) * (c1 - c0) * BM * 4));
+            for (int d = 1; d < p.CK; ++d) {
+                const int k = rank + d < p.CK ? rank + d : rank + d - p.CK;
+                const int b0 = cols * k / p.CK, b1 = cols * (k + 1) / p.CK;
+                if (b1 > b0)
+                    bulk_copy_peer(recv + (rank < k ? rank : rank - 1) * most * BM, part + b0 * BM,
+                                   (uint32_t)((b1 - b0) * BM * 4), &sh->recv,
+                                   (uint32_t)(k * CG + half));
+            }
+        }
         int patch = 0;
         for (int k = 0; k < p.CK; ++k)
             patch |= ld_dsmem_s32(cluster_map(&sh->nonfinite[0], (uint32_t)(k * CG + half)));
+        lp_wait(&sh->recv, 0, abort_flag, p.wait_ns);
         const bool quads = (p.y_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 7) == 0;
         // a warp takes a row of y, a lane 4 neighbouring columns of it (where
-        // rows are 8-byte aligned, else every 32nd); 4 rows at a time, so that
-        // their loads from the other CTAs are in flight together
-        const int at = quads ? lane * 4 : lane, step = quads ? 1 : 32;
-        const float *part = reinterpret_cast<const float *>(smem) + at;
-        const int o = m0 + at;
-        for (int r0 = c0 + warp; r0 < c1; r0 += 4 * (THREADS / 32)) {
-            float v[4][4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
+        // rows are 8-byte aligned, else every 32nd)
+        const int step = quads ? 1 : 32, o2 = quads ? lane * 4 : lane;
+        const int o = m0 + o2;
+        for (int c = c0 + warp; c < c1; c += THREADS / 32) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
             for (int k = 0; k < p.CK; ++k) {
-                const uint32_t src = cluster_map(part, (uint32_t)(k * CG + half));
-                float4 t[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int c = r0 + u * (THREADS / 32);
-                    if (c >= c1) break;
-                    const int off = c * BM;
-                    const uint32_t from = src + (uint32_t)(off * 4);
-                    if (quads && k == rank) {
-                        t[u] = *reinterpret_cast<const float4 *>(part + off);
-                    } else if (quads) {
-                        t[u] = ld_dsmem_v4(from);
-                    } else {
-                        t[u].x = ld_dsmem_f32(from);
-                        t[u].y = ld_dsmem_f32(from + 128);
-                        t[u].z = ld_dsmem_f32(from + 256);
-                        t[u].w = ld_dsmem_f32(from + 384);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (r0 + u * (THREADS / 32) >= c1) break;
-                    v[u][0] += t[u].x;
-                    v[u][1] += t[u].y;
-                    v[u][2] += t[u].z;
-                    v[u][3] += t[u].w;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int c = r0 + u * (THREADS / 32), row = n0 + c;
-                if (c >= c1 || o >= p.O) continue;
-                const int id = sh->ids[0][c];
-                if (id == -2) v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
-                if (patch && id >= 0) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (o + k * step < p.O)
-                            v[u][k] += lp_nonfinite_terms(p, id, row, o + k * step);
-                }
-                __nv_bfloat16 *dst = p.y + (long long)row * p.y_stride + o;
-                if (quads && o + 3 < p.O) {
-                    *reinterpret_cast<uint2 *>(dst) =
-                        make_uint2(pack_bf16x2(v[u][0], v[u][1]), pack_bf16x2(v[u][2], v[u][3]));
+                const float *from = (k == rank ? part + c * BM
+                                               : recv + ((k < rank ? k : k - 1) * most + c - c0) * BM) + o2;
+                if (quads) {
+                    const float4 t = *reinterpret_cast<const float4 *>(from);
+                    v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (o + k * step < p.O) dst[k * step] = __float2bfloat16(v[u][k]);
+                    for (int u = 0; u < 4; ++u) v[u] += from[u * 32];
                 }
+            }
+            if (o >= p.O) continue;
+            const int id = sh->ids[0][c], row = n0 + c;
+            if (id == -2) v[0] = v[1] = v[2] = v[3] = 0.f;
+            if (patch && id >= 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (o + u * step < p.O) v[u] += lp_nonfinite_terms(p, id, row, o + u * step);
+            }
+            __nv_bfloat16 *dst = p.y + (long long)row * p.y_stride + o;
+            if (quads && o + 3 < p.O) {
+                *reinterpret_cast<uint2 *>(dst) =
+                    make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (o + u * step < p.O) dst[u * step] = __float2bfloat16(v[u]);
             }
         }
     }
@@ -986,7 +985,9 @@ struct LpPlan {
 // measured, 130 GB/s to one) and of HBM (6 TB/s), and the latency of a load
 // (1.7 us) over the stages of its ring; an adapter block about 0.6 us. A tile
 // begins with about 3.5 us and ends with its stores (12 ns a row of x), or with
-// the sum over the cluster (20 ns a row).
+// the sum over the cluster (20 ns a row); and a CTA costs 20 ns, as it leaves
+// less of the GPU to lora_shrink (240 rows, 4096 -> 6144, rank 64: 96 CTAs 24.8
+// us, 144 CTAs 28.0 us).
 static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
     double least = 0;
     for (int cg = 1; cg <= 2; ++cg) {
@@ -1012,6 +1013,11 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
                 if (fit < 1) continue;
                 const int waves = (c.tiles + fit - 1) / fit;
                 if (c.CK > 1 && waves > 1) continue;
+                // the ring holds a partial tile and the other CTAs' parts of one
+                if (c.CK > 1 &&
+                    (size_t)lp::BM * 4 * (c.BN + (c.CK - 1) * ((c.BN + c.CK - 1) / c.CK)) >
+                        (size_t)c.stages * (lp::A_BYTES + c.BN / cg * 128))
+                    continue;
                 const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
                 double kb = c.BN * 1.05;
                 const double l2 = bytes * ctas / 19000, sm = bytes / 130;
@@ -1022,7 +1028,7 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
                 if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
                 const double t =
                     waves * ((c.kblocks * kb + blocks * 600.0) / c.CK + 3500) +
-                    (c.CK > 1 ? 1500 + 20.0 * c.BN : 12.0 * c.BN);
+                    (c.CK > 1 ? 1500 + 20.0 * c.BN : 12.0 * c.BN) + 20 * ctas;
                 if (least == 0 || t < least) {
                     least = t;
                     *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};
