@@ -148,7 +148,35 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.svf_version.argtypes = []
     lib.svf_version.restype = I
     _lib = lib
+    _load_fastcall(lib)
     return lib
+
+
+_fast = None
+
+
+def _load_fastcall(lib) -> None:
+    """The compiled checks of the short calls, if they were built for this torch."""
+    global _fast
+    path = os.path.join(_HERE, "_build", "_fastcall.so")
+    if not os.path.exists(path):
+        return
+    import importlib.machinery
+    import importlib.util
+
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_fastcall", path)
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_fastcall", loader))
+        loader.exec_module(mod)
+    except ImportError:
+        return
+    if mod.torch_version != torch.__version__.split("+")[0]:
+        return
+    mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in
+               (lib.svf_page_reserve, lib.svf_page_release, lib.svf_rope_kv_write,
+                lib.svf_lora_proj)))
+    _fast = mod
 
 
 def status_string(code: int) -> str:
@@ -679,9 +707,10 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Te
 
 # ---------------------------------------------------------------------------
 # The operators around the verify pass: pages, rotary K/V write, projections
-# with per-request adapters. Their calls are short, so a call's tensors are
-# checked in one expression; where it is false, each is checked by itself for
-# the message.
+# with per-request adapters. Their calls are short: the compiled checks
+# (fastcall.cpp) take a call that is all in order; the checks here take any
+# other, a call's tensors in one expression, and where that is false each by
+# itself for the message.
 # ---------------------------------------------------------------------------
 
 def _device_of(t, name: str) -> int:
@@ -790,6 +819,12 @@ def page_reserve(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor,
     row's position seq_lens + depth instead of seq_lens + i. Returns device
     tensors slots [rows], positions [rows], row_offsets [B + 1], status [B]."""
     lib = _lib or load_library()
+    if _fast is not None and outputs is not None:
+        rc = _fast.page_reserve(pool, page_table, seq_lens, new_lens, page_size, rows, depth,
+                                outputs, stream)
+        if rc is not None:
+            _check(rc, "svf_page_reserve")
+            return outputs
     dev, B, max_pages = _page_args(pool, page_table, seq_lens, "seq_lens", new_lens, "new_lens")
     free, i32 = pool["free"], torch.int32
     o = outputs if outputs is not None else {}
@@ -832,6 +867,11 @@ def page_release(pool: dict, page_table: torch.Tensor, old_lens: torch.Tensor,
     tokens back to the pool (after kv_commit: seq_lens + N and new_seq_lens;
     for finished requests keep 0). Returns n_released [B], status [B]."""
     lib = _lib or load_library()
+    if _fast is not None and outputs is not None:
+        rc = _fast.page_release(pool, page_table, old_lens, keep_lens, page_size, outputs, stream)
+        if rc is not None:
+            _check(rc, "svf_page_release")
+            return outputs
     dev, B, max_pages = _page_args(pool, page_table, old_lens, "old_lens", keep_lens, "keep_lens")
     free, i32 = pool["free"], torch.int32
     o = outputs if outputs is not None else {}
@@ -876,6 +916,12 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch
     Returns (q_out [T, Hq, D], status [T] int32). Rows that are left out keep
     what q_out held (a new q_out: undefined)."""
     lib = _lib or load_library()
+    if _fast is not None:
+        rc = _fast.rope_kv_write(q, k, v, rope, positions, slots, k_cache, v_cache, q_out,
+                                 interleaved, status, stream)
+        if rc is not None:
+            _check(rc, "svf_rope_kv_write")
+            return q_out, status
     dev = _device_of(q, "q")
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4 or rope.dim() != 2:
         raise SpecVerifyError("q and k must be [T, heads, D], the caches [pages, page_size, Hkv, "
@@ -938,6 +984,11 @@ def lora_proj(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, lora_
     (x [B, N, H] with ids [B]: one adapter per request); scales [adapters]
     float32. Returns (out [..., O] bfloat16, status [G] int32)."""
     lib = _lib or load_library()
+    if _fast is not None:
+        rc = _fast.lora_proj(x, weight, lora_a, lora_b, ids, scales, out, workspace, status, stream)
+        if rc is not None:
+            _check(rc, "svf_lora_proj")
+            return out, status
     dev = _device_of(x, "x")
     bf = torch.bfloat16
     if weight.dim() != 2 or lora_a.dim() != 3:

@@ -3,7 +3,9 @@
 Every .cu file under csrc/ compiles to an object in parallel; the objects link
 into _build/libspecverify.so with the CUDA runtime linked statically, so the
 library needs only the driver at run time and shares the process's primary
-context (and therefore torch's streams).
+context (and therefore torch's streams). fastcall.cpp, the binding's checks of
+its short calls, compiles beside them with g++ against torch's headers; without
+it (no headers, another compiler) the binding makes the same checks itself.
 """
 
 from __future__ import annotations
@@ -12,6 +14,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libspecverify.so")
+FAST = os.path.join(OUT, "_fastcall.so")
 SOURCES = ["mask.cu", "attn_simt.cu", "attn_tc.cu", "attn_sk.cu", "accept.cu", "accept_stream.cu",
            "accept_target_stream.cu",
            "accept_noalloc.cu", "accept_target.cu", "eagle2.cu",
@@ -46,8 +50,38 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _build_fastcall() -> None:
+    src = os.path.join(CSRC, "fastcall.cpp")
+    deps = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "specverify.h")))
+    if os.path.exists(FAST) and os.path.getmtime(FAST) >= deps:
+        return
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"],
+           os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    tmp = FAST + f".{os.getpid()}.tmp"
+    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           + [f"-I{p}" for p in inc] + [src, "-o", tmp, "-L" + os.path.join(root, "lib"),
+                                        "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+                                        "-lc10_cuda"])
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stderr if r.returncode != 0 else ""
+    except OSError as e:
+        why = str(e)
+    if why:
+        sys.stderr.write(f"fastcall.cpp was not built, its checks run in Python:\n{why[-2000:]}\n")
+        return
+    os.replace(tmp, FAST)
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+        _build_fastcall()
         return LIB
     os.makedirs(OUT, exist_ok=True)
     flags = _flags(verbose)
@@ -61,8 +95,10 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
         return obj, r.stderr
 
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 1)
-    with cf.ThreadPoolExecutor(jobs) as ex:
+    with cf.ThreadPoolExecutor(jobs + 1) as ex:
+        fast = ex.submit(_build_fastcall)
         results = list(ex.map(compile_one, SOURCES))
+        fast.result()
     if verbose:
         for _, err in results:
             sys.stderr.write(err)

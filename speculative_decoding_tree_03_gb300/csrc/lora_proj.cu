@@ -985,7 +985,7 @@ struct LpPlan {
 // measured, 130 GB/s to one) and of HBM (6 TB/s), and the latency of a load
 // (1.7 us) over the stages of its ring; an adapter block about 0.6 us. A tile
 // begins with about 3.5 us and ends with its stores (12 ns a row of x), or with
-// the sum over the cluster (20 ns a row); and a CTA costs 20 ns, as it leaves
+// the sum over the cluster (30 ns a row); and a CTA costs 20 ns, as it leaves
 // less of the GPU to lora_shrink (240 rows, 4096 -> 6144, rank 64: 96 CTAs 24.8
 // us, 144 CTAs 28.0 us).
 static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
@@ -1028,7 +1028,7 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
                 if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
                 const double t =
                     waves * ((c.kblocks * kb + blocks * 600.0) / c.CK + 3500) +
-                    (c.CK > 1 ? 1500 + 20.0 * c.BN : 12.0 * c.BN) + 20 * ctas;
+                    (c.CK > 1 ? 1500 + 30.0 * c.BN : 12.0 * c.BN) + 20 * ctas;
                 if (least == 0 || t < least) {
                     least = t;
                     *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};

@@ -1,0 +1,112 @@
+"""The compiled checks of the short calls: taken for calls that are all in
+order, with the results of the checks in Python, and left for all others."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from speculative_decoding_tree_03_gb300 import build as _b
+    _b.build()
+    import speculative_decoding_tree_03_gb300 as m
+    m.load_library()
+    return m
+
+
+def cases(sv):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    fresh = lambda: (sv.page_pool(40), torch.full((3, 8), -1, **i32))
+    lens, new = torch.tensor([0, 0, 0], **i32), torch.tensor([20, 1, 33], **i32)
+    out = lambda **kw: {k: torch.empty(n, **i32) for k, n in kw.items()}
+    res = dict(slots=60, positions=60, row_offsets=4, status=3)
+    depth = torch.arange(60, **i32)
+    qkv, rope = r(54, 6 * 64), torch.rand(100, 64, generator=g, device="cuda")
+    q, k, v = (t.unflatten(1, (-1, 64)) for t in qkv.split([256, 64, 64], 1))
+    slots, pos = torch.randperm(64, generator=g, device="cuda")[:54].int(), torch.arange(54, **i32)
+    x, w, a, b = r(6, 4, 128), r(100, 128), r(2, 8, 128), r(2, 100, 8)
+    ids, scales = torch.tensor([0, 1, -1, 1, 0, 0], **i32), torch.rand(2, device="cuda")
+    ws = torch.empty(sv.lora_proj_workspace_size(24, 8), dtype=torch.uint8, device="cuda")
+
+    def pages(stream=None, with_depth=False):
+        pool, table = fresh()
+        o, rel = out(**res), out(n_released=3, status=3)
+        sv.page_reserve(pool, table, lens, new, 16, 60, depth=depth if with_depth else None,
+                        outputs=o, stream=stream)
+        kept = table.clone()
+        sv.page_release(pool, table, new, torch.tensor([16, 0, 1], **i32), 16, outputs=rel,
+                        stream=stream)
+        return [*o.values(), kept, *rel.values(), table, pool["state"]]
+
+    def write(stream=None, interleaved=False):
+        kc, vc = torch.zeros(4, 16, 1, 64, device="cuda").bfloat16(), torch.zeros(4, 16, 1, 64, device="cuda").bfloat16()
+        qo, st = torch.empty(54, 4, 64, device="cuda").bfloat16(), torch.empty(54, **i32)
+        sv.rope_kv_write(q, k, v, rope, pos, slots, kc, vc, q_out=qo, interleaved=interleaved,
+                         status=st, stream=stream)
+        return [kc, vc, qo, st]
+
+    def proj(stream=None, scaled=True, flat=False):
+        xx = x.view(24, 128)[:, :] if flat else x
+        y, st = torch.empty(*xx.shape[:-1], 100, device="cuda").bfloat16(), torch.empty(6, **i32)
+        sv.lora_proj(xx, w, a, b, ids, scales=scales if scaled else None, out=y, workspace=ws,
+                     status=st, stream=stream)
+        return [y, st]
+
+    return [pages, lambda stream=None: pages(stream, True), write,
+            lambda stream=None: write(stream, True), proj,
+            lambda stream=None: proj(stream, False), lambda stream=None: proj(stream, True, True)]
+
+
+def test_the_same_results_with_and_without(sv, monkeypatch):
+    assert sv._fast is not None, "fastcall.cpp is built where the library is"
+    fns = cases(sv)
+    side = torch.cuda.Stream()
+    fast = [f() for f in fns]
+    torch.cuda.synchronize()
+    on_side = []
+    for f in fns:
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            on_side.append(f(stream=side))
+    torch.cuda.synchronize()
+    calls = []
+
+    class Spy:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, getattr(real, name)(*a))) or calls[-1][1]
+
+    real = sv._fast
+    monkeypatch.setattr(sv, "_fast", Spy())
+    for f in fns:
+        f()
+    assert len(calls) == 9 and all(rc == 0 for _, rc in calls)   # every call was taken
+    monkeypatch.setattr(sv, "_fast", None)
+    for f, a, b in zip(fns, fast, on_side):
+        slow = f()
+        torch.cuda.synchronize()
+        for x, y, z in zip(slow, a, b):
+            assert torch.equal(x, y) and torch.equal(x, z)
+
+
+def test_what_is_not_in_order_is_left_to_the_binding(sv):
+    f = sv._fast
+    i = torch.zeros(3, dtype=torch.int32, device="cuda")
+    pool = sv.page_pool(4)
+    table = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    o = dict(slots=i[:2].clone(), positions=i[:2].clone(), status=i.clone(),
+             row_offsets=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    good = [pool, table, i, i, 16, 2, None, o, None]
+    assert f.page_reserve(*good) == 0
+    for at, bad in ((0, {}), (0, {**pool, "state": i}), (0, None), (1, table.long()),
+                    (1, table.cpu()), (1, table[0]), (1, table.T), (1, 3), (2, i[:2]), (2, None),
+                    (3, i.float()), (4, -16), (4, 1 << 40), (4, 1.5), (5, 3), (6, i), (6, 5),
+                    (7, {}), (7, {**o, "status": i[:1]}), (7, None), (8, 7)):
+        assert f.page_reserve(*(good[:at] + [bad] + good[at + 1:])) is None, (at, bad)
+    assert f.page_reserve(*good[:5]) is None and f.page_reserve() is None
+    # errors of the library itself come back as its code
+    assert f.page_reserve(*(good[:4] + [0] + good[5:])) == sv.SVF_ERR_UNSUPPORTED
