@@ -982,10 +982,10 @@ struct LpPlan {
 // Tiles of one CTA or a pair, rows of x per tile and CTAs (pairs) per tile: the
 // least of a model of the call in ns. A block of K takes a CTA the longest of
 // its products (1900 MHz), its share of what the L2 hands to the SMs (19 TB/s
-// measured, 130 GB/s to one) and of HBM (6 TB/s), and the latency of a load
+// measured, 130 GB/s to one) and of HBM (7 TB/s), and the latency of a load
 // (1.7 us) over the stages of its ring; an adapter block about 0.6 us. A tile
 // begins with about 3.5 us and ends with its stores (12 ns a row of x), or with
-// the sum over the cluster (30 ns a row); and a CTA costs 20 ns, as it leaves
+// the sum over the cluster (30 ns a row); and a CTA costs 12 ns, as it leaves
 // less of the GPU to lora_shrink (240 rows, 4096 -> 6144, rank 64: 96 CTAs 24.8
 // us, 144 CTAs 28.0 us).
 static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
@@ -1021,14 +1021,14 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
                 const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
                 double kb = c.BN * 1.05;
                 const double l2 = bytes * ctas / 19000, sm = bytes / 130;
-                const double hbm = lp::A_BYTES * ctas / 6000 / c.n_tiles;
+                const double hbm = lp::A_BYTES * ctas / 7000 / c.n_tiles;
                 if (l2 > kb) kb = l2;
                 if (sm > kb) kb = sm;
                 if (hbm > kb) kb = hbm;
                 if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
                 const double t =
                     waves * ((c.kblocks * kb + blocks * 600.0) / c.CK + 3500) +
-                    (c.CK > 1 ? 1500 + 30.0 * c.BN : 12.0 * c.BN) + 20 * ctas;
+                    (c.CK > 1 ? 1500 + 30.0 * c.BN : 12.0 * c.BN) + 12 * ctas;
                 if (least == 0 || t < least) {
                     least = t;
                     *plan = {cg, c.BN, c.n_tiles, c.tiles, c.stages, c.CK, fit};
