@@ -14,6 +14,11 @@
 //     B_a would be NaN. Every B_a tile is looked over in shared memory before
 //     its products: non-finite elements are replaced by zero there, and their
 //     terms are added to the rows of a alone, in the epilogue.
+//   - B_a and t come by 16-byte asynchronous copies of the adapter warps, which
+//     place the chunks as the MMA's swizzle wants them, leave t's rows of other
+//     adapters zero, and bring a warp's first B_a before t is there. TMA boxes
+//     of 32-byte rows took 3.6 us from t's end to the first adapter's products
+//     (64 requests, 56 adapters of rank 16, 4096 -> 4096: 22.7 us, now 20.0).
 //   - The tensor-core work of an adapter is confined to the window of the tile
 //     that holds its rows (the MMA's N: steps of 16 rows, of 32 for a pair of
 //     CTAs), and a 64-column block carries as many adapters as fit: 4 of rank
@@ -29,14 +34,14 @@
 // would be what bounds it; the pair brings 32 KB each. CG = 1 serves few rows
 // (bound by the bytes of W).
 // Roles of a CTA (320 threads):
-//   warp 0      producer: TMA of W and x blocks, then of B_a and t blocks;
+//   warp 0      producer: TMA of W and x blocks; then it hands free stages on;
 //   warp 1      MMA issuer (of the pair's first CTA);
 //   warps 2-5   epilogue (tensor memory -> y);
 //   warps 6-9   adapters: warp 6 lists the tile's distinct adapters; each of
-//               the four takes the adapter blocks of every fourth stage: looks
-//               over their B_a and clears the rows of t that are not a's.
+//               the four fills the adapter blocks of every fourth stage and
+//               looks over their B_a.
 // The t columns come last, so the shared product runs while lora_shrink still
-// does (the launches overlap; only the producer waits for it, before t).
+// does (the launches overlap; only the adapter warps wait for it, before t).
 //
 // Few rows leave too few tiles for the SMs: CK CTAs (or pairs) of a cluster
 // then share a tile, each with an equal part of K and every CK-th adapter
@@ -46,15 +51,19 @@
 // 8192 -> 10240, 24 adapters of rank 16: the tensor cores, 200-206 us = 1.62 to
 // 1.67 PFLOP/s, 97 % of the measured sustained rate of a library product under
 // the power cap (341 us with one CTA per tile and lane-predicated issue). Few
-// rows: HBM and the call's own latency: one row, 4096 -> 6144: 16.1 us, of which
+// rows: HBM and the call's own latency: one row, 4096 -> 6144: 15.6 us, of which
 // W streams for 7 (50 MB at 7 TB/s), 3.3 pass from the first launch to this
-// kernel's start, 2.5 to the first product, 3.3 in the cluster's sum and exit.
-// Tried and dropped: adapter blocks spread among the last blocks of K (70B-shaped
-// batch 222 against 200 us: their checks and the products share shared memory's
-// bandwidth), a slot of their own for them (203 against 202), one polling lane
-// per warp (one row 19.2 against 18.3), two CTAs per SM (19.8 against 16.9),
-// B_a brought before t is there (24.1 against 24.3 for 64 requests, 28.1 against
-// 27.4 for the EAGLE-2 batch).
+// kernel's start, 2 to the first product, 3.3 in the cluster's sum and exit; 64
+// requests 20.0 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.7.
+// Tried and dropped: adapter blocks spread among the last blocks of K
+// (70B-shaped batch 222 against 200 us: their checks and the products share
+// shared memory's bandwidth), one polling lane per warp (one row 19.2
+// against 18.3), two CTAs per SM (19.8 against 16.9), a warp's next B_a on
+// its way before the last one is looked over (no gain in any shape), all
+// four adapter warps on each block where there are one or two (EAGLE-2 batch
+// 23.9 against 23.6), B_a brought to the L2 while W streams (128 rows, 100
+// adapters of rank 64: 142 against 129), 88 registers per thread (64
+// requests 22.2 against 19.9: the CTAs start later beside lora_shrink's).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -98,8 +107,8 @@ struct LpParams {
 // Shared memory behind the stage ring.
 struct LpShared {
     uint64_t full[lp::MAX_STAGES];   // a block of W and x has landed (in the pair's first CTA)
-    uint64_t bfull[lp::MAX_STAGES];  // a block of B_a has landed
-    uint64_t ext[lp::MAX_STAGES];    // ... is looked over, and t stands next to it (first CTA)
+    uint64_t ready[lp::MAX_STAGES];  // a stage is free for an adapter block
+    uint64_t ext[lp::MAX_STAGES];    // the block's B_a and t are there (first CTA: both CTAs')
     uint64_t empty[lp::MAX_STAGES];
     uint64_t recv;                   // the other CTAs' sums of this CTA's rows of y
     uint64_t acc_full[2], acc_empty[2], list_full[2], list_empty[2], ext_done[2];
@@ -112,7 +121,7 @@ struct LpShared {
     int hash_id[lp::HASH], hash_no[lp::HASH], span[lp::MAX_BN];
     uint32_t tmem;
     int committed;  // stages whose products were issued
-    uint32_t par_main, par_ext, any_main, any_ext;  // the producer's, at its end
+    uint32_t par_main, any_main;  // the producer's, at its end
     int abort;
 };
 
@@ -381,27 +390,77 @@ __device__ __forceinline__ void lp_clean(uint4 *at) {
     *at = make_uint4(wd[0], wd[1], wd[2], wd[3]);
 }
 
-// A landed adapter block of up to PACK adapters (list entries from e0 on), by
-// one warp: t's rows of other adapters become zero, non-finite elements of B_a
-// are looked for. True if there were any; they are zero then.
+// 16 bytes to shared memory, zeros unless ok (src is not read then).
+__device__ __forceinline__ void lp_copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+// Chunk c of row `row` of a tile with rows of 16 NCH bytes, swizzled over as many.
+template <int NCH>
+__device__ __forceinline__ uint32_t lp_chunk(uint32_t tile, int row, int c) {
+    const uint32_t at = tile + (uint32_t)(row * NCH + c) * 16u;
+    return at ^ ((at >> 7 & (uint32_t)(NCH - 1)) << 4);
+}
+
+// An adapter block: up to PACK adapters, entries from e0 on of list buf, columns
+// from 64 kx on.
+struct LpBlock {
+    int buf, e0, kx;
+    int m0, row0;    // the tile's first row of W (this CTA's) and of x
+    int half, slot;  // as in the kernel
+};
+
+// Copies the block's rows of t, hi and lo; zeros on rows of other adapters.
 template <int CG, int PACK>
-__device__ __forceinline__ bool lp_check_block(const LpShared *sh, int buf, int e0, int half,
-                                               int slot, uint8_t *tiles_b, uint8_t *hi, int lane) {
-    constexpr int ROW = 128 / PACK, NCH = ROW / 16;  // bytes and chunks of a row
-    const int ne = min(PACK, sh->n_list[buf] - e0);
-#pragma unroll
-    for (int e = 0; e < PACK; ++e) {
-        if (e >= ne) break;
-        const uint32_t w = sh->list[buf][e0 + e];
+__device__ __forceinline__ void lp_copy_t(const LpParams &p, const LpShared *sh, const LpBlock &b,
+                                          uint32_t hi, int lane) {
+    constexpr int NCH = 8 / PACK;  // 16-byte chunks of a row
+    const int ne = min(PACK, sh->n_list[b.buf] - b.e0);
+    const int c = lane % NCH;
+    const bool inside = b.kx * 8 + c < p.rank / 8;
+    for (int e = 0; e < ne; ++e, hi += (uint32_t)b.slot) {
+        const uint32_t w = sh->list[b.buf][b.e0 + e], lo = hi + (uint32_t)(b.slot / 2);
         // this CTA's rows of the window: all, or its half of them
-        const int rows = lp_rows(w) / CG;
-        const int *ids = sh->ids[buf] + lp_first(w) + half * rows;
-        uint4 *at = reinterpret_cast<uint4 *>(hi + e * slot);
-        const int lo = (rows == 16 ? 16 * ROW : slot / 2) / 16;
-        for (int u = lane; u < rows * NCH; u += 32)
-            if (ids[u / NCH] != lp_adapter(w))
-                at[u] = at[lo + u] = make_uint4(0, 0, 0, 0);
+        const int rows = lp_rows(w) / CG, first = lp_first(w) + b.half * rows;
+        for (int row = lane / NCH; row < rows; row += 32 / NCH) {
+            const bool ok = inside && sh->ids[b.buf][first + row] == lp_adapter(w);
+            const size_t at =
+                ok ? (size_t)(b.row0 + first + row) * p.rank + b.kx * lp::BK + c * 8 : 0;
+            lp_copy16(lp_chunk<NCH>(hi, row, c), p.t + at, ok);
+            lp_copy16(lp_chunk<NCH>(lo, row, c), p.t + (size_t)p.R * p.rank + at, ok);
+        }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Fills a stage with an adapter block, by one warp. True if B_a held an infinity
+// or NaN; they are replaced by zero.
+template <int CG, int PACK>
+__device__ __forceinline__ bool lp_load_block(const LpParams &p, const LpShared *sh,
+                                              const LpBlock &b, uint8_t *tiles_b, uint8_t *hi,
+                                              int lane) {
+    constexpr int NCH = 8 / PACK;
+    const int ne = min(PACK, sh->n_list[b.buf] - b.e0);
+    const int c = lane % NCH;
+    const bool inside = b.kx * 8 + c < p.rank / 8;
+    for (int e = 0; e < ne; ++e) {
+        const uint32_t tile = smem_u32(tiles_b) + (uint32_t)(e * lp::BM * NCH * 16);
+        const int id = lp_adapter(sh->list[b.buf][b.e0 + e]);
+        const __nv_bfloat16 *src = p.lora_b + ((size_t)id * p.O + b.m0) * (size_t)p.rank;
+#pragma unroll 8
+        for (int row = lane / NCH; row < lp::BM; row += 32 / NCH) {
+            const bool ok = inside && b.m0 + row < p.O;
+            lp_copy16(lp_chunk<NCH>(tile, row, c),
+                      src + (ok ? row * p.rank + b.kx * lp::BK + c * 8 : 0), ok);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    pdl_wait();  // t is complete
+    lp_copy_t<CG, PACK>(p, sh, b, smem_u32(hi), lane);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // B_a is there
+    __syncwarp();
     // 0 times an infinity or NaN is NaN, and stays in the sum
     uint4 *tiles = reinterpret_cast<uint4 *>(tiles_b) + lane;
     uint32_t seen[4] = {0, 0, 0, 0};
@@ -417,17 +476,18 @@ __device__ __forceinline__ bool lp_check_block(const LpShared *sh, int buf, int 
             add_zero_times(seen[3], v[u].w);
         }
     }
-    if (!__any_sync(0xffffffffu, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7fff7fffu) != 0))
-        return false;
-    for (int k = 0; k < ne * lp::BM * NCH; k += 32) lp_clean(tiles + k);
-    return true;
+    const bool bad =
+        __any_sync(0xffffffffu, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7fff7fffu) != 0);
+    if (bad)
+        for (int k = 0; k < ne * lp::BM * NCH; k += 32) lp_clean(tiles + k);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    return bad;
 }
 
 template <int CG>
 __global__ void __maxnreg__(80)
-    lora_proj_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
-                     const __grid_constant__ CUtensorMap tmb, const __grid_constant__ CUtensorMap tmt,
-                     const __grid_constant__ CUtensorMap tmt2, LpParams p) {
+    lora_proj_kernel(const __grid_constant__ CUtensorMap tmw,
+                     const __grid_constant__ CUtensorMap tmx, LpParams p) {
     using namespace lp;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -458,14 +518,18 @@ __global__ void __maxnreg__(80)
     const int row_bytes = 128 >> p.lpack, tile_bytes = BM * row_bytes;
     const int pack = 1 << p.lpack, deep = p.kchunks - 1;
     // A stage's x area is shared out among the block's adapters; each part
-    // holds the rows of t's hi, and from its middle on those of lo (16 rows:
-    // from behind the hi rows on, so that one box brings both).
+    // holds the rows of t's hi, and from its middle on those of lo.
     const int slot = b_bytes >> p.lpack;
 
-    if (tid == 0) {
+    const int rot = (int)((long long)first_tile * nkb / tile_step) % nkb;
+    // One CTA's first loads need no more than its own barriers, so they go out
+    // before tensor memory is there (one row, 4096 -> 6144: 15.9 against 16.2 us).
+    const int pre = CG == 1 ? min(S, nkb) : 0;
+
+    if (warp == 0 && lp_elect()) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->bfull[s], 1);
+            mbar_init(&sh->ready[s], 1);
             mbar_init(&sh->ext[s], CG);
             mbar_init(&sh->empty[s], 1);
         }
@@ -480,13 +544,20 @@ __global__ void __maxnreg__(80)
         sh->committed = 0;
         sh->abort = 0;
         mbar_fence_init();
+        if constexpr (CG == 1) {
+            const int m0 = first_tile / p.n_tiles * BM, n0 = first_tile % p.n_tiles * p.BN;
+            int kc = (kb0 + rot) * BK;
+            for (int s = 0; s < pre; ++s) {
+                mbar_arrive_expect_tx(&sh->full[s], (uint32_t)(A_BYTES + b_bytes));
+                tma_load_2d(sA + s * A_BYTES, &tmw, kc, m0, &sh->full[s]);
+                tma_load_2d(sB + s * b_bytes, &tmx, kc, n0, &sh->full[s]);
+                kc = kc + BK == (kb0 + nkb) * BK ? kb0 * BK : kc + BK;
+            }
+        }
     }
-    if (warp == 0 && lane == 0) {
+    if (CG == 2 && warp == 2 && lane == 0) {
         tma_prefetch_desc(&tmw);
         tma_prefetch_desc(&tmx);
-        tma_prefetch_desc(&tmb);
-        tma_prefetch_desc(&tmt);
-        tma_prefetch_desc(&tmt2);
     }
     if (warp == 1) lp_tmem_alloc<CG>(&sh->tmem, p.tmem_cols);
     tc_fence_before();
@@ -496,30 +567,30 @@ __global__ void __maxnreg__(80)
         cluster_arrive();
         cluster_wait();
     }
-    // Only t waits for the kernel before this one (in the producer): that
+    // Only t waits for the kernel before this one (in the adapter warps): that
     // kernel lets this one start after its own wait, so what this call reads
     // besides t was complete by then.
     if (tile_step >= p.tiles) pdl_launch_dependents();  // one tile each
     const uint32_t tmem = sh->tmem;
-    // A stage's full barrier counts its W and x blocks, its bfull barrier its
-    // B_a blocks; who waits for one keeps the parity of its next phase, one
-    // bit per stage.
+    // A stage's full barrier counts its W and x blocks, its ready and ext
+    // barriers its adapter blocks; who waits for one keeps the parity of its
+    // next phase, one bit per stage.
     uint32_t par_main = 0, par_ext = 0;
-    uint32_t any_main = 0, any_ext = 0;
+    uint32_t any_main = 0;
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lp_elect()) {
             bool ok = true;
-            int i = 0, s = 0;
-            bool waited = false;
-            uint32_t turn = 1;  // parity of the phase that frees stage s
-            const int rot = (int)((long long)first_tile * nkb / tile_step) % nkb;
+            int i = 0, s = pre == S ? 0 : pre, done = pre;
+            uint32_t turn = pre == S ? 0u : 1u;  // parity of the phase that frees stage s
+            par_main = any_main = (1u << pre) - 1u;
             for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
                 const int m0 = (tile / p.n_tiles * CG + half) * BM;
                 const int n0 = tile % p.n_tiles * p.BN + half * (p.BN / 2);
-                int kc = (kb0 + rot) * BK;  // tiles that start together start at different columns
-                for (int kb = 0; kb < nkb; ++kb) {
+                // tiles that start together start at different columns
+                int kc = (kb0 + (rot + done) % nkb) * BK;
+                for (int kb = done; kb < nkb; ++kb) {
                     if (!(ok = mbar_wait_for(&sh->empty[s], turn, abort_flag, p.wait_ns))) break;
                     if (half == 0)
                         mbar_arrive_expect_tx(&sh->full[s], (uint32_t)(CG * (A_BYTES + b_bytes)));
@@ -540,47 +611,16 @@ __global__ void __maxnreg__(80)
                     }
                 }
                 if (!ok) break;
+                done = 0;
                 const int buf = i & 1;
                 if (!(ok = mbar_wait_for(&sh->list_full[buf], (uint32_t)(i >> 1 & 1), abort_flag,
                                          p.wait_ns)))
                     break;
-                if (!waited) {
-                    pdl_wait();  // t is complete
-                    asm volatile("fence.proxy.async.global;" ::: "memory");
-                    waited = true;
-                }
                 const int n_list = sh->n_list[buf];
                 const int blocks = ((n_list + pack - 1) >> p.lpack) << deep;
-                const int row0 = tile % p.n_tiles * p.BN;
                 for (int x = rank; x < blocks; x += p.CK) {
-                    const int e0 = (x >> deep) << p.lpack, kx = x & deep;
-                    const int ne = min(pack, n_list - e0);
                     if (!(ok = mbar_wait_for(&sh->empty[s], turn, abort_flag, p.wait_ns))) break;
-                    int bytes = 0;
-                    for (int e = 0; e < ne; ++e)
-                        bytes += tile_bytes + 2 * lp_rows(sh->list[buf][e0 + e]) / CG * row_bytes;
-                    mbar_arrive_expect_tx(&sh->bfull[s], (uint32_t)bytes);
-                    for (int e = 0; e < ne; ++e) {
-                        const uint32_t w = sh->list[buf][e0 + e];
-                        tma_load_3d(sA + s * A_BYTES + e * tile_bytes, &tmb, kx * BK, m0,
-                                    lp_adapter(w), &sh->bfull[s]);
-                        // t of this CTA's rows of the window
-                        const int rows = lp_rows(w) / CG;
-                        const int r0 = row0 + lp_first(w) + half * rows;
-                        uint8_t *hi = sB + s * b_bytes + e * slot;
-                        if (rows == 16) {
-                            tma_load_3d(hi, &tmt2, kx * BK, r0, 0, &sh->bfull[s]);
-                        } else {
-                            for (int r = 0; r < rows; r += 16) {
-                                tma_load_3d(hi + r * row_bytes, &tmt, kx * BK, r0 + r, 0,
-                                            &sh->bfull[s]);
-                                tma_load_3d(hi + slot / 2 + r * row_bytes, &tmt, kx * BK, r0 + r,
-                                            1, &sh->bfull[s]);
-                            }
-                        }
-                    }
-                    par_ext ^= 1u << s;
-                    any_ext |= 1u << s;
+                    mbar_arrive(&sh->ready[s]);
                     if (++s == S) {
                         s = 0;
                         turn ^= 1u;
@@ -588,11 +628,9 @@ __global__ void __maxnreg__(80)
                 }
                 mbar_arrive(&sh->list_empty[buf]);
             }
-            if (!waited) pdl_wait();  // this grid ends after the one before it
+            pdl_wait();  // this grid ends after the one before it
             sh->par_main = par_main;
-            sh->par_ext = par_ext;
             sh->any_main = any_main;
-            sh->any_ext = any_ext;
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -649,10 +687,10 @@ __global__ void __maxnreg__(80)
                             const uint32_t w = sh->list[buf][e0 + e];
                             const uint32_t dw = d + (uint32_t)lp_first(w);
                             const uint32_t idw = idesc_bf16_f32(BM * CG, lp_rows(w), false, false);
-                            const uint64_t da = ext_a + (uint32_t)((s * A_BYTES + e * tile_bytes) >> 4);
+                            const uint64_t da =
+                                ext_a + (uint32_t)((s * A_BYTES + e * tile_bytes) >> 4);
                             const uint64_t hi = ext_t + (uint32_t)((s * b_bytes + e * slot) >> 4);
-                            const int lo_off = lp_rows(w) == 16 * CG ? 16 * row_bytes : slot / 2;
-                            const uint64_t lo = hi + (uint32_t)(lo_off >> 4);
+                            const uint64_t lo = hi + (uint32_t)(slot / 2 >> 4);
                             for (int k = 0; k < ksteps; ++k) {
                                 lp_mma<CG>(dw, da + 2 * k, hi + 2 * k, idw, 1u);
                                 lp_mma<CG>(dw, da + 2 * k, lo + 2 * k, idw, 1u);
@@ -775,6 +813,7 @@ __global__ void __maxnreg__(80)
         int s = 0, i = 0;
         for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
             const int n0 = tile % p.n_tiles * p.BN;
+            const int m0 = (tile / p.n_tiles * CG + half) * BM;
             const int buf = i & 1, ause = i >> 1;
             if (warp == 6) {
                 if (ause > 0 && !(ok = lp_wait(&sh->list_empty[buf], (uint32_t)((ause - 1) & 1),
@@ -790,14 +829,15 @@ __global__ void __maxnreg__(80)
             const int blocks = ((n_list + pack - 1) >> p.lpack) << deep;
             for (int x = rank; x < blocks; x += p.CK, s = s + 1 == S ? 0 : s + 1) {
                 if ((s & 3) != w) continue;
-                if (!(ok = lp_wait(&sh->bfull[s], par_ext >> s & 1u, abort_flag, p.wait_ns))) break;
+                if (!(ok = lp_wait(&sh->ready[s], par_ext >> s & 1u, abort_flag, p.wait_ns))) break;
                 par_ext ^= 1u << s;
-                const int e0 = (x >> deep) << p.lpack;
+                const int e0 = (x >> deep) << p.lpack, kx = x & deep;
                 uint8_t *tb = sA + s * A_BYTES, *hi = sB + s * b_bytes;
+                const LpBlock b = {buf, e0, kx, m0, n0, half, slot};
                 const bool bad =
-                    p.lpack == 2   ? lp_check_block<CG, 4>(sh, buf, e0, half, slot, tb, hi, lane)
-                    : p.lpack == 1 ? lp_check_block<CG, 2>(sh, buf, e0, half, slot, tb, hi, lane)
-                                   : lp_check_block<CG, 1>(sh, buf, e0, half, slot, tb, hi, lane);
+                    p.lpack == 2   ? lp_load_block<CG, 4>(p, sh, b, tb, hi, lane)
+                    : p.lpack == 1 ? lp_load_block<CG, 2>(p, sh, b, tb, hi, lane)
+                                   : lp_load_block<CG, 1>(p, sh, b, tb, hi, lane);
                 if (bad) sh->nonfinite[buf] = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -899,8 +939,6 @@ __global__ void __maxnreg__(80)
         for (int s = 0; s < S; ++s) {
             if (half == 0 && (sh->any_main >> s & 1u))
                 mbar_wait_for(&sh->full[s], (sh->par_main >> s & 1u) ^ 1u, &never, 20000000ull);
-            if (sh->any_ext >> s & 1u)
-                mbar_wait_for(&sh->bfull[s], (sh->par_ext >> s & 1u) ^ 1u, &never, 20000000ull);
             if (s < sh->committed)
                 mbar_wait_for(&sh->empty[s], (uint32_t)((sh->committed - 1 - s) / S & 1), &never,
                               20000000ull);
@@ -934,23 +972,18 @@ static PFN_cuTensorMapEncodeTiled_v12000 lp_encoder() {
     return fn;
 }
 
-// [planes, rows, cols] bf16 with the given strides (elements); boxes of
-// box_cols columns (32, 64 or 128 bytes, swizzled over as many) x box_rows
-// rows x box_planes planes. dims == 2: one plane.
-static bool lp_map(CUtensorMap *map, const void *base, int dims, long long planes, long long rows,
-                   long long cols, long long row_stride, long long plane_stride, int box_cols,
-                   int box_rows, int box_planes = 1) {
+// [rows, cols] bf16 with rows row_stride elements apart, in boxes of 64 columns
+// x box_rows rows.
+static bool lp_map(CUtensorMap *map, const void *base, long long rows, long long cols,
+                   long long row_stride, int box_rows) {
     auto enc = lp_encoder();
     if (!enc) return false;
-    cuuint64_t d[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, (cuuint64_t)plane_stride * 2};
-    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), d,
-               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-               : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                : CU_TENSOR_MAP_SWIZZLE_32B,
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_stride * 2};
+    cuuint32_t box[2] = {(cuuint32_t)lp::BK, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1096,22 +1129,16 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     p.y = static_cast<__nv_bfloat16 *>(a.y);
     p.y_stride = a.y_stride;
     p.status = a.status;
-    CUtensorMap tmw, tmx, tmb, tmt, tmt2;
-    if (!lp_map(&tmw, a.weight, 2, 1, a.O, a.H, a.H, 0, 64, lp::BM) ||
-        !lp_map(&tmx, a.x, 2, 1, a.R, a.H, a.x_stride, 0, 64, p.BN / cg) ||
-        !lp_map(&tmb, a.lora_b, 3, a.adapters, a.O, a.rank, a.rank, (long long)a.O * a.rank,
-                64 >> p.lpack, lp::BM) ||
-        !lp_map(&tmt, a.workspace, 3, 2, a.R, a.rank, a.rank, (long long)a.R * a.rank, 64 >> p.lpack,
-                16) ||
-        !lp_map(&tmt2, a.workspace, 3, 2, a.R, a.rank, a.rank, (long long)a.R * a.rank,
-                64 >> p.lpack, 16, 2))
+    CUtensorMap tmw, tmx;
+    if (!lp_map(&tmw, a.weight, a.O, a.H, a.H, lp::BM) ||
+        !lp_map(&tmx, a.x, a.R, a.H, a.x_stride, p.BN / cg))
         return SVF_ERR_LAUNCH;
     if (launch_lora_shrink(a, stream) != cudaSuccess) return SVF_ERR_LAUNCH;
     int clusters = p.tiles;
     if (p.CK == 1 && clusters > plan.resident) clusters = plan.resident;  // persistent
     const int cluster = cg * p.CK;
     if (launch_pdl(kern, dim3((unsigned)(clusters * cluster)), dim3(lp::THREADS), smem, stream,
-                   cluster > 1 ? (unsigned)cluster : 0u, tmw, tmx, tmb, tmt, tmt2, p) != cudaSuccess)
+                   cluster > 1 ? (unsigned)cluster : 0u, tmw, tmx, p) != cudaSuccess)
         return SVF_ERR_LAUNCH;
     return SVF_OK;
 }

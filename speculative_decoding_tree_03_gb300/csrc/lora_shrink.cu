@@ -20,8 +20,10 @@
 // in a fixed order. Rows of other adapters in the block are not stored, so an
 // infinity or NaN in one request's adapter or hidden state stays with it.
 //
-// The kernel is small (128 threads of 128 registers, two CTAs per SM), so that
-// the CTAs of the projection kernel start beside it: its first products need
+// The kernel is small (128 threads of 128 registers, two CTAs per SM; 96 where
+// ranks above 16 fill many CTAs: 128 rows of 100 adapters of rank 64, 8192 ->
+// 10240, took 134 us with 128 and deeper loads, 122 with 96), so that the CTAs
+// of the projection kernel start beside it: its first products need
 // no t, which is there (after 5 to 12 us) before their last. Alone it takes 5.5
 // us for one row, 7.5 us for 64 rows of 56 adapters of rank 16 (4096 columns).
 #include "common.cuh"
@@ -61,7 +63,7 @@ __device__ __forceinline__ uint4 ld16(const __nv_bfloat16 *p, bool ok) {
 // MT: 16-row tiles of x of a block; NT: 8-row tiles of A that a CTA takes
 // (rank in groups of 8 NT)
 template <int MT, int NT, int DEPTH>
-__global__ void __maxnreg__(128) lora_shrink_kernel(ShrinkArgs p) {
+__global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(ShrinkArgs p) {
     constexpr int ROWS = 16 * MT;
     __shared__ float s_acc[kShrinkWarps][ROWS][NT * 8];
     __shared__ int s_ids[32];
@@ -258,7 +260,7 @@ cudaError_t launch_lora_shrink(const LoraArgs &a, cudaStream_t stream) {
     p.per = a.rows_per_id;
     if (a.rank <= 8) return launch_ranked<1, 4, 4>(p, stream);
     if (a.rank <= 16) return launch_ranked<2, 4, 3>(p, stream);
-    return launch_ranked<4, 3, 2>(p, stream);
+    return launch_ranked<4, 2, 2>(p, stream);
 }
 
 }  // namespace svf
