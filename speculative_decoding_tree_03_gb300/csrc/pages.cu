@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kPageThreads = 256;
 constexpr int kReleaseThreads = 1024;
-constexpr int kLongRange = 256;  // pages of a sequence that a warp takes alone
+constexpr int kKept = 4;  // ids that a thread of a release keeps in registers
 
 // state[0] free pages; state[1] tickets and state[2] the largest served I_b of
 // the call in flight (both zero between calls).
@@ -173,6 +173,10 @@ __global__ void __launch_bounds__(kPageThreads) page_reserve_kernel(ReserveArgs 
     }
 }
 
+__device__ __forceinline__ void or_cluster(uint32_t at, unsigned bits) {
+    asm volatile("red.shared::cluster.or.b32 [%0], %1;" ::"r"(at), "r"(bits) : "memory");
+}
+
 struct ReleaseArgs {
     int32_t *table;
     const int32_t *old_lens, *keep_lens;
@@ -181,16 +185,36 @@ struct ReleaseArgs {
     int B, max_pages, ps, num_pages;
 };
 
-// One cluster of `ctas` CTAs: the sequences are checked (a warp to a short
-// range, a CTA to a long one), the cluster meets, and every CTA sums up how
-// many pages each sequence gives back. Rank k of all the pages, sequence by
-// sequence in table order, goes to free[F + total - 1 - k].
-// A cluster instead of two kernels (check, then give back) saves a launch; one
-// last CTA that gives back everybody's pages took 35 us for 16 thousand pages.
+// What sequence b gives back: n pages from entry `first` of its row on.
+struct Gift {
+    int first, n;
+    bool ok;
+};
+
+__device__ __forceinline__ Gift gift_of(const ReleaseArgs &a, int b) {
+    const int old = a.old_lens[b], keep = a.keep_lens[b];
+    Gift g;
+    g.ok = keep >= 0 && old >= keep && (long long)old <= (long long)a.max_pages * a.ps;
+    g.first = g.ok ? pages_of(keep, a.ps) : 0;
+    g.n = g.ok ? pages_of(old, a.ps) - g.first : 0;
+    return g;
+}
+
+// One cluster of `ctas` CTAs, or its first alone. Every CTA sums up by itself
+// how many pages each sequence gives back, so that the pages of the call have
+// ranks 0 .. total - 1, sequence by sequence in table order; thread t of all
+// takes the ranks t, t + threads, .. (their sequence by a search in the sums),
+// looks at the ids, and once nobody found a bad one puts rank k at
+// free[F + total - 1 - k]. So the chain is two reads, lengths and ids, whatever
+// the lengths are like (200 ragged prompts of 16 thousand pages, reserve and
+// release: 15.1 us; 20.7 with a warp to a sequence and long ones by whole CTAs
+// one after the other).
 __global__ void __launch_bounds__(kReleaseThreads) page_release_kernel(ReleaseArgs a, int ctas) {
     extern __shared__ int s_off[];  // [B + 1] the running sum of the pages
+    int *s_first = s_off + a.B + 1;  // [B]
+    unsigned *s_bad = reinterpret_cast<unsigned *>(s_first + a.B);  // a bit per sequence
     __shared__ int s_warp[kReleaseThreads / 32];
-    __shared__ int s_long[2];       // length of the list of long ranges, per phase
+    __shared__ int s_any;  // some bit of s_bad is set
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (!cluster_shape_is((uint32_t)ctas, 1u, 1u)) {
         pdl_wait();
@@ -201,125 +225,147 @@ __global__ void __launch_bounds__(kReleaseThreads) page_release_kernel(ReleaseAr
         return;
     }
     const int rank = blockIdx.x;
-    if (tid < 2) s_long[tid] = 0;
+    for (int i = tid; i < (a.B + 31) / 32; i += kReleaseThreads) s_bad[i] = 0;
+    if (tid == 0) s_any = 0;
+    if (ctas > 1) cluster_arrive();  // the others may set bits of s_bad
     pdl_wait();
     pdl_launch_dependents();
-    const int F = min(max(*(volatile int32_t *)a.state, 0), a.num_pages);
-    __syncthreads();
-    // s_off is the list of this CTA's long ranges until the sums need it
-    auto check = [&](int b, int at, int step, bool all) {
-        const int old = a.old_lens[b], keep = a.keep_lens[b];
-        int st = 0, n = 0;
-        if (keep < 0 || old < keep || (long long)old > (long long)a.max_pages * a.ps) {
-            st = SVF_DEV_BAD_LENGTH;
-        } else {
-            const int first = pages_of(keep, a.ps), end = pages_of(old, a.ps);
-            n = end - first;
-            if (!all && n > kLongRange) {
-                if (at == 0) s_off[atomicAdd(&s_long[0], 1)] = b;
-                return;
+    int F = rank == 0 ? *(volatile int32_t *)a.state : 0;
+    auto is_bad = [&](int b) { return (s_bad[b >> 5] >> (b & 31) & 1u) != 0; };
+    const int cap = a.num_pages + 1;
+    // the running sum of the pages of all sequences but the bad ones
+    auto scan = [&](bool checked) {
+        int carry = 0;
+        for (int i0 = 0; i0 < a.B; i0 += kReleaseThreads) {
+            const int i = i0 + tid;
+            int v = 0;
+            if (i < a.B) {
+                const Gift g = gift_of(a, i);
+                s_first[i] = g.first;
+                v = checked && is_bad(i) ? 0 : min(g.n, cap);
             }
-            const int32_t *row = a.table + (size_t)b * a.max_pages;
-            bool bad = false;
-            for (int i = first + at; i < end; i += 8 * step) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int p = i + u * step < end ? row[i + u * step] : 0;
-                    bad |= p < 0 || p >= a.num_pages;
-                }
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v = sat_add(v, u, cap);
             }
-            if (all ? __syncthreads_or(bad) : __any_sync(0xffffffffu, bad)) {
-                st = SVF_DEV_BAD_PAGE;
-                n = 0;
+            if (lane == 31) s_warp[warp] = v;
+            __syncthreads();
+            int w = s_warp[lane];  // 32 warps: every warp scans their sums
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, w, o);
+                if (lane >= o) w = sat_add(w, u, cap);
             }
+            const int below = __shfl_sync(0xffffffffu, w, warp - 1 < 0 ? 0 : warp - 1);
+            if (i < a.B) s_off[i + 1] = sat_add(sat_add(carry, warp > 0 ? below : 0, cap), v, cap);
+            carry = sat_add(carry, __shfl_sync(0xffffffffu, w, 31), cap);
+            __syncthreads();
         }
-        if (at == 0) {
-            a.n_released[b] = n;
-            a.status[b] = st;
+        if (tid == 0) s_off[0] = 0;
+        __syncthreads();
+        return carry;
+    };
+    auto owner = [&](int k) {  // the sequence of rank k < s_off[B]
+        int lo = 0, hi = a.B;  // s_off[lo] <= k < s_off[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_off[mid] <= k) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
+    auto entry = [&](int b, int j) {  // the j-th page that b gives back
+        return a.table + (size_t)b * a.max_pages + s_first[b] + j;
+    };
+    int total = scan(false);
+    if (ctas > 1) cluster_wait();
+    // Few pages are the first CTA's (64 trees of 31 nodes, reserve and release:
+    // 8.8 us, 9.1 with all CTAs).
+    const bool alone = ctas == 1 || total <= kKept * kReleaseThreads;
+    if (alone && rank > 0) return;
+    if (rank > 0) F = *(volatile int32_t *)a.state;
+    F = min(max(F, 0), a.num_pages);
+    const int threads = alone ? kReleaseThreads : ctas * kReleaseThreads;
+    const int me = rank * kReleaseThreads + tid;
+    auto mark = [&](int b) {  // in every CTA, once from each
+        if (is_bad(b) || (atomicOr(&s_bad[b >> 5], 1u << (b & 31)) >> (b & 31) & 1u)) return;
+        s_any = 1;
+        for (int c = 0; !alone && c < ctas; ++c) {
+            or_cluster(cluster_map(&s_bad[b >> 5], (uint32_t)c), 1u << (b & 31));
+            or_cluster(cluster_map(&s_any, (uint32_t)c), 1u);
         }
     };
-    const int warps = ctas * (kReleaseThreads / 32), my_warp = warp * ctas + rank;
-    for (int b = my_warp; b < a.B; b += warps) check(b, lane, 32, false);
-    __syncthreads();
-    for (int i = 0; i < s_long[0]; ++i) check(s_off[i], tid, kReleaseThreads, true);
-    if (ctas > 1) {
+    auto is_page = [&](int p) { return p >= 0 && p < a.num_pages; };
+    // a thread's first pages: the id, the sequence and the number in it
+    int id[kKept], seq[kKept], num[kKept];
+    const bool counted = total < cap, fits = counted && total <= kKept * threads;
+    if (counted) {
+#pragma unroll
+        for (int u = 0; u < kKept; ++u) {
+            const int k = me + u * threads;
+            seq[u] = -1;
+            if (k < total) {
+                seq[u] = owner(k);
+                num[u] = k - s_off[seq[u]];
+                id[u] = *entry(seq[u], num[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kKept; ++u)
+            if (seq[u] >= 0 && !is_page(id[u])) mark(seq[u]);
+        for (int k = me + kKept * threads; k < total; k += threads) {
+            const int b = owner(k);
+            if (!is_page(*entry(b, k - s_off[b]))) mark(b);
+        }
+    } else {  // more than the cache has: without the bad sequences it may be less
+        for (int b = me >> 5; b < a.B; b += threads >> 5) {
+            const Gift g = gift_of(a, b);
+            const int32_t *row = a.table + (size_t)b * a.max_pages + g.first;
+            bool bad = false;
+            for (int i = lane; i < g.n; i += 32) bad |= !is_page(row[i]);
+            if (__any_sync(0xffffffffu, bad) && lane == 0) mark(b);
+        }
+    }
+    if (alone) {
+        __syncthreads();
+    } else {
         cluster_arrive();
         cluster_wait();
-    } else {
-        __syncthreads();
     }
-    const int cap = a.num_pages + 1;
-    int carry = 0;
-    for (int i0 = 0; i0 < a.B; i0 += kReleaseThreads) {
-        const int i = i0 + tid;
-        int v = i < a.B ? min(__ldcg(a.n_released + i), cap) : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v = sat_add(v, u, cap);
+    const bool again = !counted || s_any != 0;
+    if (again) total = scan(true);
+    // more pages than the cache has: some were given back before; take none
+    const bool none = F + total > a.num_pages;
+    for (int b = me; b < a.B; b += threads) {
+        const Gift g = gift_of(a, b);
+        int st = g.ok ? 0 : SVF_DEV_BAD_LENGTH, n = g.n;
+        if (n > 0 && (none || is_bad(b))) {
+            st = SVF_DEV_BAD_PAGE;
+            n = 0;
         }
-        if (lane == 31) s_warp[warp] = v;
-        __syncthreads();
-        int w = s_warp[lane];  // 32 warps: every warp scans their sums
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w = sat_add(w, u, cap);
-        }
-        const int below = __shfl_sync(0xffffffffu, w, warp - 1 < 0 ? 0 : warp - 1);
-        if (i < a.B) s_off[i + 1] = sat_add(sat_add(carry, warp > 0 ? below : 0, cap), v, cap);
-        carry = sat_add(carry, __shfl_sync(0xffffffffu, w, 31), cap);
-        __syncthreads();
+        a.n_released[b] = n;
+        a.status[b] = st;
     }
-    if (tid == 0) s_off[0] = 0;
-    __syncthreads();
-    const int total = carry;
-    if (F + total > a.num_pages) {
-        // more pages than the cache has: some were given back before; take none
-        if (ctas > 1) {  // everybody has read n_released
-            cluster_arrive();
-            cluster_wait();
-        }
-        for (int i = rank * kReleaseThreads + tid; i < a.B; i += ctas * kReleaseThreads)
-            if (a.n_released[i] > 0) {
-                a.n_released[i] = 0;
-                a.status[i] = SVF_DEV_BAD_PAGE;
-            }
-        return;
-    }
+    if (none) return;
     int32_t *top = a.free_pages + (F + total - 1);
-    auto give = [&](int b, int at, int step) {
-        const int off = s_off[b], n = s_off[b + 1] - off;
-        int32_t *row = a.table + (size_t)b * a.max_pages + pages_of(a.keep_lens[b], a.ps);
-        for (int j0 = at; j0 < n; j0 += 8 * step) {
-            int p[8];
+    const bool kept = !again || fits;  // else the ranks are others now
+    if (kept) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (j0 + u * step < n) p[u] = row[j0 + u * step];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int j = j0 + u * step;
-                if (j >= n) break;
-                top[-(off + j)] = p[u];
-                row[j] = -1;
+        for (int u = 0; u < kKept; ++u)
+            if (seq[u] >= 0 && !is_bad(seq[u])) {
+                top[-(s_off[seq[u]] + num[u])] = id[u];
+                *entry(seq[u], num[u]) = -1;
             }
-        }
-    };
-    for (int b = my_warp; b < a.B; b += warps) {
-        const int n = s_off[b + 1] - s_off[b];
-        if (n > kLongRange) {
-            if (lane == 0) s_long[1] = 1;
-        } else if (n > 0) {
-            give(b, lane, 32);
-        }
     }
-    __syncthreads();
-    if (s_long[1])  // the same sequences' long ranges, by the whole CTA
-        for (int w = 0; w < kReleaseThreads / 32; ++w)
-            for (int b = w * ctas + rank; b < a.B; b += warps)
-                if (s_off[b + 1] - s_off[b] > kLongRange) give(b, tid, kReleaseThreads);
+    for (int k = me + (kept ? kKept * threads : 0); k < total; k += threads) {
+        const int b = owner(k);
+        int32_t *at = entry(b, k - s_off[b]);
+        top[-k] = *at;
+        *at = -1;
+    }
     // every CTA read the count before the cluster met
-    if (rank == 0 && tid == 0) a.state[0] = F + total;
+    if (me == 0) a.state[0] = F + total;
 }
 
 __global__ void __launch_bounds__(kPageThreads)
@@ -386,9 +432,15 @@ cudaError_t launch_page_release(const PageReleaseArgs &p, cudaStream_t stream) {
     a.ps = p.page_size;
     a.num_pages = p.num_pages;
     const int ctas = p.B == 1 ? 1 : 8;
-    return launch_pdl(page_release_kernel, dim3((unsigned)ctas), dim3(kReleaseThreads),
-                      (size_t)(p.B + 1) * sizeof(int), stream, ctas > 1 ? (unsigned)ctas : 0u, a,
-                      ctas);
+    const size_t smem = (size_t)(2 * p.B + 1 + (p.B + 31) / 32) * sizeof(int);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            page_release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (2 * kMaxPageSequences + 1 + kMaxPageSequences / 32) * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(page_release_kernel, dim3((unsigned)ctas), dim3(kReleaseThreads), smem, stream,
+                      ctas > 1 ? (unsigned)ctas : 0u, a, ctas);
 }
 
 }  // namespace svf

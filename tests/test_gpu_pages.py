@@ -245,6 +245,54 @@ def test_giving_back_twice_is_refused(sv):
                 dev(one.table), lens[:1], np.zeros(1, np.int32))
 
 
+# more pages than the threads of one CTA, or of the cluster, hold at once; the largest batch
+@pytest.mark.parametrize("B,max_pages,least", [(1, 9001, 9000), (3, 3001, 2990), (6, 12000, 9000),
+                                               (8192, 9, 0)])
+@pytest.mark.parametrize("bad", [0, 1, 2])
+def test_large_releases(sv, B, max_pages, least, bad):
+    """All pages good, one bad id in one sequence, bad ids all over two others."""
+    ps = 4
+    rng = np.random.default_rng(B + bad)
+    held = rng.integers(least, max_pages + 1, B)
+    lens = np.maximum(held * ps - rng.integers(0, ps, B), 0).astype(np.int32)
+    n = int(held.sum()) + 17
+    perm = rng.permutation(n).astype(np.int32)
+    table = np.full((B, max_pages), -5, np.int32)
+    at = 17
+    for b in range(B):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+    keep = np.minimum(rng.integers(0, 3 * ps, B), lens).astype(np.int32)
+    if bad == 1:
+        table[B // 2, held[B // 2] - 1] = n
+    elif bad == 2:
+        table[0, 3:held[0]] = -1
+        table[B - 1, 3:held[B - 1]] = -1
+    free = np.full(n, -9, np.int32)
+    free[:17] = perm[:17]
+    m = Model(table, free, 17, ps, n)
+    pool = {"free": dev(free), "state": dev(np.array([17, 0, 0, 0], np.int32))}
+    run_release(sv, m, pool, dev(table), lens, keep)
+
+
+def test_release_of_more_than_the_cache(sv):
+    """The ranges add up to more pages than there are: without the sequence that
+    holds a bad id the rest goes back, without that id nothing does."""
+    ps, mp, n = 2, 40, 50
+    for bad in (True, False):
+        table = np.tile(np.arange(mp, dtype=np.int32), (4, 1))
+        table[0] = 40 + np.arange(mp) % 10
+        if bad:
+            table[1, 39] = table[2, 0] = -1
+        lens = np.array([10, 80, 80, 60], np.int32)
+        keep = np.array([2, 0, 0, 3], np.int32)
+        free = np.full(n, -9, np.int32)
+        m = Model(table, free, 0, ps, n)
+        pool = {"free": dev(free), "state": dev(np.zeros(4, np.int32))}
+        run_release(sv, m, pool, dev(table), lens, keep)
+        assert (m.count > 0) == bad
+
+
 @pytest.mark.parametrize("n", [1, 255, 256, 100003])
 def test_pool_init(sv, n):
     pool = sv.page_pool(n)
