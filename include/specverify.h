@@ -582,7 +582,8 @@ int svf_spec_accept_lmhead(const void *hidden, const void *weight, const float *
  * in the range of one sequence only.
  *
  * Limits: B <= 8192, 1 <= page_size, num_pages * page_size and max_pages *
- * page_size below 2^31, 1 <= num_pages < 2^30, 0 <= rows < 2^30.
+ * page_size below 2^31, 1 <= num_pages < 2^30, 0 <= rows < 2^30 - 1. B = 0
+ * writes nothing.
  * ---------------------------------------------------------------------- */
 int svf_page_pool_init(int32_t *free_pages, int32_t *pool_state, int num_pages,
                        svf_stream_t stream);
@@ -662,7 +663,7 @@ int svf_rope_kv_write(const void *q, const void *k, const void *v, long long q_s
  *            undefined)
  * An infinity or NaN in a row of x or in an adapter reaches the rows that use
  * it and no others.
- * Limits: 1 <= R <= 2^17, R a multiple of rows_per_id >= 1; H <= 65536 a
+ * Limits: R <= 2^17 (R = 0 writes nothing), a multiple of rows_per_id >= 1; H <= 65536 a
  * multiple of 8; 1 <= O <= 2^20; rank <= 128 a multiple of 8; 1 <= adapters <=
  * 65536; x, weight, lora_a and lora_b 16-byte aligned, x_stride a multiple of
  * 8, x_stride >= H and y_stride >= O. y must not overlap an input.

@@ -15,6 +15,7 @@ without the built library, raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -757,11 +758,22 @@ def _call(fn, what: str, dev: int, stream, *args) -> None:
         _check(rc, what)
 
 
-def _outs(o: dict, dtype, like: torch.Tensor, dev: int, **shapes) -> None:
+def _on(stream, device):
+    """Where a call allocates for itself: memory of the stream that it runs on,
+    so that nothing on the current one uses it before or after the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _outs(o: dict, dtype, like: torch.Tensor, dev: int, stream, **shapes) -> None:
     """Allocate the outputs that ``o`` lacks, check the ones that it has."""
     for key, shape in shapes.items():
         if o.get(key) is None:
-            o[key] = torch.empty(shape, dtype=dtype, device=like.device)
+            with _on(stream, like.device):
+                o[key] = torch.empty(shape, dtype=dtype, device=like.device)
         else:
             _p(o[key], key, dtype, shape, dev)
 
@@ -771,8 +783,9 @@ def page_pool(num_pages: int, device="cuda", stream=None) -> dict:
     stack of page ids) and ``state`` [4] int32 (state[0] free pages)."""
     if num_pages < 1:
         raise SpecVerifyError("num_pages must be at least 1")
-    pool = {"free": torch.empty((num_pages,), dtype=torch.int32, device=device),
-            "state": torch.empty((4,), dtype=torch.int32, device=device)}
+    with _on(stream, device):
+        pool = {"free": torch.empty((num_pages,), dtype=torch.int32, device=device),
+                "state": torch.empty((4,), dtype=torch.int32, device=device)}
     free, state = pool["free"], pool["state"]
     _call(load_library().svf_page_pool_init, "svf_page_pool_init", _device_of(free, "device"),
           stream, free.data_ptr(), state.data_ptr(), num_pages)
@@ -844,8 +857,8 @@ def page_reserve(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor,
     if not fine:
         if rows < 0:
             raise SpecVerifyError("rows must not be negative")
-        _outs(o, i32, page_table, dev, slots=(rows,), positions=(rows,), row_offsets=(B + 1,),
-              status=(B,))
+        _outs(o, i32, page_table, dev, stream, slots=(rows,), positions=(rows,),
+              row_offsets=(B + 1,), status=(B,))
         slots, positions, offsets, status = (o["slots"], o["positions"], o["row_offsets"],
                                              o["status"])
     d = None
@@ -853,6 +866,12 @@ def page_reserve(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor,
         if depth.numel() != rows:
             raise SpecVerifyError("depth must hold one value per row")
         d = _p(depth, "depth", i32, depth.shape, dev)
+    if B == 0:  # all rows are behind the last sequence
+        with _on(stream, page_table.device):
+            slots.fill_(-1)
+            positions.zero_()
+            offsets.zero_()
+        return o
     _call(lib.svf_page_reserve, "svf_page_reserve", dev, stream, page_table.data_ptr(), max_pages,
           page_size, free.data_ptr(), pool["state"].data_ptr(), free.numel(), seq_lens.data_ptr(),
           new_lens.data_ptr(), B, rows, d, slots.data_ptr(), positions.data_ptr(),
@@ -884,7 +903,7 @@ def page_release(pool: dict, page_table: torch.Tensor, old_lens: torch.Tensor,
     except (KeyError, AttributeError):
         fine = False
     if not fine:
-        _outs(o, i32, page_table, dev, n_released=(B,), status=(B,))
+        _outs(o, i32, page_table, dev, stream, n_released=(B,), status=(B,))
         n_released, status = o["n_released"], o["status"]
     _call(lib.svf_page_release, "svf_page_release", dev, stream, page_table.data_ptr(), max_pages,
           page_size, free.data_ptr(), pool["state"].data_ptr(), free.numel(), old_lens.data_ptr(),
@@ -933,10 +952,12 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch
     max_pos, rot = rope.shape
     pages, ps = k_cache.shape[:2]
     cache, row = (pages, ps, Hkv, D), (T,)
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-    if status is None:
-        status = torch.empty(row, dtype=i32, device=q.device)
+    if q_out is None or status is None:
+        with _on(stream, q.device):
+            if q_out is None:
+                q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+            if status is None:
+                status = torch.empty(row, dtype=i32, device=q.device)
     try:
         fine = (rope.dtype is torch.float32 and rope.get_device() == dev and rope.is_contiguous()
                 and positions.dtype is i32 and positions.get_device() == dev
@@ -1008,8 +1029,16 @@ def lora_proj(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, lora_
     if R > 0 and (G < 1 or R % G):
         raise SpecVerifyError("ids must be [G] with G dividing the rows of x")
     shape = x.shape[:-1] + (O,)
-    if out is None:
-        out = torch.empty(shape, dtype=bf, device=x.device)
+    i32 = torch.int32
+    if out is None or status is None or workspace is None:
+        with _on(stream, x.device):
+            if out is None:
+                out = torch.empty(shape, dtype=bf, device=x.device)
+            if status is None:
+                status = torch.empty((G,), dtype=i32, device=x.device)
+            if workspace is None:
+                workspace = torch.empty((lora_proj_workspace_size(R, rank),), dtype=torch.uint8,
+                                        device=x.device)
     if out.dim() == 2 and out.shape[0] > 1 and not out.is_contiguous():
         if out.stride(1) != 1 or out.shape != shape or out.dtype is not bf \
                 or out.get_device() != dev:
@@ -1017,12 +1046,6 @@ def lora_proj(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, lora_
         op, os_ = out.data_ptr(), out.stride(0)
     else:
         op, os_ = _p(out, "out", bf, shape, dev), O
-    i32 = torch.int32
-    if status is None:
-        status = torch.empty((G,), dtype=i32, device=x.device)
-    if workspace is None:
-        workspace = torch.empty((lora_proj_workspace_size(R, rank),), dtype=torch.uint8,
-                                device=x.device)
     try:
         fine = (weight.dtype is bf and weight.get_device() == dev and weight.is_contiguous()
                 and lora_a.dtype is bf and lora_a.get_device() == dev
@@ -1047,6 +1070,10 @@ def lora_proj(x: torch.Tensor, weight: torch.Tensor, lora_a: torch.Tensor, lora_
             _p(scales, "scales", torch.float32, (adapters,), dev)
         _p(status, "status", i32, (G,), dev)
         raise SpecVerifyError("workspace must be a contiguous tensor on x's device")
+    if R == 0:
+        with _on(stream, x.device):
+            status.zero_()
+        return out, status
     _call(lib.svf_lora_proj, "svf_lora_proj", dev, stream, x.data_ptr(), xs, weight.data_ptr(),
           lora_a.data_ptr(), lora_b.data_ptr(), None if scales is None else scales.data_ptr(),
           ids.data_ptr(), R // G if G else 1, R, H, O, adapters, rank, op, os_,

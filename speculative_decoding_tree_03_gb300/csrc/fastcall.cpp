@@ -103,6 +103,16 @@ struct Args {
 
 bool fits(int64_t v) { return v <= INT_MAX; }
 
+// The C call, with the interpreter free: a launch waits where the stream is full.
+template <typename F>
+PyObject *call(F f) {
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = f();
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 // page_reserve(pool, page_table, seq_lens, new_lens, page_size, rows, depth, outputs, stream)
 PyObject *page_reserve(PyObject *const *a, Py_ssize_t n) {
     if (n != 9 || !g_reserve) Py_RETURN_NONE;
@@ -111,6 +121,7 @@ PyObject *page_reserve(PyObject *const *a, Py_ssize_t n) {
     if (!c.device_of(table) || table->dim() != 2 || !free || free->dim() != 1) Py_RETURN_NONE;
     const int64_t B = table->size(0), mp = table->size(1), pages = free->numel();
     const int ps = c.integer(a[4]), rows = c.integer(a[5]);
+    if (B < 1) Py_RETURN_NONE;  // the binding fills the outputs
     const at::Tensor *depth = tensor(a[6]);
     if ((a[6] != Py_None && (!depth || depth->numel() != rows)) || !fits(B) || !fits(mp) ||
         !fits(pages))
@@ -125,8 +136,10 @@ PyObject *page_reserve(PyObject *const *a, Py_ssize_t n) {
     if (!c.ok) Py_RETURN_NONE;
     const svf_stream_t s = c.stream(a[8]);
     if (!c.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(g_reserve(t, (int)mp, ps, f, st, (int)pages, l, w, (int)B, rows, d,
-                                     slots, pos, off, status, s));
+    return call([&] {
+        return g_reserve(t, (int)mp, ps, f, st, (int)pages, l, w, (int)B, rows, d, slots, pos, off,
+                         status, s);
+    });
 }
 
 // page_release(pool, page_table, old_lens, keep_lens, page_size, outputs, stream)
@@ -145,8 +158,9 @@ PyObject *page_release(PyObject *const *a, Py_ssize_t n) {
     if (!c.ok) Py_RETURN_NONE;
     const svf_stream_t s = c.stream(a[6]);
     if (!c.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(
-        g_release(t, (int)mp, ps, f, st, (int)pages, o, k, (int)B, nr, status, s));
+    return call([&] {
+        return g_release(t, (int)mp, ps, f, st, (int)pages, o, k, (int)B, nr, status, s);
+    });
 }
 
 // rope_kv_write(q, k, v, rope, positions, slots, k_cache, v_cache, q_out, interleaved, status,
@@ -177,11 +191,12 @@ PyObject *rope_kv_write(PyObject *const *a, Py_ssize_t n) {
     if (!c.ok) Py_RETURN_NONE;
     const svf_stream_t s = c.stream(a[11]);
     if (!c.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(g_rope(q->data_ptr(), k->data_ptr(), v->data_ptr(), qs, ks, vs, (int)T,
-                                  (int)Hq, (int)Hkv, (int)D,
-                                  type == at::kFloat ? SVF_F32 : SVF_BF16, r, (int)rot,
-                                  (int)max_pos, a[9] == Py_True, pos, slots, out, kp, vp,
-                                  (int)(pages * ps), status, s));
+    const void *qp = q->data_ptr(), *kin = k->data_ptr(), *vin = v->data_ptr();
+    return call([&] {
+        return g_rope(qp, kin, vin, qs, ks, vs, (int)T, (int)Hq, (int)Hkv, (int)D,
+                      type == at::kFloat ? SVF_F32 : SVF_BF16, r, (int)rot, (int)max_pos,
+                      a[9] == Py_True, pos, slots, out, kp, vp, (int)(pages * ps), status, s);
+    });
 }
 
 // lora_proj(x, weight, lora_a, lora_b, ids, scales, out, workspace, status, stream)
@@ -223,9 +238,13 @@ PyObject *lora_proj(PyObject *const *a, Py_ssize_t n) {
     if (!c.ok) Py_RETURN_NONE;
     const svf_stream_t s = c.stream(a[9]);
     if (!c.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(g_lora(x->data_ptr(), xs, wp, ap, bp, sp, ip, (int)(R / G), (int)R,
-                                  (int)H, (int)O, (int)A, (int)rank, out->data_ptr(), os, wsp,
-                                  (size_t)ws->nbytes(), status, s));
+    const void *xp = x->data_ptr();
+    void *op = out->data_ptr();
+    const size_t bytes = ws->nbytes();
+    return call([&] {
+        return g_lora(xp, xs, wp, ap, bp, sp, ip, (int)(R / G), (int)R, (int)H, (int)O, (int)A,
+                      (int)rank, op, os, wsp, bytes, status, s);
+    });
 }
 
 // No C++ exception leaves a function (a tensor without storage throws).

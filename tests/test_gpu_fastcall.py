@@ -110,3 +110,57 @@ def test_what_is_not_in_order_is_left_to_the_binding(sv):
     assert f.page_reserve(*good[:5]) is None and f.page_reserve() is None
     # errors of the library itself come back as its code
     assert f.page_reserve(*(good[:4] + [0] + good[5:])) == sv.SVF_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_what_a_call_allocates_belongs_to_its_stream(sv, monkeypatch, fast):
+    """A workspace that the call allocates is not handed out on the current
+    stream while the call's own stream still works with it."""
+    if not fast:
+        monkeypatch.setattr(sv, "_fast", None)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    x, w, a, b = r(64, 512), r(256, 512), r(3, 16, 512), r(3, 256, 16)
+    ids = torch.arange(64, device="cuda", dtype=torch.int32) % 3
+    want, _ = sv.lora_proj(x, w, a, b, ids)
+    side, need = torch.cuda.Stream(), sv.lora_proj_workspace_size(64, 16)
+    outs = [torch.empty_like(want) for _ in range(50)]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)   # about 10 ms, in which the calls queue up
+    for y in outs:
+        sv.lora_proj(x, w, a, b, ids, out=y, stream=side)
+    new = sv.lora_proj(x, w, a, b, ids, stream=side)[0]
+    mine = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(2000):
+        for m in mine:
+            m.fill_(255)
+    torch.cuda.synchronize()
+    for y in outs + [new]:
+        assert torch.equal(y, want)
+    pool = sv.page_pool(20, stream=side)
+    side.synchronize()
+    assert pool["state"].tolist() == [20, 0, 0, 0]
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_no_sequences_and_no_rows(sv, monkeypatch, fast):
+    """Calls without sequences or rows leave their outputs as documented."""
+    if not fast:
+        monkeypatch.setattr(sv, "_fast", None)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool, none = sv.page_pool(4), torch.empty(0, **i32)
+    o = {k: torch.full((n,), 77, **i32) for k, n in (("slots", 5), ("positions", 5),
+                                                     ("row_offsets", 1), ("status", 0))}
+    for given in (o, None):
+        got = sv.page_reserve(pool, torch.empty((0, 3), **i32), none, none, 16, 5, outputs=given)
+        assert got["slots"].tolist() == [-1] * 5 and got["positions"].tolist() == [0] * 5
+        assert got["row_offsets"].tolist() == [0]
+    assert sv.page_release(pool, torch.empty((0, 3), **i32), none, none, 16)["status"].numel() == 0
+    assert pool["state"].tolist() == [4, 0, 0, 0]
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    st = torch.full((4,), 77, **i32)
+    y, st = sv.lora_proj(torch.empty(4, 0, 64, **bf), torch.zeros(32, 64, **bf),
+                         torch.zeros(2, 8, 64, **bf), torch.zeros(2, 32, 8, **bf),
+                         torch.zeros(4, **i32), status=st)
+    assert y.shape == (4, 0, 32) and st.tolist() == [0] * 4
