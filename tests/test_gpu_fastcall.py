@@ -164,3 +164,39 @@ def test_no_sequences_and_no_rows(sv, monkeypatch, fast):
                          torch.zeros(2, 8, 64, **bf), torch.zeros(2, 32, 8, **bf),
                          torch.zeros(4, **i32), status=st)
     assert y.shape == (4, 0, 32) and st.tolist() == [0] * 4
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_two_threads_at_once(sv, monkeypatch, fast):
+    """Two host threads with streams, workspaces and shapes of their own."""
+    import threading
+
+    if not fast:
+        monkeypatch.setattr(sv, "_fast", None)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    jobs = []
+    for rows, out, rank in ((96, 264, 16), (5, 1000, 72)):
+        x, w, a, b = r(rows, 512), r(out, 512), r(3, rank, 512), r(3, out, rank)
+        ids = torch.arange(rows, device="cuda", dtype=torch.int32) % 4 - 1
+        jobs.append((x, w, a, b, ids, sv.lora_proj(x, w, a, b, ids)[0], torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+
+    def work(x, w, a, b, ids, want, stream, got):
+        with torch.cuda.stream(stream):
+            ws = torch.empty(sv.lora_proj_workspace_size(x.shape[0], a.shape[1]),
+                             dtype=torch.uint8, device="cuda")
+            st = torch.empty(ids.shape, dtype=torch.int32, device="cuda")
+            for _ in range(60):
+                y = torch.empty_like(want)
+                sv.lora_proj(x, w, a, b, ids, out=y, workspace=ws, status=st)
+                got.append(y)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for *_, want, _, got in jobs:
+        assert len(got) == 60 and all(torch.equal(y, want) for y in got)
