@@ -1016,7 +1016,9 @@ struct LpPlan {
 // least of a model of the call in ns. A block of K takes a CTA the longest of
 // its products (1900 MHz), its share of what the L2 hands to the SMs (19 TB/s
 // measured, 130 GB/s to one) and of HBM (7 TB/s), and the latency of a load
-// (1.7 us) over the stages of its ring; an adapter block about 0.6 us. A tile
+// (1.7 us) over the stages of its ring; an adapter block about 0.5 us, 0.8 in a
+// pair (128 rows, 100 adapters of rank 16, 4096 -> 6144: pairs 33.6 us, single
+// CTAs 29.4; 100 of rank 64, 8192 -> 10240: pairs 121, single CTAs 136). A tile
 // begins with about 3.5 us and ends with its stores (12 ns a row of x), or with
 // the sum over the cluster (30 ns a row); and a CTA costs 12 ns, as it leaves
 // less of the GPU to lora_shrink (240 rows, 4096 -> 6144, rank 64: 96 CTAs 24.8
@@ -1060,7 +1062,7 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
                 if (hbm > kb) kb = hbm;
                 if (1700.0 / c.stages > kb) kb = 1700.0 / c.stages;
                 const double t =
-                    waves * ((c.kblocks * kb + blocks * 600.0) / c.CK + 3500) +
+                    waves * ((c.kblocks * kb + blocks * (cg == 2 ? 800.0 : 500.0)) / c.CK + 3500) +
                     (c.CK > 1 ? 1500 + 30.0 * c.BN : 12.0 * c.BN) + 12 * ctas;
                 if (least == 0 || t < least) {
                     least = t;
