@@ -18,7 +18,7 @@
 //     place the chunks as the MMA's swizzle wants them, leave t's rows of other
 //     adapters zero, and bring a warp's first B_a before t is there. TMA boxes
 //     of 32-byte rows took 3.6 us from t's end to the first adapter's products
-//     (64 requests, 56 adapters of rank 16, 4096 -> 4096: 22.7 us, now 20.0).
+//     (64 requests, 56 adapters of rank 16, 4096 -> 4096: 22.7 us; 20.0 with the copies).
 //   - The tensor-core work of an adapter is confined to the window of the tile
 //     that holds its rows (the MMA's N: steps of 16 rows, of 32 for a pair of
 //     CTAs), and a 64-column block carries as many adapters as fit: 4 of rank
@@ -51,10 +51,10 @@
 // 8192 -> 10240, 24 adapters of rank 16: the tensor cores, 200-206 us = 1.62 to
 // 1.67 PFLOP/s, 97 % of the measured sustained rate of a library product under
 // the power cap (341 us with one CTA per tile and lane-predicated issue). Few
-// rows: HBM and the call's own latency: one row, 4096 -> 6144: 15.6 us, of which
+// rows: HBM and the call's own latency: one row, 4096 -> 6144: 15.2 us, of which
 // W streams for 7 (50 MB at 7 TB/s), 3.3 pass from the first launch to this
-// kernel's start, 2 to the first product, 3.3 in the cluster's sum and exit; 64
-// requests 20.0 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.7.
+// kernel's start, 2 to the first product, 3 in the cluster's sum and exit; 64
+// requests 19.6 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.7.
 // Tried and dropped: adapter blocks spread among the last blocks of K
 // (70B-shaped batch 222 against 200 us: their checks and the products share
 // shared memory's bandwidth), one polling lane per warp (one row 19.2
@@ -726,7 +726,9 @@ __global__ void __maxnreg__(80)
             const int o = m0 + q * 32 + lane;
             const bool patch = sh->nonfinite[buf] != 0;
             if (p.CK > 1) {
-                // partial sums into the (now idle) stage ring, [column][128] fp32
+                // The ring is idle: the others may send once all say so. Partial
+                // sums into it, [column][128] fp32.
+                cluster_arrive();
                 float *part = reinterpret_cast<float *>(smem) + q * 32 + lane;
                 for (int c = 0; c < p.BN; c += 32) {
                     uint32_t r[32];
@@ -804,6 +806,7 @@ __global__ void __maxnreg__(80)
                 mbar_arrive(&sh->list_empty[buf]);
             }
         }
+        if (p.CK > 1 && !ok) cluster_arrive();
     } else {
         // ------------------------------------------------------------ adapters
         // a stage's adapter blocks are always the same warp's, so that it sees
@@ -857,18 +860,19 @@ __global__ void __maxnreg__(80)
         }
     }
 
+    if (p.CK > 1 && (warp < 2 || warp > 5)) cluster_arrive();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (p.CK > 1) {
         // ------------------------------------------------------------ cluster sum
-        // Each CTA adds up an equal part of the tile's columns (rows of y)
-        // from the CK partial tiles of its rows of W, in order of K. The parts
-        // move by bulk copies from shared memory to shared memory, one per
-        // pair of CTAs, behind the receiver's own partial tile (128 rows of y
-        // of a tile of 256, two CTAs: loads from the other CTA's shared memory
-        // took 4.5 us, at 7 bytes a cycle).
-        cluster_arrive();
+        // Each CTA adds up an equal part of the tile's columns (rows of y) from
+        // the CK partial tiles of its rows of W, in order of K. Every CTA came
+        // to the barrier before it read its tensor memory (one after that cost
+        // 0.4 us more). The parts move by bulk copies from shared memory to
+        // shared memory, one per pair of CTAs, behind the receiver's own
+        // partial tile (128 rows of y of a tile of 256, two CTAs: loads from
+        // the other CTA's shared memory took 4.5 us, at 7 bytes a cycle).
         cluster_wait();
         const int m0 = (first_tile / p.n_tiles * CG + half) * BM;
         const int n0 = first_tile % p.n_tiles * p.BN;
