@@ -51,10 +51,10 @@
 // 8192 -> 10240, 24 adapters of rank 16: the tensor cores, 200-206 us = 1.62 to
 // 1.67 PFLOP/s, 97 % of the measured sustained rate of a library product under
 // the power cap (341 us with one CTA per tile and lane-predicated issue). Few
-// rows: HBM and the call's own latency: one row, 4096 -> 6144: 15.2 us, of which
+// rows: HBM and the call's own latency: one row, 4096 -> 6144: 15.0 us, of which
 // W streams for 7 (50 MB at 7 TB/s), 3.3 pass from the first launch to this
 // kernel's start, 2 to the first product, 3 in the cluster's sum and exit; 64
-// requests 19.6 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.7.
+// requests 18.5 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.6.
 // Tried and dropped: adapter blocks spread among the last blocks of K
 // (70B-shaped batch 222 against 200 us: their checks and the products share
 // shared memory's bandwidth), one polling lane per warp (one row 19.2
@@ -84,7 +84,7 @@ constexpr int A_BYTES = BM * BK * 2;
 constexpr int MAX_STAGES = 12;
 constexpr int THREADS = 320;
 constexpr int MAX_BN = 256;
-constexpr int MAX_LIST = 2 * MAX_BN;    // adapter windows of one row tile
+constexpr int MAX_LIST = 3 * MAX_BN / 2; // adapter windows of one row tile
 constexpr int HASH = 2 * MAX_BN;        // slots for the distinct adapters of a row tile
 constexpr int SMEM_BUDGET = 192 * 1024; // stage ring; leaves lora_shrink room beside it
 }  // namespace lp

@@ -14,18 +14,23 @@
 // registers. The tcgen05 path would have to stage both operands through shared
 // memory and tensor memory for N = rank columns.
 //
-// A CTA takes a block of 16 MT rows and one of the distinct adapters in it; its
-// 4 warps, and the KS CTAs of its cluster, share the 32-wide blocks of K. The
-// warps' sums meet in shared memory, the CTAs' over distributed shared memory,
-// in a fixed order. Rows of other adapters in the block are not stored, so an
-// infinity or NaN in one request's adapter or hidden state stays with it.
+// A CTA takes a block of 16 MT rows and one of the distinct adapters in it;
+// its 4 warps, and the KS CTAs of its cluster, share the 32-wide blocks of
+// K. The warps' sums meet in shared memory; every CTA sends each of the
+// others its share of them (asynchronous stores that count on the receiver's
+// barrier) and adds up the terms of its own share, both in a fixed order (64
+// requests with 56 adapters, the whole call: 18.5 us; 19.4 where they read
+// each other's sums between two barriers). Rows of other adapters in the
+// block are not stored, so an infinity or NaN in one request's adapter or
+// hidden state stays with it.
 //
-// The kernel is small (128 threads of 128 registers, two CTAs per SM; 96 where
-// ranks above 16 fill many CTAs: 128 rows of 100 adapters of rank 64, 8192 ->
-// 10240, took 134 us with 128 and deeper loads, 122 with 96), so that the CTAs
-// of the projection kernel start beside it: its first products need
-// no t, which is there (after 5 to 12 us) before their last. Alone it takes 5.5
-// us for one row, 7.5 us for 64 rows of 56 adapters of rank 16 (4096 columns).
+// The kernel is small (128 threads of 128 registers, two CTAs per SM; 96
+// where ranks above 16 fill many CTAs: 128 rows of 100 adapters of rank 64,
+// 8192 -> 10240, took 134 us with 128 and deeper loads, 122 with 96), so
+// that the CTAs of the projection kernel start beside it: its first products
+// need no t, which is there (after 5 to 12 us) before their last. Alone it
+// takes 5.5 us for one row, 7.5 us for 64 rows of 56 adapters of rank 16
+// (4096 columns).
 #include "common.cuh"
 #include "internal.h"
 #include "lora.h"
@@ -65,7 +70,12 @@ __device__ __forceinline__ uint4 ld16(const __nv_bfloat16 *p, bool ok) {
 template <int MT, int NT, int DEPTH>
 __global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(ShrinkArgs p) {
     constexpr int ROWS = 16 * MT;
-    __shared__ float s_acc[kShrinkWarps][ROWS][NT * 8];
+    constexpr int TILE = ROWS * NT * 8;
+    __shared__ __align__(16) float s_acc[kShrinkWarps][TILE];
+    // Every CTA of the cluster sums up an equal share of the tile: s_recv
+    // [KS][TILE / KS] gets the CTAs' terms of it.
+    __shared__ __align__(16) float s_recv[TILE];
+    __shared__ __align__(8) uint64_t s_full;
     __shared__ int s_ids[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ks = blockIdx.x % p.KS;
@@ -75,6 +85,15 @@ __global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(Sh
     const int slot = rest % p.slots, blk = rest / p.slots;
     const int row0 = blk * ROWS;
     const bool shaped = cluster_shape_is((uint32_t)p.KS, 1u, 1u);
+    const bool shared = shaped && p.KS > 1;
+    if (shared) {
+        if (tid == 0) {
+            mbar_init(&s_full, 1);
+            mbar_fence_init();
+            mbar_arrive_expect_tx(&s_full, TILE * 4);
+        }
+        cluster_arrive();  // the others may send
+    }
     pdl_wait();
     // The projection kernel starts when every CTA here has come to this call,
     // so after the wait above: what it reads besides t is complete by then.
@@ -100,6 +119,7 @@ __global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(Sh
     for (int i = 0; i < slot && todo; ++i) todo &= todo - 1;
     const int kchunks = (p.H + 31) / 32, kstep = p.KS * kShrinkWarps;
     const int g = lane >> 2, q = lane & 3;
+    bool sent = false, lost = false;
     const int n0 = ng * NT * 8;
     const int nt = min(NT, (p.rank - n0) / 8);
     while (todo) {  // the slot-th distinct adapter, then every slots-th after it
@@ -151,41 +171,39 @@ __global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(Sh
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float *d = &s_acc[warp][m * 16 + g][n * 8 + q * 2];
+                float *d = &s_acc[warp][(m * 16 + g) * NT * 8 + n * 8 + q * 2];
                 *reinterpret_cast<float2 *>(d) = make_float2(acc[m][n][0], acc[m][n][1]);
                 *reinterpret_cast<float2 *>(d + 8 * NT * 8) = make_float2(acc[m][n][2], acc[m][n][3]);
             }
         __syncthreads();
-        // the warps' sums, into the first one's place
-        for (int i = tid; i < ROWS * NT * 8; i += kShrinkThreads) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kShrinkWarps; ++w) v += (&s_acc[w][0][0])[i];
-            (&s_acc[0][0][0])[i] = v;
-        }
+        const int share = TILE / p.KS;  // KS is a power of two
         if (p.KS > 1) {
-            cluster_arrive();
+            // The host gives a cluster one adapter only, so nothing is sent twice.
             cluster_wait();
-        } else {
-            __syncthreads();
+            for (int i = 4 * tid; i < TILE; i += 4 * kShrinkThreads) {
+                float4 v = *reinterpret_cast<const float4 *>(&s_acc[0][i]);
+#pragma unroll
+                for (int w = 1; w < kShrinkWarps; ++w) {
+                    const float4 u = *reinterpret_cast<const float4 *>(&s_acc[w][i]);
+                    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+                }
+                const uint32_t to = (uint32_t)(i / share);
+                st_async_v4(cluster_map(&s_recv[ks * share + i % share], to), v,
+                            cluster_map(&s_full, to));
+            }
+            sent = true;
+            lost = !mbar_wait_cluster(&s_full, 0);
         }
         const float scale = p.scales ? p.scales[id] : 1.f;
-        const int share = ROWS * NT * 8 / p.KS;  // KS is a power of two
         for (int i = ks * share + tid; i < (ks + 1) * share; i += kShrinkThreads) {
             const int row = i / (NT * 8), j = i % (NT * 8);
             if (s_ids[row] != id || n0 + j >= p.rank) continue;
             float v = 0.f;
             if (p.KS > 1) {
-                float part[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    part[c] = c < p.KS
-                                  ? ld_dsmem_f32(cluster_map(&s_acc[0][0][0] + i, (uint32_t)c))
-                                  : 0.f;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) v += part[c];
+                for (int c = 0; c < p.KS; ++c) v += s_recv[c * share + i - ks * share];
             } else {
-                v = (&s_acc[0][0][0])[i];
+#pragma unroll
+                for (int w = 0; w < kShrinkWarps; ++w) v += s_acc[w][i];
             }
             v *= scale;
             const __nv_bfloat16 hi = __float2bfloat16(v);
@@ -195,12 +213,15 @@ __global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(Sh
             // an infinite hi has no remainder
             t[(size_t)p.R * p.rank] = __float2bfloat16(isfinite(h) ? v - h : 0.f);
         }
-        if (p.KS > 1) {
-            cluster_arrive();
-            cluster_wait();
-        } else {
-            __syncthreads();
-        }
+        if (p.KS > 1) break;
+        __syncthreads();
+    }
+    if (shared && !sent) cluster_wait();
+    if (shared && __syncthreads_or(lost)) {
+        // terms may still be on their way here: leave after those who send them
+        cluster_arrive();
+        cluster_wait();
+        if (tid == 0) atomicOr(p.status, SVF_DEV_TIMEOUT);
     }
 }
 
