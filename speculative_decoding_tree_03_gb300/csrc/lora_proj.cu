@@ -36,7 +36,8 @@
 // Roles of a CTA (320 threads):
 //   warp 0      producer: TMA of W and x blocks; then it hands free stages on;
 //   warp 1      MMA issuer (of the pair's first CTA);
-//   warps 2-5   epilogue (tensor memory -> y);
+//   warps 2-5   epilogue (tensor memory -> y; in pairs warps 6-9 take half of
+//               the last tile's);
 //   warps 6-9   adapters: warp 6 lists the tile's distinct adapters; each of
 //               the four fills the adapter blocks of every fourth stage and
 //               looks over their B_a.
@@ -54,7 +55,7 @@
 // rows: HBM and the call's own latency: one row, 4096 -> 6144: 15.0 us, of which
 // W streams for 7 (50 MB at 7 TB/s), 3.3 pass from the first launch to this
 // kernel's start, 2 to the first product, 3 in the cluster's sum and exit; 64
-// requests 18.5 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.6.
+// requests 18.5 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.0.
 // Tried and dropped: adapter blocks spread among the last blocks of K
 // (70B-shaped batch 222 against 200 us: their checks and the products share
 // shared memory's bandwidth), one polling lane per warp (one row 19.2
@@ -578,6 +579,90 @@ __global__ void __maxnreg__(80)
     uint32_t par_main = 0, par_ext = 0;
     uint32_t any_main = 0;
 
+    // Columns from .. to - 1 of a finished tile (rows of y): the work of warps 2
+    // to 5. In pairs, whose tiles are wide, warps 6 to 9 take the second half of
+    // a CTA's last tile; their adapter blocks are done by then (EAGLE-2 batch
+    // 23.1 us against 23.5; the 32 to 64 columns of single CTAs lost 1 to 4 %).
+    const int split = CG == 2 ? (p.BN / 32 + 1) / 2 * 32 : p.BN;
+    auto drain = [&](int buf, int m0, int n0, int from, int to) {
+        const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        const bool pairs = (p.y_stride & 1) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 3) == 0;
+        const int o = m0 + q * 32 + lane;
+        const bool patch = sh->nonfinite[buf] != 0;
+        if (p.CK > 1) {
+            // The ring is idle: the others may send once all say so. Partial
+            // sums into it, [column][128] fp32.
+            cluster_arrive();
+            float *part = reinterpret_cast<float *>(smem) + q * 32 + lane;
+            for (int c = from; c < to; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + lane_base + (uint32_t)(buf * p.BN + c), r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) part[(c + j) * BM] = __uint_as_float(r[j]);
+            }
+            fence_proxy_async_smem();  // the bulk copies below read them
+        } else {
+            const bool plain = !patch && !sh->bad_id[buf];
+            for (int c = from; c < to; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + lane_base + (uint32_t)(buf * p.BN + c), r);
+                tmem_wait_ld();
+                const int rows_left = p.R - (n0 + c);
+                if (plain && !pairs) {
+                    __nv_bfloat16 *at = p.y + (long long)(n0 + c) * p.y_stride + o;
+                    if (o < p.O) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (j < rows_left) *at = __float2bfloat16(__uint_as_float(r[j]));
+                            at += p.y_stride;
+                        }
+                    }
+                    continue;
+                }
+                if (!plain) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = r[j];
+                    if (o < p.O)
+                        lp_store_checked(p, sh->ids[buf] + c, v, patch, rows_left, n0 + c, o);
+                    continue;
+                }
+                // two lanes swap a value each, so that a lane stores two
+                // neighbours of one row: even lanes of row j, odd of j + 1
+                const int odd = lane & 1;
+                __nv_bfloat16 *dst =
+                    p.y + (long long)(n0 + c + odd) * p.y_stride + (o - odd);
+                const bool both = o - odd + 1 < p.O, one = o - odd < p.O;
+                if (rows_left >= 32 && m0 + q * 32 + 32 <= p.O) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]);
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                        *reinterpret_cast<uint32_t *>(dst) =
+                            odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                        dst += 2 * p.y_stride;
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]);
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                    const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                    if (j + odd < rows_left) {
+                        if (both)
+                            *reinterpret_cast<uint32_t *>(dst) = w;
+                        else if (one)
+                            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)w;
+                    }
+                    dst += 2 * p.y_stride;
+                }
+            }
+        }
+    };
+
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lp_elect()) {
@@ -709,9 +794,6 @@ __global__ void __maxnreg__(80)
         __syncwarp();
     } else if (warp < 6) {
         // ------------------------------------------------------------ epilogue
-        const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31
-        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        const bool pairs = (p.y_stride & 1) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 3) == 0;
         bool ok = true;
         int i = 0;
         for (int tile = first_tile; tile < p.tiles && ok; tile += tile_step, ++i) {
@@ -723,79 +805,7 @@ __global__ void __maxnreg__(80)
             if (!(ok = lp_wait(&sh->ext_done[buf], (uint32_t)(ause & 1), abort_flag, p.wait_ns)))
                 break;
             tc_fence_after();
-            const int o = m0 + q * 32 + lane;
-            const bool patch = sh->nonfinite[buf] != 0;
-            if (p.CK > 1) {
-                // The ring is idle: the others may send once all say so. Partial
-                // sums into it, [column][128] fp32.
-                cluster_arrive();
-                float *part = reinterpret_cast<float *>(smem) + q * 32 + lane;
-                for (int c = 0; c < p.BN; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(tmem + lane_base + (uint32_t)(buf * p.BN + c), r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) part[(c + j) * BM] = __uint_as_float(r[j]);
-                }
-                fence_proxy_async_smem();  // the bulk copies below read them
-            } else {
-                const bool plain = !patch && !sh->bad_id[buf];
-                for (int c = 0; c < p.BN; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(tmem + lane_base + (uint32_t)(buf * p.BN + c), r);
-                    tmem_wait_ld();
-                    const int rows_left = p.R - (n0 + c);
-                    if (plain && !pairs) {
-                        __nv_bfloat16 *to = p.y + (long long)(n0 + c) * p.y_stride + o;
-                        if (o < p.O) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                if (j < rows_left) *to = __float2bfloat16(__uint_as_float(r[j]));
-                                to += p.y_stride;
-                            }
-                        }
-                        continue;
-                    }
-                    if (!plain) {
-                        uint32_t v[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = r[j];
-                        if (o < p.O)
-                            lp_store_checked(p, sh->ids[buf] + c, v, patch, rows_left, n0 + c, o);
-                        continue;
-                    }
-                    // two lanes swap a value each, so that a lane stores two
-                    // neighbours of one row: even lanes of row j, odd of j + 1
-                    const int odd = lane & 1;
-                    __nv_bfloat16 *dst =
-                        p.y + (long long)(n0 + c + odd) * p.y_stride + (o - odd);
-                    const bool both = o - odd + 1 < p.O, one = o - odd < p.O;
-                    if (rows_left >= 32 && m0 + q * 32 + 32 <= p.O) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]);
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                            *reinterpret_cast<uint32_t *>(dst) =
-                                odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-                            dst += 2 * p.y_stride;
-                        }
-                        continue;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]);
-                        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                        const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-                        if (j + odd < rows_left) {
-                            if (both)
-                                *reinterpret_cast<uint32_t *>(dst) = w;
-                            else if (one)
-                                *reinterpret_cast<uint16_t *>(dst) = (uint16_t)w;
-                        }
-                        dst += 2 * p.y_stride;
-                    }
-                }
-            }
+            drain(buf, m0, n0, 0, tile + tile_step < p.tiles ? p.BN : split);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -857,10 +867,23 @@ __global__ void __maxnreg__(80)
                 mbar_arrive(&sh->list_empty[buf]);
             }
             __syncwarp();
+            if constexpr (CG == 2) {
+                if (tile + tile_step < p.tiles) continue;
+                // (A list of this tile says that the uses of its buffer before are
+                // over, so the parity is of this one.)
+                if (!(ok = lp_wait(&sh->acc_full[buf], (uint32_t)(ause & 1), abort_flag,
+                                   p.wait_ns)) ||
+                    !(ok = lp_wait(&sh->ext_done[buf], (uint32_t)(ause & 1), abort_flag,
+                                   p.wait_ns)))
+                    break;
+                tc_fence_after();
+                drain(buf, m0, n0, split, p.BN);
+            }
         }
+        if (CG == 2 && p.CK > 1 && !ok) cluster_arrive();
     }
 
-    if (p.CK > 1 && (warp < 2 || warp > 5)) cluster_arrive();
+    if (p.CK > 1 && (warp < 2 || (CG == 1 && warp > 5))) cluster_arrive();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
