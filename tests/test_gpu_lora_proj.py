@@ -258,3 +258,33 @@ def test_binding_refusals(sv):
                         lora_b=c["lora_b"][:, :, :4].contiguous())):
         with pytest.raises(sv.SpecVerifyError):
             sv.lora_proj(**{**c, **change})
+
+
+# pairs of CTAs: one tile each, one tile shared by two pairs, several tiles each; one CTA per
+# tile of 64 rows
+@pytest.mark.parametrize("G,H,O,rank", [(240, 2048, 6144, 16), (256, 4104, 4099, 24),
+                                        (520, 256, 40000, 40), (128, 1024, 6144, 16)])
+def test_bad_ids_and_non_finite_adapters_at_the_end_of_wide_tiles(sv, G, H, O, rank):
+    """The last rows of every 16 have a bad id, an adapter with an infinity, and
+    one with a NaN; all others are as without them."""
+    adapters = 60
+    ids = np.arange(G) * 7 % (adapters - 2)
+    want = case(G, G, H, O, rank, adapters, ids)
+    y, bound = reference(want)
+    ids = ids.copy()
+    ids[13::16], ids[14::16], ids[15::16] = adapters, adapters - 2, adapters - 1
+    c = dict(want, ids=torch.as_tensor(ids, dtype=torch.int32, device="cuda"))
+    c["lora_b"] = want["lora_b"].clone()
+    c["lora_b"][adapters - 2, 3::5, rank - 1] = float("inf")
+    c["lora_b"][adapters - 1, 3::5, 0] = float("nan")
+    got, status = sv.lora_proj(**c)
+    row = torch.arange(G, device="cuda") % 16
+    assert torch.equal(status, torch.where(row == 13, BAD_ADAPTER, 0).int())
+    plain = row < 13
+    assert bool(((got.double() - y).abs() <= bound)[plain].all())
+    assert bool((got[row == 13] == 0).all())
+    hit = torch.zeros(O, dtype=torch.bool, device="cuda")
+    hit[3::5] = True
+    for r in (14, 15):
+        assert not bool(got[row == r][:, hit].isfinite().any())
+        assert bool(got[row == r][:, ~hit].isfinite().all())
