@@ -435,12 +435,13 @@ cudaError_t launch_page_release(const PageReleaseArgs &p, cudaStream_t stream) {
     a.num_pages = p.num_pages;
     const int ctas = p.B == 1 ? 1 : 8;
     const size_t smem = (size_t)(2 * p.B + 1 + (p.B + 31) / 32) * sizeof(int);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            page_release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (2 * kMaxPageSequences + 1 + kMaxPageSequences / 32) * (int)sizeof(int));
-        if (e != cudaSuccess) return e;
-    }
+    // The kernel's static arrays count towards the default limit of 48 KB too
+    // (sums of 6032 to 6048 sequences fit it, but not together with them), and
+    // calls of several host threads agree on one limit.
+    const cudaError_t e = cudaFuncSetAttribute(
+        page_release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (2 * kMaxPageSequences + 1 + kMaxPageSequences / 32) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
     return launch_pdl(page_release_kernel, dim3((unsigned)ctas), dim3(kReleaseThreads), smem, stream,
                       ctas > 1 ? (unsigned)ctas : 0u, a, ctas);
 }
