@@ -672,12 +672,12 @@ cudaError_t launch_eagle2_finalize(int B, int C, const int32_t *parent, const in
                                    int32_t *out_token, double *out_value, int32_t *out_cid,
                                    int32_t *n_out, cudaStream_t stream) {
     const size_t smem = eagle2_finalize_smem(C);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(eagle2_finalize_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    // The kernel's static arrays count towards the default limit of 48 KB too
+    // (pools of 1115 to 1117 nodes fit it, but not together with them).
+    const cudaError_t e =
+        cudaFuncSetAttribute(eagle2_finalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)eagle2_finalize_smem(kEagle2MaxPool));
+    if (e != cudaSuccess) return e;
     return launch_pdl(eagle2_finalize_kernel, dim3((unsigned)B), dim3(e2::kFinThreads), smem,
                       stream, 0u, C, parent, depth, token, value, count, n_nodes, out_parent,
                       out_token, out_value, out_cid, n_out);
