@@ -12,8 +12,12 @@
 //     result's own when the adapter's part dominates.
 //   - A product of a zero of t with an infinity or NaN of another request's
 //     B_a would be NaN. Every B_a tile is looked over in shared memory before
-//     its products: non-finite elements are replaced by zero there, and their
-//     terms are added to the rows of a alone, in the epilogue.
+//     its products: non-finite elements are replaced by tiny numbers of their
+//     sign there, and their terms are added to the rows of a alone, in the
+//     epilogue. Not by zero: an infinite t times the tiny number is the
+//     infinity that it is times the element, where zero would make it NaN; on
+//     the rows of a the sum is infinite or NaN by the added terms whatever a
+//     tiny number leaves, on all others it meets a zero of t.
 //   - B_a and t come by 16-byte asynchronous copies of the adapter warps, which
 //     place the chunks as the MMA's swizzle wants them, leave t's rows of other
 //     adapters zero, and bring a warp's first B_a before t is there. TMA boxes
@@ -379,14 +383,15 @@ __device__ __forceinline__ void add_zero_times(uint32_t &acc, uint32_t v) {
     asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v), "r"(0u));
 }
 
-// Replaces the non-finite elements of 8 bf16 values by zero.
+// Replaces the non-finite elements of 8 bf16 values by numbers of their sign
+// between 2^-126 and 2^-125 (the largest exponent becomes the smallest).
 __device__ __forceinline__ void lp_clean(uint4 *at) {
     const uint4 b = *at;
     uint32_t wd[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        if ((wd[k] & 0x7f80u) == 0x7f80u) wd[k] &= 0xffff0000u;
-        if ((wd[k] & 0x7f800000u) == 0x7f800000u) wd[k] &= 0xffffu;
+        if ((wd[k] & 0x7f80u) == 0x7f80u) wd[k] &= ~0x7f00u;
+        if ((wd[k] & 0x7f800000u) == 0x7f800000u) wd[k] &= ~0x7f000000u;
     }
     *at = make_uint4(wd[0], wd[1], wd[2], wd[3]);
 }
@@ -437,7 +442,7 @@ __device__ __forceinline__ void lp_copy_t(const LpParams &p, const LpShared *sh,
 }
 
 // Fills a stage with an adapter block, by one warp. True if B_a held an infinity
-// or NaN; they are replaced by zero.
+// or NaN; they are replaced (lp_clean).
 template <int CG, int PACK>
 __device__ __forceinline__ bool lp_load_block(const LpParams &p, const LpShared *sh,
                                               const LpBlock &b, uint8_t *tiles_b, uint8_t *hi,
