@@ -711,6 +711,18 @@ int svf_debug_set_attn_splits(int splits);
  * ---------------------------------------------------------------------- */
 int svf_debug_set_attn_kernel(int which);
 
+/* ------------------------------------------------------------------------
+ * svf_debug_lora_plan -- test hook: how svf_lora_proj cuts a call of these
+ * sizes into tiles on the current device. plan [6] int32, host memory, out:
+ * CTAs that work on one tile of W's rows (1, or a pair); rows of x per tile;
+ * CTAs or pairs of a cluster that share a tile's K; tiles; stages of a CTA's
+ * ring; clusters that fit on the device at once. The pages have no
+ * counterpart; it lets tests check that their sizes reach the variants that
+ * they are for. Returns SVF_OK, or the code of a call of these sizes.
+ * ---------------------------------------------------------------------- */
+int svf_debug_lora_plan(int R, int rows_per_id, int H, int O, int adapters, int rank,
+                        int32_t *plan);
+
 /* Human-readable name of a host return code or of one device status bit. */
 const char *svf_status_string(int code);
 

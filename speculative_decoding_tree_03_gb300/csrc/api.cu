@@ -348,6 +348,13 @@ int svf_lora_proj(const void *x, long long x_stride, const void *weight, const v
     return launch_lora_proj(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int svf_debug_lora_plan(int R, int rows_per_id, int H, int O, int adapters, int rank,
+                        int32_t *plan) {
+    if (!plan || rows_per_id < 1 || R < 1 || R % rows_per_id != 0) return SVF_ERR_ARG;
+    if (!lora_proj_supported(R, H, O, adapters, rank)) return SVF_ERR_UNSUPPORTED;
+    return lora_proj_plan(R, rows_per_id, H, O, adapters, rank, plan) ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
 int svf_lm_head(const void *hidden, const void *weight, int R, int H, int V, float *logits,
                 int32_t *status, svf_stream_t stream) {
     if (R < 0 || H < 0 || V < 0) return SVF_ERR_ARG;

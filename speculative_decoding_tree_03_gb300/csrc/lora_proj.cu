@@ -1038,6 +1038,21 @@ static void lp_stages(LpParams *p, int cg) {
     if (p->stages > lp::MAX_STAGES) p->stages = lp::MAX_STAGES;
 }
 
+// What the kernel takes for granted of a way to cut a call into tiles: a ring
+// within its budget that holds, where CTAs share K, a partial tile and the
+// other CTAs' parts of one; adapter windows of half a tile; whole clusters.
+static bool lp_fits(const LpParams &p, int cg) {
+    if ((cg != 1 && cg != 2) || p.BN < 32 || p.BN > lp::MAX_BN || p.BN % 32 != 0 ||
+        p.BN / 2 < 16 * cg || p.CK < 1 || p.CK > p.kblocks || p.CK * cg > 8 || p.stages < 2 ||
+        p.stages > lp::MAX_STAGES)
+        return false;
+    const size_t ring = (size_t)p.stages * (lp::A_BYTES + p.BN / cg * 128);
+    const size_t sums = (size_t)lp::BM * 4 * (p.BN + (p.CK - 1) * ((p.BN + p.CK - 1) / p.CK));
+    return ring <= lp::SMEM_BUDGET && (p.CK == 1 || sums <= ring) &&
+           (long long)p.n_tiles * p.BN >= p.R &&
+           (long long)(p.tiles / p.n_tiles) * cg * lp::BM >= p.O;
+}
+
 // How a call is cut into tiles.
 struct LpPlan {
     int cg, BN, n_tiles, tiles, stages, CK;
@@ -1080,11 +1095,7 @@ static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
                 if (fit < 1) continue;
                 const int waves = (c.tiles + fit - 1) / fit;
                 if (c.CK > 1 && waves > 1) continue;
-                // the ring holds a partial tile and the other CTAs' parts of one
-                if (c.CK > 1 &&
-                    (size_t)lp::BM * 4 * (c.BN + (c.CK - 1) * ((c.BN + c.CK - 1) / c.CK)) >
-                        (size_t)c.stages * (lp::A_BYTES + c.BN / cg * 128))
-                    continue;
+                if (!lp_fits(c, cg)) continue;
                 const double ctas = (double)(c.tiles < fit ? c.tiles : fit) * c.CK * cg;
                 double kb = c.BN * 1.05;
                 const double l2 = bytes * ctas / 19000, sm = bytes / 130;
@@ -1125,29 +1136,47 @@ static bool lp_plan(const LpParams &p, int groups, LpPlan *plan) {
     return true;
 }
 
+// A call's sizes and the way that it is cut into tiles; false if there is none,
+// or one that the kernel does not take.
+static bool lp_shape(int R, int per, int H, int O, int adapters, int rank, LpParams *p,
+                     LpPlan *plan) {
+    p->R = R;
+    p->H = H;
+    p->O = O;
+    p->rank = rank;
+    p->adapters = adapters;
+    p->per = per;
+    p->kblocks = (H + lp::BK - 1) / lp::BK;
+    p->kchunks = (rank + lp::BK - 1) / lp::BK;
+    p->lpack = rank <= 16 ? 2 : rank <= 32 ? 1 : 0;
+    try {
+        if (!lp_plan(*p, R / per, plan)) return false;
+    } catch (...) {  // no host memory: no exception leaves a C entry
+        return false;
+    }
+    p->BN = plan->BN;
+    p->n_tiles = plan->n_tiles;
+    p->tiles = plan->tiles;
+    p->stages = plan->stages;
+    p->CK = plan->CK;
+    return lp_fits(*p, plan->cg) && plan->resident >= 1;
+}
+
+bool lora_proj_plan(int R, int per, int H, int O, int adapters, int rank, int32_t *plan) {
+    LpParams p;
+    LpPlan c;
+    if (!lp_shape(R, per, H, O, adapters, rank, &p, &c)) return false;
+    const int32_t v[6] = {c.cg, c.BN, c.CK, c.tiles, c.stages, c.resident};
+    for (int i = 0; i < 6; ++i) plan[i] = v[i];
+    return true;
+}
+
 int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     LpParams p;
-    p.R = a.R;
-    p.H = a.H;
-    p.O = a.O;
-    p.rank = a.rank;
-    p.adapters = a.adapters;
-    p.per = a.rows_per_id;
-    p.kblocks = (a.H + lp::BK - 1) / lp::BK;
-    p.kchunks = (a.rank + lp::BK - 1) / lp::BK;
-    p.lpack = a.rank <= 16 ? 2 : a.rank <= 32 ? 1 : 0;
     LpPlan plan;
-    try {
-        if (!lp_plan(p, a.R / a.rows_per_id, &plan)) return SVF_ERR_LAUNCH;
-    } catch (...) {  // no host memory: no exception leaves a C entry
+    if (!lp_shape(a.R, a.rows_per_id, a.H, a.O, a.adapters, a.rank, &p, &plan))
         return SVF_ERR_LAUNCH;
-    }
     const int cg = plan.cg;
-    p.BN = plan.BN;
-    p.n_tiles = plan.n_tiles;
-    p.tiles = plan.tiles;
-    p.stages = plan.stages;
-    p.CK = plan.CK;
     auto kern = cg == 2 ? lora_proj_kernel<2> : lora_proj_kernel<1>;
     const size_t smem = lp_smem(p, cg);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLpMaxSmem) !=

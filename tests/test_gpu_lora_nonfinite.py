@@ -11,10 +11,10 @@ from test_gpu_lora_proj import case, check, sv  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
-# one CTA per tile and K shared by a cluster; pairs; pairs that share K; several tiles each
-@pytest.mark.parametrize("R,H,O,rank", [(64, 512, 256, 16), (240, 2048, 6144, 64),
-                                        (256, 4104, 4099, 24), (600, 256, 40000, 40),
-                                        (33, 64, 40, 96)])
+# one CTA per tile; K shared by a cluster; pairs; pairs that share K; several tiles each
+@pytest.mark.parametrize("R,H,O,rank", [(64, 512, 256, 16), (64, 2048, 1024, 16),
+                                        (240, 2048, 6144, 64), (256, 4104, 4099, 24),
+                                        (600, 256, 40000, 40), (33, 64, 40, 96)])
 @pytest.mark.parametrize("value", [float("inf"), float("-inf")])
 def test_infinity_times_infinity(sv, value, R, H, O, rank):  # noqa: F811
     ids = np.arange(R) % 4 - 1          # every 16-row window holds every adapter
