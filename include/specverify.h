@@ -712,6 +712,16 @@ int svf_debug_set_attn_splits(int splits);
 int svf_debug_set_attn_kernel(int which);
 
 /* ------------------------------------------------------------------------
+ * svf_debug_set_lora_wait_ns -- test hook: the deadline of every internal wait
+ * of the kernels of svf_lora_proj, for later calls in this process, as
+ * svf_debug_set_attn_wait_ns for the attention. A kernel whose wait runs out
+ * waits (with limits of its own) for its copies and tensor-core operations in
+ * flight, releases its tensor memory and sets SVF_DEV_TIMEOUT in status[0]; y
+ * is undefined then. ns <= 0 restores the default of 2 s. Returns SVF_OK.
+ * ---------------------------------------------------------------------- */
+int svf_debug_set_lora_wait_ns(long long ns);
+
+/* ------------------------------------------------------------------------
  * svf_debug_lora_plan -- test hook: how svf_lora_proj cuts a call of these
  * sizes into tiles on the current device. plan [6] int32, host memory, out:
  * CTAs that work on one tile of W's rows (1, or a pair); rows of x per tile;

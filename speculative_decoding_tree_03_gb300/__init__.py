@@ -44,6 +44,7 @@ EXPORTED = [
     "svf_debug_set_attn_wait_ns",
     "svf_debug_set_attn_splits",
     "svf_debug_set_attn_kernel",
+    "svf_debug_set_lora_wait_ns",
     "svf_debug_lora_plan",
     "svf_spec_accept_lmhead",
     "svf_kv_commit",
@@ -131,6 +132,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.svf_debug_set_attn_splits.restype = I
     lib.svf_debug_set_attn_kernel.argtypes = [I]
     lib.svf_debug_set_attn_kernel.restype = I
+    lib.svf_debug_set_lora_wait_ns.argtypes = [ctypes.c_longlong]
+    lib.svf_debug_set_lora_wait_ns.restype = I
     lib.svf_debug_lora_plan.argtypes = [I, I, I, I, I, I, P]
     lib.svf_debug_lora_plan.restype = I
     L = ctypes.c_longlong

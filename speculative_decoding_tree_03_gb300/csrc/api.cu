@@ -348,6 +348,11 @@ int svf_lora_proj(const void *x, long long x_stride, const void *weight, const v
     return launch_lora_proj(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int svf_debug_set_lora_wait_ns(long long ns) {
+    lora_proj_set_wait_ns(ns);
+    return SVF_OK;
+}
+
 int svf_debug_lora_plan(int R, int rows_per_id, int H, int O, int adapters, int rank,
                         int32_t *plan) {
     if (!plan || rows_per_id < 1 || R < 1 || R % rows_per_id != 0) return SVF_ERR_ARG;

@@ -128,15 +128,31 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
     return ok != 0;
 }
 
+__device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait for a phase completed by other CTAs of the cluster; false after
-// the deadline.
+// the deadline. As above, deadlines under 1 ms poll without blocking.
 __device__ __forceinline__ bool mbar_wait_cluster_for(uint64_t *bar, uint32_t parity,
                                                       unsigned long long deadline_ns) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const bool quick = deadline_ns < 1000000ull;
+    if (quick ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity))
+        return true;
     const unsigned long long t0 = globaltimer_ns();
+    const uint32_t every = quick ? 0u : 63u;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((it & 63u) == 0 && globaltimer_ns() - t0 > deadline_ns) return false;
+        if (quick ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity))
+            return true;
+        if ((it & every) == 0 && globaltimer_ns() - t0 > deadline_ns) return false;
     }
 }
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {

@@ -214,6 +214,9 @@ int launch_lm_head(const void *hidden, const void *weight, int R, int H, int V, 
 struct LoraArgs;
 bool lora_proj_supported(int R, int H, int O, int adapters, int rank);
 int launch_lora_proj(const LoraArgs &a, cudaStream_t stream);
+// Test hook: the deadline of both its kernels' waits (ns; 0 or less restores
+// the default of 2 s).
+void lora_proj_set_wait_ns(long long ns);
 // Test hook: the tile plan of a call (six numbers, specverify.h); false if the
 // shape has none on this device.
 bool lora_proj_plan(int R, int per, int H, int O, int adapters, int rank, int32_t *plan);

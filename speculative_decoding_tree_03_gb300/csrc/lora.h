@@ -22,6 +22,7 @@ struct LoraArgs {
 };
 
 // t = scale * x A^T of every row's own adapter, and the status words (lora_shrink.cu).
-cudaError_t launch_lora_shrink(const LoraArgs &a, cudaStream_t stream);
+// wait_ns: the deadline of its wait.
+cudaError_t launch_lora_shrink(const LoraArgs &a, unsigned long long wait_ns, cudaStream_t stream);
 
 }  // namespace svf

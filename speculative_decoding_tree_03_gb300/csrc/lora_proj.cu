@@ -72,6 +72,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -148,11 +149,15 @@ __device__ __forceinline__ bool lp_wait(uint64_t *bar, uint32_t parity, volatile
 // A thread's wait for a barrier that threads of another CTA arrive on.
 __device__ __forceinline__ bool lp_wait_cluster(uint64_t *bar, uint32_t parity,
                                                 volatile int *abort, unsigned long long ns) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const bool quick = ns < 1000000ull;  // as in mbar_wait_for
+    if (quick ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity))
+        return true;
     const unsigned long long t0 = globaltimer_ns();
+    const uint32_t every = quick ? 0u : 63u;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((it & 63u) == 0) {
+        if (quick ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity))
+            return true;
+        if ((it & every) == 0) {
             if (*abort) return false;
             if (globaltimer_ns() - t0 > ns) {
                 *abort = 1;
@@ -960,12 +965,14 @@ __global__ void __maxnreg__(80)
             }
         }
     }
-    // Leave only when every load that this CTA issued has landed and every
-    // commit that frees one of its stages has arrived. A tile that was
-    // finished implies both (its products are done, in both CTAs of a pair);
-    // after a wait that gave up the barriers are waited for with a limit, and
-    // a pair, whose loads count on the first CTA's barriers, leaves 20 ms for
-    // them to land.
+    // Leave only when every load that this CTA issued has landed, every commit
+    // that frees one of its stages has arrived, and the others' partial sums,
+    // which every CTA sends whatever became of them, are here. A tile that was
+    // finished implies all three (its products are done, in both CTAs of a
+    // pair); after a wait that gave up the barriers are waited for with a
+    // limit, and 20 ms are left for what counts elsewhere: the loads of a
+    // pair's second CTA (on the first one's barriers) and the last commit (on
+    // acc_full). No CTA of a cluster leaves before the others have done this.
     if (*abort_flag && warp == 0 && lane == 0) {
         volatile int never = 0;
         for (int s = 0; s < S; ++s) {
@@ -975,8 +982,9 @@ __global__ void __maxnreg__(80)
                 mbar_wait_for(&sh->empty[s], (uint32_t)((sh->committed - 1 - s) / S & 1), &never,
                               20000000ull);
         }
+        if (p.CK > 1) mbar_wait_for(&sh->recv, 0, &never, 20000000ull);
         const unsigned long long t0 = globaltimer_ns();
-        while (CG == 2 && globaltimer_ns() - t0 < 20000000ull) {
+        while (globaltimer_ns() - t0 < 20000000ull) {
         }
     }
     __syncthreads();
@@ -1171,6 +1179,10 @@ bool lora_proj_plan(int R, int per, int H, int O, int adapters, int rank, int32_
     return true;
 }
 
+static std::atomic<long long> g_lora_wait_ns{0};
+
+void lora_proj_set_wait_ns(long long ns) { g_lora_wait_ns.store(ns > 0 ? ns : 0); }
+
 int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     LpParams p;
     LpPlan plan;
@@ -1185,7 +1197,8 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     uint32_t cols = 32;
     while (cols < (uint32_t)((p.CK > 1 ? 1 : 2) * p.BN)) cols <<= 1;
     p.tmem_cols = cols;
-    p.wait_ns = kWaitDeadlineNs;
+    const long long wns = g_lora_wait_ns.load();
+    p.wait_ns = wns > 0 ? (unsigned long long)wns : kWaitDeadlineNs;
     p.t = static_cast<const __nv_bfloat16 *>(a.workspace);
     p.ids = a.ids;
     p.lora_b = static_cast<const __nv_bfloat16 *>(a.lora_b);
@@ -1196,7 +1209,7 @@ int launch_lora_proj(const LoraArgs &a, cudaStream_t stream) {
     if (!lp_map(&tmw, a.weight, a.O, a.H, a.H, lp::BM) ||
         !lp_map(&tmx, a.x, a.R, a.H, a.x_stride, p.BN / cg))
         return SVF_ERR_LAUNCH;
-    if (launch_lora_shrink(a, stream) != cudaSuccess) return SVF_ERR_LAUNCH;
+    if (launch_lora_shrink(a, p.wait_ns, stream) != cudaSuccess) return SVF_ERR_LAUNCH;
     int clusters = p.tiles;
     if (p.CK == 1 && clusters > plan.resident) clusters = plan.resident;  // persistent
     const int cluster = cg * p.CK;

@@ -51,6 +51,7 @@ struct ShrinkArgs {
     long long x_stride;
     int R, H, rank, adapters, per;
     int KS, slots, ngroups;
+    unsigned long long wait_ns;
 };
 
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
@@ -192,7 +193,7 @@ __global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(Sh
                             cluster_map(&s_full, to));
             }
             sent = true;
-            lost = !mbar_wait_cluster(&s_full, 0);
+            lost = !mbar_wait_cluster_for(&s_full, 0, p.wait_ns);
         }
         const float scale = p.scales ? p.scales[id] : 1.f;
         for (int i = ks * share + tid; i < (ks + 1) * share; i += kShrinkThreads) {
@@ -218,10 +219,15 @@ __global__ void __maxnreg__(MT == 1 && NT == 4 ? 96 : 128) lora_shrink_kernel(Sh
     }
     if (shared && !sent) cluster_wait();
     if (shared && __syncthreads_or(lost)) {
-        // terms may still be on their way here: leave after those who send them
+        // Terms may still be on their way here. Every other CTA has sent its own
+        // once it comes to this barrier too, or has left; then they land.
         cluster_arrive();
         cluster_wait();
-        if (tid == 0) atomicOr(p.status, SVF_DEV_TIMEOUT);
+        if (tid == 0) {
+            mbar_wait_cluster_for(&s_full, 0, 20000000ull);
+            atomicOr(p.status, SVF_DEV_TIMEOUT);
+        }
+        __syncthreads();
     }
 }
 
@@ -265,7 +271,8 @@ cudaError_t launch_ranked(const ShrinkArgs &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_lora_shrink(const LoraArgs &a, cudaStream_t stream) {
+cudaError_t launch_lora_shrink(const LoraArgs &a, unsigned long long wait_ns,
+                               cudaStream_t stream) {
     ShrinkArgs p;
     p.x = static_cast<const __nv_bfloat16 *>(a.x);
     p.la = static_cast<const __nv_bfloat16 *>(a.lora_a);
@@ -279,6 +286,7 @@ cudaError_t launch_lora_shrink(const LoraArgs &a, cudaStream_t stream) {
     p.rank = a.rank;
     p.adapters = a.adapters;
     p.per = a.rows_per_id;
+    p.wait_ns = wait_ns;
     if (a.rank <= 8) return launch_ranked<1, 4, 4>(p, stream);
     if (a.rank <= 16) return launch_ranked<2, 4, 3>(p, stream);
     return launch_ranked<4, 2, 2>(p, stream);

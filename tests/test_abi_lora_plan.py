@@ -16,3 +16,10 @@ def test_refusals(size, rc):
     lib = sv.load_library()
     assert lib.svf_debug_lora_plan(*size, (ctypes.c_int32 * 6)()) == rc
     assert lib.svf_debug_lora_plan(*size, None) == -1
+
+
+def test_deadline_hook():
+    import speculative_decoding_tree_03_gb300 as sv
+    lib = sv.load_library()
+    assert lib.svf_debug_set_lora_wait_ns(1) == sv.SVF_OK
+    assert lib.svf_debug_set_lora_wait_ns(-5) == sv.SVF_OK   # the default again
