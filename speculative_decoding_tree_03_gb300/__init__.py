@@ -163,22 +163,23 @@ _fast = None
 
 
 def _load_fastcall(lib) -> None:
-    """The compiled checks of the short calls, if they were built for this torch."""
+    """The compiled checks of the short calls, if they were built from these sources
+    for this interpreter and torch."""
     global _fast
-    path = os.path.join(_HERE, "_build", "_fastcall.so")
-    if not os.path.exists(path):
-        return
     import importlib.machinery
     import importlib.util
 
+    from . import build as _build
+
     try:
+        path = _build.fastcall_path()
+        if not os.path.exists(path):
+            return
         loader = importlib.machinery.ExtensionFileLoader("_fastcall", path)
         mod = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_fastcall", loader))
         loader.exec_module(mod)
-    except ImportError:
-        return
-    if mod.torch_version != torch.__version__.split("+")[0]:
+    except (ImportError, OSError):
         return
     mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in
                (lib.svf_page_reserve, lib.svf_page_release, lib.svf_rope_kv_write,

@@ -4,14 +4,19 @@ Every .cu file under csrc/ compiles to an object in parallel; the objects link
 into _build/libspecverify.so with the CUDA runtime linked statically, so the
 library needs only the driver at run time and shares the process's primary
 context (and therefore torch's streams). fastcall.cpp, the binding's checks of
-its short calls, compiles beside them with g++ against torch's headers; without
-it (no headers, another compiler) the binding makes the same checks itself.
+its short calls, compiles beside them with g++ against torch's headers, into a
+file named by what it was made from; without it (no headers, another compiler)
+the binding makes the same checks itself.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import glob
+import hashlib
 import os
+import platform
 import subprocess
 import sys
 import sysconfig
@@ -22,7 +27,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libspecverify.so")
-FAST = os.path.join(OUT, "_fastcall.so")
 SOURCES = ["mask.cu", "attn_simt.cu", "attn_tc.cu", "attn_sk.cu", "accept.cu", "accept_stream.cu",
            "accept_target_stream.cu",
            "accept_noalloc.cu", "accept_target.cu", "eagle2.cu",
@@ -50,33 +54,49 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
-def _build_fastcall() -> None:
-    src = os.path.join(CSRC, "fastcall.cpp")
-    deps = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "specverify.h")))
-    if os.path.exists(FAST) and os.path.getmtime(FAST) >= deps:
-        return
+def fastcall_path() -> str:
+    """Where the compiled checks of the present sources, interpreter and torch are."""
     import torch
 
-    root = os.path.dirname(torch.__file__)
-    inc = [INCLUDE, os.path.join(root, "include"),
-           os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"],
-           os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
-    tmp = FAST + f".{os.getpid()}.tmp"
-    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-           + [f"-I{p}" for p in inc] + [src, "-o", tmp, "-L" + os.path.join(root, "lib"),
-                                        "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
-                                        "-lc10_cuda"])
+    h = hashlib.sha256("\0".join((torch.__version__, sys.implementation.cache_tag,
+                                  platform.machine())).encode())
+    for path in (os.path.join(CSRC, "fastcall.cpp"), os.path.join(INCLUDE, "specverify.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return os.path.join(OUT, f"_fastcall_{h.hexdigest()[:16]}.so")
+
+
+def _build_fastcall(force: bool = False) -> None:
+    why = ""
     try:
+        import torch
+
+        path = fastcall_path()
+        if os.path.exists(path) and not force:
+            return
+        root = os.path.dirname(torch.__file__)
+        inc = [INCLUDE, os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"],
+               os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+        tmp = path + f".{os.getpid()}.tmp"
+        cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+               + [f"-I{p}" for p in inc] + [os.path.join(CSRC, "fastcall.cpp"), "-o", tmp,
+                                            "-L" + os.path.join(root, "lib"), "-ltorch_python",
+                                            "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"])
         r = subprocess.run(cmd, capture_output=True, text=True)
-        why = r.stderr if r.returncode != 0 else ""
-    except OSError as e:
+        why = r.stderr or "g++ failed" if r.returncode != 0 else ""
+    except (ImportError, AttributeError, OSError) as e:
         why = str(e)
+    # modules of other sources are not kept, whether this one could be built or not
+    for old in glob.glob(os.path.join(OUT, "_fastcall*.so")):
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(old)
     if why:
         sys.stderr.write(f"fastcall.cpp was not built, its checks run in Python:\n{why[-2000:]}\n")
         return
-    os.replace(tmp, FAST)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
@@ -96,7 +116,7 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
 
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 1)
     with cf.ThreadPoolExecutor(jobs + 1) as ex:
-        fast = ex.submit(_build_fastcall)
+        fast = ex.submit(_build_fastcall, force)
         results = list(ex.map(compile_one, SOURCES))
         fast.result()
     if verbose:

@@ -16,7 +16,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include "specverify.h"
 
@@ -298,7 +297,5 @@ PyMODINIT_FUNC PyInit__fastcall() {
     k_status = PyUnicode_InternFromString("status");
     k_n_released = PyUnicode_InternFromString("n_released");
     k_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    PyObject *m = PyModule_Create(&module);
-    if (m) PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION);
-    return m;
+    return PyModule_Create(&module);
 }
