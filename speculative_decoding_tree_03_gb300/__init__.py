@@ -760,6 +760,9 @@ def _call(fn, what: str, dev: int, stream, *args) -> None:
     if dev != _current_device():
         with torch.cuda.device(dev):
             return _call(fn, what, dev, stream, *args)
+    for v, c in zip(args, fn.argtypes):  # ctypes would cut them to 32 bits
+        if c is ctypes.c_int and not -(1 << 31) <= v < 1 << 31:
+            raise SpecVerifyError(f"{what}: {v} does not fit into 32 bits")
     rc = fn(*args, _current_stream(dev) if stream is None else stream.cuda_stream)
     if rc != SVF_OK:
         _check(rc, what)
