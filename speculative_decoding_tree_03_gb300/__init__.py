@@ -1106,7 +1106,8 @@ def verify_step(parent, tokens, q, k_cache, v_cache, page_table, seq_lens, targe
         B, N, Hq, D = q.shape
         need = tree_verify_attn_workspace_size(B, N, Hq, k_cache.shape[2], D, q.dtype,
                                                page_table.shape[1], k_cache.shape[1])
-        bufs["attn_ws"] = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+        with _on(stream, q.device):  # the attention's counters begin at zero
+            bufs["attn_ws"] = torch.zeros((max(need, 1),), dtype=torch.uint8, device=q.device)
     out, lse, astatus, anc, depth, mstatus = tree_mask_attn(
         parent, q, k_cache, v_cache, page_table, seq_lens, anc=bufs.get("anc"),
         depth=bufs.get("depth"), mask_status=bufs.get("mask_status"), out=bufs.get("attn_out"),
