@@ -215,14 +215,16 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
 _ZEROED_WS = {}
 
 
-def _zeroed_workspace(need: int, dev: torch.device) -> torch.Tensor:
+def _zeroed_workspace(need: int, dev: torch.device, stream=None) -> torch.Tensor:
     """The attention workspace used when the caller passes none: zero-filled
-    once and kept per device (every call leaves it zero-filled). Calls that
-    may overlap on the GPU should pass workspaces of their own."""
+    once, on the stream of the call that makes it, and kept per device (every
+    call leaves it zero-filled). Calls that may overlap on the GPU should pass
+    workspaces of their own."""
     key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device())
     ws = _ZEROED_WS.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros((need,), dtype=torch.uint8, device=dev)
+        with _on(stream, dev):
+            ws = torch.zeros((need,), dtype=torch.uint8, device=dev)
         _ZEROED_WS[key] = ws
     return ws
 
@@ -324,7 +326,7 @@ def tree_verify_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     need = int(lib.svf_tree_verify_attn_workspace_size(B, N, Hq, Hkv, D, code, max_pages,
                                                        page_size))
     if workspace is None and need > 0:
-        workspace = _zeroed_workspace(need, dev)
+        workspace = _zeroed_workspace(need, dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib.svf_tree_verify_attn(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, page_size, _ptr(page_table), max_pages,
@@ -382,7 +384,7 @@ def tree_mask_attn(parent: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     need = int(lib.svf_tree_verify_attn_workspace_size(B, N, Hq, Hkv, D, code, max_pages,
                                                        page_size))
     if workspace is None and need > 0:
-        workspace = _zeroed_workspace(need, dev)
+        workspace = _zeroed_workspace(need, dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib.svf_tree_mask_attn(
         _ptr(parent), _ptr(anc), _ptr(depth), _ptr(mask_status), _ptr(q), _ptr(k_cache),

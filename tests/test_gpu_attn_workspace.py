@@ -73,3 +73,25 @@ def test_verify_step(sv, persistent, data, side):
         check(out, bufs["attn_status"], ref)
         # every call leaves the counters, the workspace's last bytes, at zero
         assert not bool(bufs["attn_ws"][-16:].any())
+
+
+def attend(sv, d, stream=None):
+    out, _, status, *_ = sv.tree_mask_attn(d["parent"], d["q"], d["k"], d["v"], d["page_table"],
+                                           d["seq_lens"], stream=stream)
+    return out, status
+
+
+def test_the_shared_workspace_is_zeroed_on_the_call_s_stream(sv, persistent, data, monkeypatch):
+    """The current stream is busy while the call runs on another one."""
+    d, ref = data
+    attend(sv, d)                # whatever a first call sets up
+    torch.cuda.synchronize()
+    monkeypatch.setattr(sv, "_ZEROED_WS", {})
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        leave_ones(size(sv, d))
+    leave_ones(size(sv, d))
+    torch.cuda._sleep(40_000_000)      # about 20 ms of the current stream
+    out, status = attend(sv, d, stream=side)
+    torch.cuda.synchronize()
+    check(out, status, ref)
