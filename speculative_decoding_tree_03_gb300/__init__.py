@@ -219,14 +219,18 @@ def _zeroed_workspace(need: int, dev: torch.device, stream=None) -> torch.Tensor
     """The attention workspace used when the caller passes none: zero-filled
     once, on the stream of the call that makes it, and kept per device (every
     call leaves it zero-filled). Calls that may overlap on the GPU should pass
-    workspaces of their own."""
-    key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device())
-    ws = _ZEROED_WS.get(key)
-    if ws is None or ws.numel() < need:
-        with _on(stream, dev):
+    workspaces of their own. A captured call gets one of the graph's memory,
+    filled in every replay: the kept one goes when a larger shape comes, and
+    one made in a capture would begin at zero only in the replays."""
+    with _on(stream, dev):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros((need,), dtype=torch.uint8, device=dev)
+        key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device())
+        ws = _ZEROED_WS.get(key)
+        if ws is None or ws.numel() < need:
             ws = torch.zeros((need,), dtype=torch.uint8, device=dev)
-        _ZEROED_WS[key] = ws
-    return ws
+            _ZEROED_WS[key] = ws
+        return ws
 
 
 def _stream(stream) -> ctypes.c_void_p:

@@ -95,3 +95,35 @@ def test_the_shared_workspace_is_zeroed_on_the_call_s_stream(sv, persistent, dat
     out, status = attend(sv, d, stream=side)
     torch.cuda.synchronize()
     check(out, status, ref)
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_a_captured_call_has_a_workspace_of_the_graph(sv, persistent, data, monkeypatch, kept):
+    """The graph's first call makes no workspace for eager calls, and a larger
+    eager shape does not take the graph's away."""
+    d, ref = data
+    attend(sv, d)
+    torch.cuda.synchronize()
+    if not kept:
+        monkeypatch.setattr(sv, "_ZEROED_WS", {})
+    before = dict(sv._ZEROED_WS)
+    leave_ones(size(sv, d))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, status = attend(sv, d)
+    assert {k: t.data_ptr() for k, t in sv._ZEROED_WS.items()} == {
+        k: t.data_ptr() for k, t in before.items()}
+    check(*attend(sv, d), ref)            # eager, before the first replay
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        check(out, status, ref)
+    need = size(sv, d)
+    sv._zeroed_workspace(4 * max(need, max(t.numel() for t in sv._ZEROED_WS.values())),
+                         torch.device("cuda", 0))    # a larger shape: the kept one is replaced
+    leave_ones(need)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    check(out, status, ref)
