@@ -1108,16 +1108,19 @@ def verify_step(parent, tokens, q, k_cache, v_cache, page_table, seq_lens, targe
     (optional) holds preallocated outputs and workspaces and is filled on the
     first call."""
     bufs = buffers if buffers is not None else {}
-    if "attn_ws" not in bufs:
+    ws = bufs.get("attn_ws")
+    if ws is None:
         B, N, Hq, D = q.shape
         need = tree_verify_attn_workspace_size(B, N, Hq, k_cache.shape[2], D, q.dtype,
                                                page_table.shape[1], k_cache.shape[1])
         with _on(stream, q.device):  # the attention's counters begin at zero
-            bufs["attn_ws"] = torch.zeros((max(need, 1),), dtype=torch.uint8, device=q.device)
+            ws = torch.zeros((max(need, 1),), dtype=torch.uint8, device=q.device)
+            if not torch.cuda.is_current_stream_capturing():
+                bufs["attn_ws"] = ws  # (one of a graph does so in its replays only)
     out, lse, astatus, anc, depth, mstatus = tree_mask_attn(
         parent, q, k_cache, v_cache, page_table, seq_lens, anc=bufs.get("anc"),
         depth=bufs.get("depth"), mask_status=bufs.get("mask_status"), out=bufs.get("attn_out"),
-        lse=bufs.get("lse"), workspace=bufs["attn_ws"], status=bufs.get("attn_status"),
+        lse=bufs.get("lse"), workspace=ws, status=bufs.get("attn_status"),
         stream=stream)
     bufs["anc"], bufs["depth"], bufs["mask_status"] = anc, depth, mstatus
     bufs["attn_out"], bufs["lse"], bufs["attn_status"] = out, lse, astatus

@@ -127,3 +127,23 @@ def test_a_captured_call_has_a_workspace_of_the_graph(sv, persistent, data, monk
     g.replay()
     torch.cuda.synchronize()
     check(out, status, ref)
+
+
+def test_verify_step_first_called_in_a_capture(sv, persistent, data):
+    """The buffers that such a call leaves serve an eager call before any replay."""
+    d, ref = data
+    args = [d[k] for k in ("parent", "tokens", "q", "k", "v", "page_table", "seq_lens", "target",
+                           "draft", "u_accept", "u_bonus")]
+    sv.verify_step(*args)
+    leave_ones(size(sv, d))
+    bufs = {}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.verify_step(*args, buffers=bufs)
+    for call in (lambda: sv.verify_step(*args, buffers=bufs), g.replay,
+                 lambda: sv.verify_step(*args, buffers=bufs), g.replay):
+        if "attn_out" in bufs:
+            bufs["attn_out"].zero_()
+        call()
+        torch.cuda.synchronize()
+        check(bufs["attn_out"], bufs["attn_status"], ref)
