@@ -27,7 +27,9 @@
 // The kernel is small (128 threads of 128 registers, two CTAs per SM; 96
 // where ranks above 16 fill many CTAs: 128 rows of 100 adapters of rank 64,
 // 8192 -> 10240, took 134 us with 128 and deeper loads, 122 with 96), so
-// that the CTAs of the projection kernel start beside it: its first products
+// that the CTAs of the projection kernel start beside it (the cap of 128 makes
+// the instance of rank 8 spill 52 bytes, and 32-row tiles of rank 16 20): its
+// first products
 // need no t, which is there (after 5 to 12 us) before their last. Alone it
 // takes 5.5 us for one row, 7.5 us for 64 rows of 56 adapters of rank 16
 // (4096 columns).
@@ -241,20 +243,32 @@ cudaError_t launch_tiled(ShrinkArgs p, cudaStream_t stream) {
     const int groups = p.R / p.per;
     if (most > groups) most = groups;
     if (most > rows) most = rows;
-    // Two CTAs per SM, so that the projection's CTAs fit beside them, while
-    // what is read is small; six where it would take longer than the
-    // projection's first products (then the sooner it is over the better).
-    // Where there are fewer blocks than that, an adapter of a block each.
+    // As many CTAs as hold an adapter of a block each, but at most so many per SM:
+    // two while what is read is small, so that the projection's CTAs fit beside
+    // them (64 rows, 56 adapters of rank 16, 4096 -> 4096: 18.5 us, 20.2 with
+    // six); six where it would take longer than the projection's first products
+    // (then the sooner it is over the better: 512 rows in groups of 4, 100
+    // adapters of rank 64, 4096 -> 6144: 74.5 us, 89 with two).
     const int used = groups < p.adapters ? groups : p.adapters;
     const double bytes = 2.0 * p.H * (p.R + (double)used * p.rank);
-    const long long room = (bytes > 16e6 ? 6ll : 2ll) * num_sms();
+    const bool large = bytes > 16e6;
+    const long long room = (large ? 6ll : 2ll) * num_sms();
     int slots = most;
     while (slots > 1 && (long long)blocks * slots * p.ngroups > room) slots = (slots + 1) / 2;
     p.slots = slots;
-    // then up to 8 CTAs over K, each warp with a block of its own
+    // Then up to 8 CTAs over K, each warp with a block of its own (a cluster takes
+    // one adapter, so only where there are slots for all). Of the six per SM this
+    // fills three for ranks up to 32 and fewer than 1024 rows: 256 rows of 200
+    // adapters of rank 16, 4096 -> 4096: 31.3 us, 37.3 with six; 64 rows, 40
+    // adapters of rank 16, 14336 -> 4096: 32.0, 34.0; 640 rows in groups of 4, 160
+    // adapters of rank 32: 46.8, 44.6. All six else: 32 rows of 32 adapters of rank
+    // 64: 22.7, 25.1 with two; 4096 rows in groups of 64, 60 adapters of rank 16:
+    // 101, 105 to 117 with two.
+    const long long room_k =
+        large && p.rank <= 32 && p.R < 1024 ? 3ll * num_sms() : room;
     const int kchunks = (p.H + 31) / 32;
     p.KS = 1;
-    while (p.KS < 8 && 2ll * p.KS * blocks * slots * p.ngroups <= room &&
+    while (slots == most && p.KS < 8 && 2ll * p.KS * blocks * slots * p.ngroups <= room_k &&
            p.KS * kShrinkWarps < kchunks)
         p.KS *= 2;
     return launch_pdl(lora_shrink_kernel<MT, NT, DEPTH>,
@@ -264,8 +278,12 @@ cudaError_t launch_tiled(ShrinkArgs p, cudaStream_t stream) {
 
 template <int NT, int D1, int D2>
 cudaError_t launch_ranked(const ShrinkArgs &p, cudaStream_t stream) {
-    // groups of 16 rows or more: a tile of A serves 32 rows
-    return p.per >= 16 && p.R >= 1024 ? launch_tiled<2, NT, D2>(p, stream)
+    // Tiles of 32 rows, which a tile of A serves at once, where they meet at most
+    // two groups (4096 columns; tiles of 16 in brackets: 768 rows in groups of 32,
+    // 24 adapters of rank 16: 26.4 us [27.6]; 900 in groups of 60, rank 64: 50.9
+    // [54.6]; 1984 in groups of 31, rank 16: 75.6 [74.4]; but 1024 in groups of 16,
+    // rank 16: 41.5 [37.2]) and are many (256 in groups of 64, rank 64: 22.1 [21.0]).
+    return p.per >= 31 && p.R >= 512 ? launch_tiled<2, NT, D2>(p, stream)
                                      : launch_tiled<1, NT, D1>(p, stream);
 }
 
