@@ -15,10 +15,12 @@
 // Bound: latency. The 70B-shaped batch (64 trees of 31 nodes) moves 28 KB; the
 // time is the launch, three dependent reads (lengths, top of the stack, page
 // id) and the stores. So every CTA sums the lengths of all sequences before
-// its own (a few loads per thread, all from L2) instead of waiting for a scan
-// by somebody else, and only the counter of the pool needs an order: the CTAs
-// take tickets after they have read it, and the last one writes the new count
-// (no CTA waits).
+// its own instead of waiting for a scan by somebody else, and only the counter
+// of the pool needs an order: the CTAs take tickets after they have read it, and
+// the last one writes the new count (no CTA waits). That is a few loads per
+// thread, all from L2, for batches of some hundred sequences; its cost grows
+// with the square of the batch (trees of 31 nodes, reserve alone: 64 sequences
+// 4 us, 1024 9 us, 4096 50 us, 8192, the most, 167 us).
 #include "common.cuh"
 #include "internal.h"
 
@@ -207,10 +209,11 @@ __device__ __forceinline__ Gift gift_of(const ReleaseArgs &a, int b) {
 // ranks 0 .. total - 1, sequence by sequence in table order; thread t of all
 // takes the ranks t, t + threads, .. (their sequence by a search in the sums),
 // looks at the ids, and once nobody found a bad one puts rank k at
-// free[F + total - 1 - k]. So the chain is two reads, lengths and ids, whatever
-// the lengths are like (200 ragged prompts of 16 thousand pages, reserve and
-// release: 15.3 us; 20.7 with a warp to a sequence and long ones by whole CTAs
-// one after the other).
+// free[F + total - 1 - k]. So the chain is two reads, lengths and ids (and the
+// lengths once more where bad sequences are left out), whatever the lengths are
+// like (200 ragged prompts of 16 thousand pages, reserve and release: 15.3 us;
+// 20.7 with a warp to a sequence and long ones by whole CTAs one after the
+// other).
 __global__ void __launch_bounds__(kReleaseThreads) page_release_kernel(ReleaseArgs a, int ctas) {
     extern __shared__ int s_off[];  // [B + 1] the running sum of the pages
     int *s_first = s_off + a.B + 1;  // [B]

@@ -1,5 +1,5 @@
 """Page calls at the ends of their documented range: batch sizes whose sums just
-fill a block's default shared memory."""
+fill a block's default shared memory, and the largest batch."""
 
 import os
 import subprocess
@@ -7,8 +7,9 @@ import sys
 
 import numpy as np
 import pytest
+import torch
 
-from test_gpu_pages import Model, dev, run_release, sv, world  # noqa: F401
+from test_gpu_pages import Model, dev, run_release, run_reserve, sv, up, world  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,25 @@ def test_release_where_its_sums_fill_the_default_shared_memory(sv):  # noqa: F81
             % (here, os.path.dirname(here)))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("scarce", [False, True])
+def test_reserve_for_the_largest_batch(sv, scarce):  # noqa: F811
+    B, ps, mp = 8192, 16, 9
+    rng, lens, table, free, n = world(77, B, ps, mp, 100, 12000)
+    new = rng.integers(0, 41, B).astype(np.int32)
+    need = sum(up(int(a + b), ps) - up(int(a), ps) for a, b in zip(lens, new))
+    assert need < 12000
+    m = Model(table, free, need // 2 if scarce else 12000, ps, n)
+    run_reserve(sv, m, lens, new, int(new.sum()) + 5)
+
+
+def test_batches_past_the_limit_are_refused(sv):  # noqa: F811
+    B = 8193
+    i = torch.zeros(B, dtype=torch.int32, device="cuda")
+    table = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    pool = sv.page_pool(4)
+    for call in (lambda: sv.page_reserve(pool, table, i, i, 16, 4),
+                 lambda: sv.page_release(pool, table, i, i, 16)):
+        with pytest.raises(sv.SpecVerifyError):
+            call()
