@@ -279,11 +279,13 @@ cudaError_t launch_tiled(ShrinkArgs p, cudaStream_t stream) {
 template <int NT, int D1, int D2>
 cudaError_t launch_ranked(const ShrinkArgs &p, cudaStream_t stream) {
     // Tiles of 32 rows, which a tile of A serves at once, where they meet at most
-    // two groups (4096 columns; tiles of 16 in brackets: 768 rows in groups of 32,
-    // 24 adapters of rank 16: 26.4 us [27.6]; 900 in groups of 60, rank 64: 50.9
-    // [54.6]; 1984 in groups of 31, rank 16: 75.6 [74.4]; but 1024 in groups of 16,
-    // rank 16: 41.5 [37.2]) and are many (256 in groups of 64, rank 64: 22.1 [21.0]).
-    return p.per >= 31 && p.R >= 512 ? launch_tiled<2, NT, D2>(p, stream)
+    // two groups (4096 columns; tiles of 16 in brackets: 1024 rows in groups of 32,
+    // 9 adapters of rank 32: 38.8 us [40.4]; 4096 in groups of 128, rank 8: 97
+    // [102]; 1984 in groups of 31, rank 16: 75.6 [74.4]; but 1024 in groups of 16,
+    // rank 16: 41.5 [37.2]) and are many (512 in groups of 32, rank 16, 4096 ->
+    // 6144: 30.3 [27.9]; -> 4096: 22.2 [22.8]; 256 in groups of 64, rank 64: 22.1
+    // [21.0]).
+    return p.per >= 31 && p.R >= 1024 ? launch_tiled<2, NT, D2>(p, stream)
                                      : launch_tiled<1, NT, D1>(p, stream);
 }
 

@@ -8,14 +8,14 @@ from test_gpu_lora_proj import case, check, sv  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
-# groups, rows each, H, O, adapters, ranks: tiles of 32 rows (groups of 31 rows or more, 512 rows or
-# more) and of 16, each with 8, 16 and 32 columns of a rank
+# groups, rows each, H, O, adapters, ranks: tiles of 32 rows (groups of 31 rows or more, 1024 rows
+# or more) and of 16, each with 8, 16 and 32 columns of a rank
 SHAPES = [
-    (33, 31, 520, 40, 5, (8, 16, 24, 128)),      # 1023 rows: the last tile is cut
-    (16, 32, 4096, 64, 9, (8, 16, 64)),
+    (35, 31, 520, 40, 5, (8, 16, 24, 128)),      # 1085 rows: the last tile is cut
+    (32, 32, 4096, 64, 9, (8, 16, 64)),
     (8, 128, 1000, 33, 3, (8, 16, 40)),          # the rows of a tile have one adapter
     (64, 16, 264, 40, 30, (8, 16, 32)),          # groups of 16 rows
-    (2, 511, 72, 40, 2, (8, 16, 96)),            # the two requests meet in one tile
+    (2, 513, 72, 40, 2, (8, 16, 96)),            # the two requests meet in one tile
     (24, 21, 600, 40, 24, (8, 16, 56)),          # 504 rows
 ]
 
