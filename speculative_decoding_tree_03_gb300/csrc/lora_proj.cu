@@ -53,13 +53,15 @@
 // block, and their sums meet over distributed shared memory in a fixed order.
 //
 // Bound and measured (graph replays, three sets of inputs in turn): 1984 rows,
-// 8192 -> 10240, 24 adapters of rank 16: the tensor cores, 200-206 us = 1.62 to
-// 1.67 PFLOP/s, 97 % of the measured sustained rate of a library product under
-// the power cap (341 us with one CTA per tile and lane-predicated issue). Few
-// rows: HBM and the call's own latency: one row, 4096 -> 6144: 15.0 us, of which
-// W streams for 7 (50 MB at 7 TB/s), 3.3 pass from the first launch to this
-// kernel's start, 2 to the first product, 3 in the cluster's sum and exit; 64
-// requests 18.5 us, an EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 23.0.
+// 8192 -> 10240, 24 adapters of rank 16: the tensor cores under the power cap,
+// 202-221 us from one run to the next, 1.51 to 1.66 PFLOP/s, 88 to 97 % of the
+// measured sustained rate of a library product, whose own product of this shape
+// without adapters takes 210 (341 us with one CTA per tile and lane-predicated
+// issue); in a stream of eager calls 230. Few rows: HBM and the call's own
+// latency: one row, 4096 -> 6144: 14.5 us, of which 2.2 pass until this kernel
+// starts, 2.6 to the first product, 6.6 while W streams (50 MB), 3.1 in the
+// adapter's products, the cluster's sum and the exit; 64 requests 18.1 us, an
+// EAGLE-2 batch of 4 x 60 rows (rank 64, 4096 -> 6144) 22.4.
 // Tried and dropped: adapter blocks spread among the last blocks of K
 // (70B-shaped batch 222 against 200 us: their checks and the products share
 // shared memory's bandwidth), one polling lane per warp (one row 19.2
@@ -495,7 +497,8 @@ __device__ __forceinline__ bool lp_load_block(const LpParams &p, const LpShared 
 // that are not inlined take their address, for which every thread would else
 // make a copy in local memory and read all of them from there (one row, 4096 ->
 // 6144: 15.1 against 14.4 us; EAGLE-2 batch 23.5 against 22.5; 128 rows, 100
-// adapters of rank 16, in single CTAs 30.8 against 30.0).
+// adapters of rank 16, in single CTAs 30.8 against 30.0; of ten larger shapes
+// 768 rows of 24 adapters of rank 16 lost most, 33.7 to 34.7).
 template <int CG>
 __global__ void __maxnreg__(80)
     lora_proj_kernel(const __grid_constant__ CUtensorMap tmw,
@@ -594,7 +597,9 @@ __global__ void __maxnreg__(80)
     // Columns from .. to - 1 of a finished tile (rows of y): the work of warps 2
     // to 5. In pairs, whose tiles are wide, warps 6 to 9 take the second half of
     // a CTA's last tile; their adapter blocks are done by then (EAGLE-2 batch
-    // 23.1 us against 23.5; the 32 to 64 columns of single CTAs lost 1 to 4 %).
+    // 23.1 us against 23.5; the 32 to 64 columns of single CTAs lost 1 to 4 %). One
+    // code for both sizes costs single CTAs of many adapters 3 % (128 rows, 100
+    // adapters of rank 16: 30.0 us against 29.1 with a copy of their own).
     const int split = CG == 2 ? (p.BN / 32 + 1) / 2 * 32 : p.BN;
     auto drain = [&](int buf, int m0, int n0, int from, int to) {
         const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31
@@ -1074,12 +1079,12 @@ struct LpPlan {
 // its products (1900 MHz), its share of what the L2 hands to the SMs (19 TB/s
 // measured, 130 GB/s to one) and of HBM (7 TB/s), and the latency of a load
 // (1.7 us) over the stages of its ring; an adapter block about 0.5 us, 0.8 in a
-// pair (128 rows, 100 adapters of rank 16, 4096 -> 6144: pairs 33.6 us, single
-// CTAs 29.4; 100 of rank 64, 8192 -> 10240: pairs 121, single CTAs 136). A tile
+// pair (128 rows, 100 adapters of rank 16, 4096 -> 6144: single CTAs 29.9 us,
+// pairs 33.5; 100 of rank 64, 8192 -> 10240: single CTAs 138, pairs 118). A tile
 // begins with about 3.5 us and ends with its stores (12 ns a row of x), or with
 // the sum over the cluster (30 ns a row); and a CTA costs 12 ns, as it leaves
-// less of the GPU to lora_shrink (240 rows, 4096 -> 6144, rank 64: 96 CTAs 24.8
-// us, 144 CTAs 28.0 us).
+// less of the GPU to lora_shrink (240 rows, 4096 -> 6144, rank 64: 96 CTAs 22.5
+// us, 144 CTAs 26.1; without adapters 20.1 and 19.8).
 static bool lp_make_plan(LpParams c, int groups, LpPlan *plan) {
     double least = 0;
     for (int cg = 1; cg <= 2; ++cg) {
