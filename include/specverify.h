@@ -72,7 +72,8 @@ enum svf_device_status {
                                 launched for (e.g. re-launched by a tool that drops the
                                 cluster attribute); it did no work, outputs undefined */
     SVF_DEV_NO_PAGES = 128,   /* the pool has too few free pages for this sequence */
-    SVF_DEV_BAD_ADAPTER = 256 /* an adapter id outside [-1, number of adapters) */
+    SVF_DEV_BAD_ADAPTER = 256, /* an adapter id outside [-1, number of adapters) */
+    SVF_DEV_BAD_ROW = 512      /* a fork's table row outside the table, or used twice */
 };
 
 /* ------------------------------------------------------------------------
@@ -598,6 +599,78 @@ int svf_page_release(int32_t *page_table, int max_pages, int page_size, int32_t 
                      svf_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * svf_page_fork, svf_page_copy, svf_page_release_shared -- sequences that
+ * share pages: several samples or beams of one prompt.
+ *
+ * "EAGLE 演化史", § Tree Verification 详解, A: every pass reads the cached
+ * prefix; sequences that go on from the same prefix need it in the cache once.
+ * The caller keeps a third array beside the pool's two,
+ *   shares [num_pages] int32   how many sequences besides one hold the page;
+ *                              all 0 at first, and 0 for every free page
+ * (svf_page_reserve needs nothing of it: a page that it hands out is held by
+ * one sequence). Full pages are shared, since nothing is written into them any
+ * more; the tokens behind them get a page of their own. Calls on one pool,
+ * table or shares that may overlap on the GPU must be ordered by the caller.
+ *
+ * svf_page_fork: for f = 0 .. forks - 1, row dst[f] of the table becomes a
+ * sequence of the L = seq_lens[src[f]] tokens of row src[f]. Its first
+ * floor(L / page_size) pages are the source's (shares + 1 each). Where tokens
+ * are left over, it takes a page from the pool and
+ *   copy_src[f], copy_dst[f]   are the source's page and the new one,
+ *   copy_len[f]                is the number of tokens to copy
+ * (else -1, -1, 0), which svf_page_copy does. The rest of the row is -1, and
+ * seq_lens[dst[f]] = L. What row dst[f] held before must have been released.
+ * Forks are served in order: fork f takes its page if the pages taken by forks
+ * 0..f together are free; a fork that is not served leaves row dst[f] empty
+ * (all -1) with length 0.
+ *   seq_lens [B] int32 in and out; src, dst, copy_src, copy_dst, copy_len
+ *   [forks] int32
+ *   status  [forks] int32 out: SVF_DEV_NO_PAGES; SVF_DEV_BAD_ROW (src or dst
+ *           outside [0, B), a dst that another fork writes too, or a row that
+ *           is a src and a dst: nothing is done for these forks);
+ *           SVF_DEV_BAD_LENGTH (a length outside the table's row: nothing is
+ *           done); SVF_DEV_BAD_PAGE (a page id outside [0, num_pages): that
+ *           entry becomes -1 and is not counted or copied)
+ *
+ * svf_page_copy: the first lens[i] tokens of page src[i] over those of page
+ * dst[i], i < n, K and V, every layer. src = dst = -1 leaves an entry out. A
+ * page that is a dst must be no other entry's src or dst (otherwise what it
+ * holds is undefined). k_cache, v_cache, layer_stride as in svf_kv_commit.
+ *   lens    [n] int32, NULL: whole pages
+ *   status  [n] int32 out: SVF_DEV_BAD_PAGE (an id outside [0, num_pages)),
+ *           SVF_DEV_BAD_LENGTH (lens[i] outside [0, page_size]); such an entry
+ *           copies nothing
+ *
+ * svf_page_release_shared: svf_page_release where pages have other holders.
+ * Every page that a sequence leaves loses a holder; one without any goes back
+ * to the pool, at the place in the stack that its last holder in the call (by
+ * index) has in a release without shares, so a call in which nobody shares does
+ * exactly what svf_page_release does.
+ *   n_released [B] int32 out: pages that b put back
+ *   status     [B] int32 out: SVF_DEV_BAD_LENGTH, SVF_DEV_BAD_PAGE (an id
+ *              outside [0, num_pages); such a sequence leaves no page). Pages
+ *              released more often than held are the caller's error; what the
+ *              stack cannot take is dropped, with SVF_DEV_BAD_PAGE for the
+ *              sequence that put it back.
+ *
+ * Limits: those of svf_page_reserve; forks <= 8192; one row holds a page once.
+ * For svf_page_copy 1 <= num_layers <= 65535, Hkv * D * element size a multiple
+ * of 16 bytes, num_pages * page_size below 2^31.
+ * ---------------------------------------------------------------------- */
+int svf_page_fork(int32_t *page_table, int max_pages, int page_size, const int32_t *free_pages,
+                  int32_t *pool_state, int num_pages, int32_t *shares, int32_t *seq_lens, int B,
+                  const int32_t *src, const int32_t *dst, int forks, int32_t *copy_src,
+                  int32_t *copy_dst, int32_t *copy_len, int32_t *status, svf_stream_t stream);
+int svf_page_copy(void *k_cache, void *v_cache, int num_layers, long long layer_stride,
+                  int num_pages, int page_size, const int32_t *src, const int32_t *dst,
+                  const int32_t *lens, int n, int Hkv, int D, int dtype, int32_t *status,
+                  svf_stream_t stream);
+int svf_page_release_shared(int32_t *page_table, int max_pages, int page_size,
+                            int32_t *free_pages, int32_t *pool_state, int num_pages,
+                            int32_t *shares, const int32_t *old_lens, const int32_t *keep_lens,
+                            int B, int32_t *n_released, int32_t *status, svf_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * svf_rope_kv_write -- rotary positions of a step's q and k rows, and their
  * K/V into the cache: what svf_tree_verify_attn takes (q post-RoPE, the
  * tree's K/V written at its slots).
@@ -635,6 +708,90 @@ int svf_rope_kv_write(const void *q, const void *k, const void *v, long long q_s
                       int dtype, const float *rope, int rot, int max_pos, int interleaved,
                       const int32_t *positions, const int32_t *slots, void *q_out, void *k_cache,
                       void *v_cache, int num_slots, int32_t *status, svf_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * svf_norm_rope_kv_write -- svf_rope_kv_write for models that normalise the
+ * heads of q and k first, or turn them by positions on several axes.
+ *
+ * "EAGLE 演化史", § Tree Verification 详解, B (a node stands at the position
+ * that it has in an ordinary sequence, whatever slot holds its K/V). Every head
+ * x of q becomes y = x q_norm / sqrt(sum_i x_i^2 / D + eps), of k the same with
+ * k_norm; then the pairs of y turn as svf_rope_kv_write turns those of x, pair
+ * i by rope[pos][..] at pos = positions[pair_axis[i]][t] (a token of an image
+ * or a video has a time, a height and a width). All of it is fp32, rounded once
+ * to dtype.
+ *   q_norm, k_norm  [D] dtype, 16-byte aligned; NULL: no norm for these heads
+ *   eps             >= 0
+ *   positions       [axes, T] int32
+ *   pair_axis       [rot / 2] int32 in [0, axes); not read for axes = 1
+ *   status          [T] int32, may be NULL: as svf_rope_kv_write's;
+ *                   SVF_DEV_BAD_LENGTH for a position on any axis outside
+ *                   [0, max_pos) and, in every row, for a pair_axis outside
+ *                   [0, axes)
+ * The other arguments, and rows that are left out or flagged, are those of
+ * svf_rope_kv_write. v is copied.
+ * Limits: those of svf_rope_kv_write with D <= 256; 1 <= axes <= 4.
+ * ---------------------------------------------------------------------- */
+int svf_norm_rope_kv_write(const void *q, const void *k, const void *v, long long q_stride,
+                           long long k_stride, long long v_stride, int T, int Hq, int Hkv, int D,
+                           int dtype, const void *q_norm, const void *k_norm, float eps,
+                           const float *rope, int rot, int max_pos, int interleaved,
+                           const int32_t *positions, int axes, const int32_t *pair_axis,
+                           const int32_t *slots, void *q_out, void *k_cache, void *v_cache,
+                           int num_slots, int32_t *status, svf_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * svf_chunk_attn -- causal attention of chunks of new tokens over the paged
+ * cache: prompts, chunks of prompts and single decoded tokens in one call.
+ *
+ * "EAGLE 演化史", § Tree Verification 详解, A and § D.2: the tree's pass
+ * reads a cached prefix; this is the pass that a prompt, or a token outside a
+ * tree, makes over the same cache, grouped-query heads as in
+ * svf_tree_verify_attn. Sequence b's new tokens are rows row_offsets[b] ..
+ * row_offsets[b + 1] - 1 of q (svf_page_reserve's), token i at position
+ * seq_lens[b] + i. With G = Hq / Hkv and KV head g = h / G, row i of b sees the
+ * tokens t <= L_b + i:
+ *   s_t = sm_scale * <q[row][h], K_b,g(t)>
+ *   out[row][h] = sum_t softmax(s)_t V_b,g(t),  lse[row][h] = log sum_t e^{s_t}
+ * The chunk's own K/V must already be in the cache (svf_rope_kv_write).
+ *
+ *   q           [rows, Hq, D] dtype (post-RoPE)
+ *   k_cache, v_cache, num_pages, page_size, page_table, max_pages, sm_scale
+ *               as in svf_tree_verify_attn
+ *   seq_lens    [B] int32      L_b, the tokens before the chunk
+ *   row_offsets [B + 1] int32  rising; lengths of 0 are fine
+ *   out         [rows, Hq, D] dtype; rows behind the last sequence are not
+ *               written, nor read
+ *   lse         [rows, Hq] float32, may be NULL (natural log)
+ *   workspace   device scratch of svf_chunk_attn_workspace_size(...) bytes,
+ *               16-byte aligned, ZERO-FILLED once before its first use; every
+ *               call leaves what has to be zero at zero, so a workspace that is
+ *               large enough serves svf_chunk_attn calls of any shape (no other
+ *               operator's). Calls that may overlap on the GPU need workspaces
+ *               of their own.
+ *   status      [B] int32 out: SVF_DEV_BAD_LENGTH (offsets that fall or pass
+ *               rows: no row of b is written; L_b < 0 or L_b + n_b past the
+ *               page table: its rows are 0); SVF_DEV_BAD_PAGE (a page of its
+ *               tokens has an id outside [0, num_pages): the rows that see a
+ *               token of that page are 0, lse 0); SVF_DEV_TIMEOUT (undefined)
+ * What lies behind a row's last visible token, in later tokens of the chunk or
+ * in the last page, may hold anything and does not reach the row. bf16: products on the
+ * tensor cores with fp32 sums; the weights 2^(s - m) are rounded to bf16
+ * before they multiply V (half a step of the result's type each), their sum is
+ * taken in fp32.
+ * Limits: rows <= 2^24, B <= 2^20, Hkv <= 1024, Hq a multiple of Hkv with
+ * Hq / Hkv <= 64; D in {64, 128} for SVF_F32, D == 128 for SVF_BF16; for
+ * SVF_BF16 page_size in {16, 32, 64} or a multiple of 128; num_pages *
+ * page_size and max_pages * page_size below 2^31; q, k_cache, v_cache, out
+ * 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+size_t svf_chunk_attn_workspace_size(int rows, int B, int Hq, int Hkv, int D, int dtype);
+int svf_chunk_attn(const void *q, const void *k_cache, const void *v_cache, int num_pages,
+                   int page_size, const int32_t *page_table, int max_pages,
+                   const int32_t *seq_lens, const int32_t *row_offsets, int B, int rows, int Hq,
+                   int Hkv, int D, int dtype, float sm_scale, void *out, float *lse,
+                   void *workspace, size_t workspace_bytes, int32_t *status,
+                   svf_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * svf_lora_proj -- a projection shared by all requests, with a low-rank
@@ -732,6 +889,17 @@ int svf_debug_set_lora_wait_ns(long long ns);
  * ---------------------------------------------------------------------- */
 int svf_debug_lora_plan(int R, int rows_per_id, int H, int O, int adapters, int rank,
                         int32_t *plan);
+
+/* ------------------------------------------------------------------------
+ * svf_debug_set_chunk_wait_ns -- test hook: the deadline of every internal
+ * wait of svf_chunk_attn's bf16 kernel, for later calls in this process, as
+ * svf_debug_set_attn_wait_ns for the tree attention. A CTA whose wait runs out
+ * leaves its loops, waits (with the default deadline) for its copies and
+ * products in flight, releases its tensor memory, and the sequences that it had
+ * tiles of get SVF_DEV_TIMEOUT. ns <= 0 restores the default of 2 s. Returns
+ * SVF_OK.
+ * ---------------------------------------------------------------------- */
+int svf_debug_set_chunk_wait_ns(long long ns);
 
 /* Human-readable name of a host return code or of one device status bit. */
 const char *svf_status_string(int code);

@@ -31,6 +31,7 @@ SVF_ERR_SCRATCH_LIMIT = -5
 SVF_DEV_BAD_PARENT, SVF_DEV_BAD_TOKEN, SVF_DEV_BAD_PAGE, SVF_DEV_BAD_LENGTH, SVF_DEV_TIMEOUT = (
     1, 2, 4, 8, 16)
 SVF_DEV_BAD_PATH, SVF_DEV_BAD_CLUSTER, SVF_DEV_NO_PAGES, SVF_DEV_BAD_ADAPTER = 32, 64, 128, 256
+SVF_DEV_BAD_ROW = 512
 
 EXPORTED = [
     "svf_tree_mask_build",
@@ -60,7 +61,14 @@ EXPORTED = [
     "svf_page_pool_init",
     "svf_page_reserve",
     "svf_page_release",
+    "svf_page_fork",
+    "svf_page_copy",
+    "svf_page_release_shared",
     "svf_rope_kv_write",
+    "svf_norm_rope_kv_write",
+    "svf_chunk_attn_workspace_size",
+    "svf_chunk_attn",
+    "svf_debug_set_chunk_wait_ns",
     "svf_lora_proj_workspace_size",
     "svf_lora_proj",
     "svf_status_string",
@@ -146,6 +154,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.svf_rope_kv_write.argtypes = [P, P, P, L, L, L, I, I, I, I, I, P, I, I, I, P, P, P, P, P,
                                       I, P, P]
     lib.svf_rope_kv_write.restype = I
+    lib.svf_page_fork.argtypes = [P, I, I, P, P, I, P, P, I, P, P, I, P, P, P, P, P]
+    lib.svf_page_fork.restype = I
+    lib.svf_page_copy.argtypes = [P, P, I, L, I, I, P, P, P, I, I, I, I, P, P]
+    lib.svf_page_copy.restype = I
+    lib.svf_page_release_shared.argtypes = [P, I, I, P, P, I, P, P, P, I, P, P, P]
+    lib.svf_page_release_shared.restype = I
+    lib.svf_norm_rope_kv_write.argtypes = [P, P, P, L, L, L, I, I, I, I, I, P, P, F, P, I, I, I, P,
+                                           I, P, P, P, P, P, I, P, P]
+    lib.svf_norm_rope_kv_write.restype = I
+    lib.svf_chunk_attn_workspace_size.argtypes = [I, I, I, I, I, I]
+    lib.svf_chunk_attn_workspace_size.restype = Z
+    lib.svf_chunk_attn.argtypes = [P, P, P, I, I, P, I, P, P, I, I, I, I, I, I, F, P, P, P, Z, P, P]
+    lib.svf_chunk_attn.restype = I
+    lib.svf_debug_set_chunk_wait_ns.argtypes = [L]
+    lib.svf_debug_set_chunk_wait_ns.restype = I
     lib.svf_lora_proj_workspace_size.argtypes = [I, I]
     lib.svf_lora_proj_workspace_size.restype = Z
     lib.svf_lora_proj.argtypes = [P, L, P, P, P, P, P, I, I, I, I, I, I, P, L, P, Z, P, P]
@@ -215,17 +238,17 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
 _ZEROED_WS = {}
 
 
-def _zeroed_workspace(need: int, dev: torch.device, stream=None) -> torch.Tensor:
+def _zeroed_workspace(need: int, dev: torch.device, stream=None, of="tree") -> torch.Tensor:
     """The attention workspace used when the caller passes none: zero-filled
-    once, on the stream of the call that makes it, and kept per device (every
-    call leaves it zero-filled). Calls that may overlap on the GPU should pass
+    once, on the stream of the call that makes it, and kept per device and
+    operator (every call leaves zero what has to be). Calls that may overlap on the GPU should pass
     workspaces of their own. A captured call gets one of the graph's memory,
     filled in every replay: the kept one goes when a larger shape comes, and
     one made in a capture would begin at zero only in the replays."""
     with _on(stream, dev):
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros((need,), dtype=torch.uint8, device=dev)
-        key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device())
+        key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device(), of)
         ws = _ZEROED_WS.get(key)
         if ws is None or ws.numel() < need:
             ws = torch.zeros((need,), dtype=torch.uint8, device=dev)
@@ -794,14 +817,18 @@ def _outs(o: dict, dtype, like: torch.Tensor, dev: int, stream, **shapes) -> Non
             _p(o[key], key, dtype, shape, dev)
 
 
-def page_pool(num_pages: int, device="cuda", stream=None) -> dict:
+def page_pool(num_pages: int, device="cuda", stream=None, shared: bool = False) -> dict:
     """A pool of ``num_pages`` pages, all free: ``free`` [num_pages] int32 (a
-    stack of page ids) and ``state`` [4] int32 (state[0] free pages)."""
+    stack of page ids) and ``state`` [4] int32 (state[0] free pages). With
+    ``shared`` also ``shares`` [num_pages] int32, how many sequences besides one
+    hold a page, for page_fork; page_release then goes by it."""
     if num_pages < 1:
         raise SpecVerifyError("num_pages must be at least 1")
     with _on(stream, device):
         pool = {"free": torch.empty((num_pages,), dtype=torch.int32, device=device),
                 "state": torch.empty((4,), dtype=torch.int32, device=device)}
+        if shared:
+            pool["shares"] = torch.zeros((num_pages,), dtype=torch.int32, device=device)
     free, state = pool["free"], pool["state"]
     _call(load_library().svf_page_pool_init, "svf_page_pool_init", _device_of(free, "device"),
           stream, free.data_ptr(), state.data_ptr(), num_pages)
@@ -900,9 +927,11 @@ def page_release(pool: dict, page_table: torch.Tensor, old_lens: torch.Tensor,
                  stream=None) -> dict:
     """Give the pages past the first ``keep_lens`` [B] of ``old_lens`` [B]
     tokens back to the pool (after kv_commit: seq_lens + N and new_seq_lens;
-    for finished requests keep 0). Returns n_released [B], status [B]."""
+    for finished requests keep 0). In a pool with ``shares`` a page goes back
+    when its last holder leaves it. Returns n_released [B], status [B]."""
     lib = _lib or load_library()
-    if _fast is not None and outputs is not None:
+    shares = pool.get("shares")
+    if _fast is not None and outputs is not None and shares is None:
         rc = _fast.page_release(pool, page_table, old_lens, keep_lens, page_size, outputs, stream)
         if rc is not None:
             _check(rc, "svf_page_release")
@@ -921,10 +950,90 @@ def page_release(pool: dict, page_table: torch.Tensor, old_lens: torch.Tensor,
     if not fine:
         _outs(o, i32, page_table, dev, stream, n_released=(B,), status=(B,))
         n_released, status = o["n_released"], o["status"]
+    if shares is not None:
+        _call(lib.svf_page_release_shared, "svf_page_release_shared", dev, stream,
+              page_table.data_ptr(), max_pages, page_size, free.data_ptr(),
+              pool["state"].data_ptr(), free.numel(),
+              _p(shares, "pool['shares']", i32, free.shape, dev), old_lens.data_ptr(),
+              keep_lens.data_ptr(), B, n_released.data_ptr(), status.data_ptr())
+        return o
     _call(lib.svf_page_release, "svf_page_release", dev, stream, page_table.data_ptr(), max_pages,
           page_size, free.data_ptr(), pool["state"].data_ptr(), free.numel(), old_lens.data_ptr(),
           keep_lens.data_ptr(), B, n_released.data_ptr(), status.data_ptr())
     return o
+
+
+def page_fork(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor, src: torch.Tensor,
+              dst: torch.Tensor, page_size: int, outputs: Optional[dict] = None,
+              stream=None) -> dict:
+    """Rows ``dst`` [F] of ``page_table`` become sequences of the tokens of rows
+    ``src`` [F] (int32): full pages are shared, the tokens behind them get a page
+    of the pool, which page_copy fills. The pool has ``shares``
+    (page_pool(..., shared=True)); page_table, seq_lens and the pool are updated in
+    place. Returns device tensors copy_src, copy_dst, copy_len, status [F]."""
+    lib = _lib or load_library()
+    if "shares" not in pool:
+        raise SpecVerifyError("the pool has no 'shares': make it with page_pool(..., shared=True)")
+    dev, B, max_pages = _page_args(pool, page_table, seq_lens, "seq_lens", seq_lens, "seq_lens")
+    i32, free = torch.int32, pool["free"]
+    shares = _p(pool["shares"], "pool['shares']", i32, free.shape, dev)
+    F = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
+    if F < 0:
+        raise SpecVerifyError("src must be [F]")
+    sp, dp = _p(src, "src", i32, (F,), dev), _p(dst, "dst", i32, (F,), dev)
+    o = outputs if outputs is not None else {}
+    _outs(o, i32, page_table, dev, stream, copy_src=(F,), copy_dst=(F,), copy_len=(F,),
+          status=(F,))
+    _call(lib.svf_page_fork, "svf_page_fork", dev, stream, page_table.data_ptr(), max_pages,
+          page_size, free.data_ptr(), pool["state"].data_ptr(), free.numel(), shares,
+          seq_lens.data_ptr(), B, sp, dp, F, o["copy_src"].data_ptr(), o["copy_dst"].data_ptr(),
+          o["copy_len"].data_ptr(), o["status"].data_ptr())
+    return o
+
+
+def _layered(k_cache, v_cache):
+    """(layers, layer stride, pages, page size, Hkv, D) of a pair of caches."""
+    dev = _device_of(k_cache, "k_cache")
+    if k_cache.dim() == 4:
+        layers, (num_pages, page_size, Hkv, D), stride = 1, k_cache.shape, 0
+    elif k_cache.dim() == 5:
+        layers, num_pages, page_size, Hkv, D = k_cache.shape
+        stride = k_cache.stride(0)
+    else:
+        raise SpecVerifyError("k_cache must be [layers,] num_pages, page_size, Hkv, D")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != k_cache.dtype \
+                or t.shape != k_cache.shape:
+            _bad(t, name, k_cache.dtype, k_cache.shape, dev)
+        if layers and not (t[0] if t.dim() == 5 else t).is_contiguous():
+            raise SpecVerifyError(f"each layer of {name} must be contiguous")
+    if v_cache.stride() != k_cache.stride():
+        raise SpecVerifyError("v_cache must have k_cache's strides")
+    return dev, layers, stride, num_pages, page_size, Hkv, D
+
+
+def page_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+              lens: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """The first ``lens`` [n] tokens (None: all) of pages ``src`` [n] over those of
+    pages ``dst`` [n] (int32; -1, -1 leaves an entry out), in place, in every layer of
+    k_cache and v_cache [layers, num_pages, page_size, Hkv, D] (or without the layer
+    axis). Returns status [n]."""
+    lib = _lib or load_library()
+    dev, layers, stride, num_pages, page_size, Hkv, D = _layered(k_cache, v_cache)
+    i32 = torch.int32
+    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
+    if n < 0:
+        raise SpecVerifyError("src must be [n]")
+    sp, dp = _p(src, "src", i32, (n,), dev), _p(dst, "dst", i32, (n,), dev)
+    lp = None if lens is None else _p(lens, "lens", i32, (n,), dev)
+    if status is None:
+        with _on(stream, k_cache.device):
+            status = torch.empty((n,), dtype=i32, device=k_cache.device)
+    _call(lib.svf_page_copy, "svf_page_copy", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(),
+          layers, stride, num_pages, page_size, sp, dp, lp, n, Hkv, D, _dtype_code(k_cache.dtype),
+          _p(status, "status", i32, (n,), dev))
+    return status
 
 
 def _row_stride(t, name: str, dtype, shape, dev: int) -> int:
@@ -1002,6 +1111,121 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch
           1 if interleaved else 0, positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), pages * ps, status.data_ptr())
     return q_out, status
+
+
+def norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       q_norm: Optional[torch.Tensor], k_norm: Optional[torch.Tensor],
+                       rope: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                       k_cache: torch.Tensor, v_cache: torch.Tensor, eps: float = 1e-6,
+                       pair_axis: Optional[torch.Tensor] = None,
+                       q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                       status: Optional[torch.Tensor] = None, stream=None):
+    """rope_kv_write with a norm of every q and k head before it, and positions on
+    several axes.
+
+    q_norm, k_norm [D] of q's dtype (None: no norm); positions [T], or [axes, T] with
+    ``pair_axis`` [rot / 2] int32, the axis that turns each pair. The other arguments,
+    the results and the rows that are left out are rope_kv_write's."""
+    lib = _lib or load_library()
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4 or rope.dim() != 2:
+        raise SpecVerifyError("q and k must be [T, heads, D], the caches [pages, page_size, Hkv, "
+                              "D], rope [max_pos, rot]")
+    T, Hq, D = q.shape
+    Hkv, dt, i32 = k.shape[1], q.dtype, torch.int32
+    qs, ks, vs = (_row_stride(q, "q", dt, (T, Hq, D), dev), _row_stride(k, "k", dt, (T, Hkv, D), dev),
+                  _row_stride(v, "v", dt, (T, Hkv, D), dev))
+    max_pos, rot = rope.shape
+    pages, ps = k_cache.shape[:2]
+    if positions.dim() == 2:
+        axes = positions.shape[0]
+        if axes > 1 and pair_axis is None:
+            raise SpecVerifyError("positions on several axes need pair_axis")
+        pos = _p(positions, "positions", i32, (axes, T), dev)
+    else:
+        axes, pos = 1, _p(positions, "positions", i32, (T,), dev)
+    axis = None if pair_axis is None else _p(pair_axis, "pair_axis", i32, (rot // 2,), dev)
+    wq = None if q_norm is None else _p(q_norm, "q_norm", dt, (D,), dev)
+    wk = None if k_norm is None else _p(k_norm, "k_norm", dt, (D,), dev)
+    if q_out is None or status is None:
+        with _on(stream, q.device):
+            if q_out is None:
+                q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+            if status is None:
+                status = torch.empty((T,), dtype=i32, device=q.device)
+    cache = (pages, ps, Hkv, D)
+    _call(lib.svf_norm_rope_kv_write, "svf_norm_rope_kv_write", dev, stream, q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), qs, ks, vs, T, Hq, Hkv, D, _dtype_code(dt), wq, wk,
+          float(eps), _p(rope, "rope", torch.float32, (max_pos, rot), dev), rot, max_pos,
+          1 if interleaved else 0, pos, axes, axis, _p(slots, "slots", i32, (T,), dev),
+          _p(q_out, "q_out", dt, (T, Hq, D), dev), _p(k_cache, "k_cache", dt, cache, dev),
+          _p(v_cache, "v_cache", dt, cache, dev), pages * ps, _p(status, "status", i32, (T,), dev))
+    return q_out, status
+
+
+# ---------------------------------------------------------------------------
+# Attention of chunks of new tokens over the paged cache
+# ---------------------------------------------------------------------------
+
+def chunk_attn_workspace_size(rows, B, Hq, Hkv, D, dtype) -> int:
+    return int((_lib or load_library()).svf_chunk_attn_workspace_size(
+        rows, B, Hq, Hkv, D, _dtype_code(dtype) if isinstance(dtype, torch.dtype) else int(dtype)))
+
+
+def chunk_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+               page_table: torch.Tensor, seq_lens: torch.Tensor, row_offsets: torch.Tensor,
+               sm_scale: float = 0.0, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+    """Causal attention of chunks of new tokens over the paged cache.
+
+    q [rows, Hq, D]; k_cache, v_cache [num_pages, page_size, Hkv, D] (same dtype,
+    float32 or bfloat16), the chunks' own K/V already in it; page_table [B, max_pages],
+    seq_lens [B] (tokens before the chunk), row_offsets [B + 1] int32 (page_reserve's:
+    sequence b's tokens are rows row_offsets[b] .. row_offsets[b + 1]). A row sees the
+    tokens up to its own. ``workspace``: chunk_attn_workspace_size bytes, zero-filled
+    once; calls that may overlap need workspaces of their own. Returns (out [rows, Hq,
+    D], lse [rows, Hq] float32 or None, status [B] int32); rows behind the last sequence
+    keep what out and lse held (new ones: undefined)."""
+    lib = _lib or load_library()
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
+        raise SpecVerifyError("q must be [rows, Hq, D], k_cache [pages, page_size, Hkv, D], "
+                              "page_table [B, max_pages]")
+    rows, Hq, D = q.shape
+    dt, i32, f32 = q.dtype, torch.int32, torch.float32
+    num_pages, page_size, Hkv = k_cache.shape[:3]
+    B, max_pages = page_table.shape
+    cache = (num_pages, page_size, Hkv, D)
+    code = _dtype_code(dt)
+    args = (_p(q, "q", dt, (rows, Hq, D), dev), _p(k_cache, "k_cache", dt, cache, dev),
+            _p(v_cache, "v_cache", dt, cache, dev), num_pages, page_size,
+            _p(page_table, "page_table", i32, (B, max_pages), dev), max_pages,
+            _p(seq_lens, "seq_lens", i32, (B,), dev),
+            _p(row_offsets, "row_offsets", i32, (B + 1,), dev), B, rows, Hq, Hkv, D, code,
+            float(sm_scale))
+    if out is None or status is None or (lse is None and want_lse):
+        with _on(stream, q.device):
+            if out is None:
+                out = torch.empty((rows, Hq, D), dtype=dt, device=q.device)
+            if lse is None and want_lse:
+                lse = torch.empty((rows, Hq), dtype=f32, device=q.device)
+            if status is None:
+                status = torch.empty((B,), dtype=i32, device=q.device)
+    op = _p(out, "out", dt, (rows, Hq, D), dev)
+    lp = None if lse is None else _p(lse, "lse", f32, (rows, Hq), dev)
+    st = _p(status, "status", i32, (B,), dev)
+    if workspace is None:
+        need = int(lib.svf_chunk_attn_workspace_size(rows, B, Hq, Hkv, D, code))
+        if need:
+            with torch.cuda.device(dev):
+                workspace = _zeroed_workspace(need, q.device, stream, "chunk")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise SpecVerifyError("workspace must be a contiguous tensor on q's device")
+    _call(lib.svf_chunk_attn, "svf_chunk_attn", dev, stream, *args, op, lp,
+          None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.nbytes, st)
+    return out, lse, status
 
 
 def lora_proj_workspace_size(R: int, rank: int) -> int:

@@ -31,7 +31,8 @@ SOURCES = ["mask.cu", "attn_simt.cu", "attn_tc.cu", "attn_sk.cu", "accept.cu", "
            "accept_target_stream.cu",
            "accept_noalloc.cu", "accept_target.cu", "eagle2.cu",
            "kv_commit.cu", "lm_head.cu", "lora_proj.cu", "lora_shrink.cu", "pages.cu",
-           "rope_kv.cu", "selftest.cu", "api.cu"]
+           "pages_shared.cu", "rope_kv.cu", "norm_rope.cu", "chunk.cu", "chunk_simt.cu",
+           "chunk_tc.cu", "selftest.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

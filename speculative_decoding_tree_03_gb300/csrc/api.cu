@@ -55,6 +55,7 @@ const char *svf_status_string(int code) {
         case SVF_DEV_BAD_CLUSTER: return "device: kernel ran without its thread-block cluster";
         case SVF_DEV_NO_PAGES: return "device: too few free pages in the pool";
         case SVF_DEV_BAD_ADAPTER: return "device: adapter id outside the adapters";
+        case SVF_DEV_BAD_ROW: return "device: table row outside the table or used twice";
         default: return "unknown status";
     }
 }
@@ -583,6 +584,181 @@ int svf_kv_commit(void *k_cache, void *v_cache, int num_layers, long long layer_
     a.max_free = max_free; a.n_freed = n_freed; a.status = status;
     cudaError_t e = launch_kv_commit(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+int svf_page_release_shared(int32_t *page_table, int max_pages, int page_size,
+                            int32_t *free_pages, int32_t *pool_state, int num_pages,
+                            int32_t *shares, const int32_t *old_lens, const int32_t *keep_lens,
+                            int B, int32_t *n_released, int32_t *status, svf_stream_t stream) {
+    if (B < 0) return SVF_ERR_ARG;
+    if (B == 0) return SVF_OK;
+    if (!n_released || !status || !shares) return SVF_ERR_ARG;
+    const int rc = page_arg_check(page_table, max_pages, page_size, free_pages, pool_state,
+                                  num_pages, old_lens, keep_lens, B);
+    if (rc != SVF_OK) return rc;
+    const PageReleaseArgs a = {page_table, old_lens,   keep_lens, free_pages, pool_state,
+                               n_released, status,     B,         max_pages,  page_size,
+                               num_pages};
+    cudaError_t e = launch_page_release_shared(a, shares, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+int svf_page_fork(int32_t *page_table, int max_pages, int page_size, const int32_t *free_pages,
+                  int32_t *pool_state, int num_pages, int32_t *shares, int32_t *seq_lens, int B,
+                  const int32_t *src, const int32_t *dst, int forks, int32_t *copy_src,
+                  int32_t *copy_dst, int32_t *copy_len, int32_t *status, svf_stream_t stream) {
+    if (B < 0 || forks < 0) return SVF_ERR_ARG;
+    if (forks == 0) return SVF_OK;
+    if (!shares || !src || !dst || !copy_src || !copy_dst || !copy_len || !status)
+        return SVF_ERR_ARG;
+    const int rc = page_arg_check(page_table, max_pages, page_size, free_pages, pool_state,
+                                  num_pages, seq_lens, seq_lens, B);
+    if (rc != SVF_OK) return rc;
+    if (forks > kMaxPageSequences) return SVF_ERR_UNSUPPORTED;
+    const PageForkArgs a = {page_table, free_pages, pool_state, shares,    seq_lens, src,
+                            dst,        copy_src,   copy_dst,   copy_len,  status,   B,
+                            forks,      max_pages,  page_size,  num_pages};
+    cudaError_t e = launch_page_fork(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+int svf_page_copy(void *k_cache, void *v_cache, int num_layers, long long layer_stride,
+                  int num_pages, int page_size, const int32_t *src, const int32_t *dst,
+                  const int32_t *lens, int n, int Hkv, int D, int dtype, int32_t *status,
+                  svf_stream_t stream) {
+    if (n < 0 || num_layers < 0 || Hkv <= 0 || D <= 0 || num_pages <= 0 || page_size <= 0 ||
+        layer_stride < 0)
+        return SVF_ERR_ARG;
+    if (n == 0) return SVF_OK;
+    if (!k_cache || !v_cache || !src || !dst || !status) return SVF_ERR_ARG;
+    if (num_layers < 1 || num_layers > 65535) return SVF_ERR_UNSUPPORTED;
+    const int elem = dtype == SVF_BF16 ? 2 : dtype == SVF_F32 ? 4 : 0;
+    if (elem == 0 || ((long long)Hkv * D * elem) % 16 != 0) return SVF_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size > INT_MAX || (long long)Hkv * D * elem / 16 > INT_MAX)
+        return SVF_ERR_UNSUPPORTED;
+    if (num_layers > 1 && layer_stride / num_pages / page_size / Hkv < D) return SVF_ERR_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || (layer_stride * elem) % 16 != 0)
+        return SVF_ERR_ARG;
+    const PageCopyArgs a = {k_cache,   v_cache,   num_layers, num_layers > 1 ? layer_stride : 0,
+                            num_pages, page_size, Hkv,        D,
+                            elem,      n,         src,        dst,
+                            lens,      status};
+    cudaError_t e = launch_page_copy(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+int svf_norm_rope_kv_write(const void *q, const void *k, const void *v, long long q_stride,
+                           long long k_stride, long long v_stride, int T, int Hq, int Hkv, int D,
+                           int dtype, const void *q_norm, const void *k_norm, float eps,
+                           const float *rope, int rot, int max_pos, int interleaved,
+                           const int32_t *positions, int axes, const int32_t *pair_axis,
+                           const int32_t *slots, void *q_out, void *k_cache, void *v_cache,
+                           int num_slots, int32_t *status, svf_stream_t stream) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || D < 0 || rot < 0 || max_pos < 0 || num_slots < 0 ||
+        axes < 1 || !(eps >= 0.0f))
+        return SVF_ERR_ARG;
+    if (T == 0) return SVF_OK;
+    if ((Hq > 0 && (!q || !q_out)) || !k || !v || !rope || !positions || !slots || !k_cache ||
+        !v_cache || (axes > 1 && !pair_axis))
+        return SVF_ERR_ARG;
+    if (dtype != SVF_F32 && dtype != SVF_BF16) return SVF_ERR_UNSUPPORTED;
+    const int es = dtype == SVF_F32 ? 4 : 2;
+    if (!norm_rope_supported(T, Hq, Hkv, D, rot, axes, es)) return SVF_ERR_UNSUPPORTED;
+    const long long unit = 16 / es;
+    if ((Hq > 0 && (q_stride < (long long)Hq * D || q_stride % unit || !aligned16(q) ||
+                    !aligned16(q_out))) ||
+        k_stride < (long long)Hkv * D || k_stride % unit || v_stride < (long long)Hkv * D ||
+        v_stride % unit || !aligned16(k) || !aligned16(v) || !aligned16(rope) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q_norm) || !aligned16(k_norm))
+        return SVF_ERR_ARG;
+    NormRopeArgs n;
+    RopeKvArgs &a = n.rope;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.rope = rope;
+    a.positions = positions;
+    a.slots = slots;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.rot = rot;
+    a.max_pos = max_pos;
+    a.num_slots = num_slots;
+    a.elem_size = es;
+    a.interleaved = interleaved != 0;
+    a.q_out = q_out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.status = status;
+    n.q_norm = q_norm;
+    n.k_norm = k_norm;
+    n.pair_axis = pair_axis;
+    n.axes = axes;
+    n.eps = eps;
+    cudaError_t e = launch_norm_rope(n, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SVF_OK : SVF_ERR_LAUNCH;
+}
+
+size_t svf_chunk_attn_workspace_size(int rows, int B, int Hq, int Hkv, int D, int dtype) {
+    if (rows < 0 || B <= 0 || Hq <= 0 || Hkv <= 0 ||
+        !chunk_supported(rows, B, Hq, Hkv, D, dtype, 16))
+        return 0;
+    return chunk_workspace_bytes(rows, Hq, Hkv, D, dtype);
+}
+
+int svf_chunk_attn(const void *q, const void *k_cache, const void *v_cache, int num_pages,
+                   int page_size, const int32_t *page_table, int max_pages,
+                   const int32_t *seq_lens, const int32_t *row_offsets, int B, int rows, int Hq,
+                   int Hkv, int D, int dtype, float sm_scale, void *out, float *lse,
+                   void *workspace, size_t workspace_bytes, int32_t *status,
+                   svf_stream_t stream) {
+    if (B < 0 || rows < 0 || Hq < 0 || Hkv < 0 || D < 0 || num_pages < 0 || page_size < 0 ||
+        max_pages < 0)
+        return SVF_ERR_ARG;
+    if (B == 0) return SVF_OK;
+    if (!page_table || !seq_lens || !row_offsets || !k_cache || !v_cache || !status ||
+        (rows > 0 && (!q || !out)))
+        return SVF_ERR_ARG;
+    if (num_pages < 1 || page_size < 1 || max_pages < 1 ||
+        !chunk_supported(rows, B, Hq, Hkv, D, dtype, page_size) ||
+        (long long)num_pages * page_size > INT_MAX || (long long)max_pages * page_size > INT_MAX)
+        return SVF_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+        !aligned16(workspace))
+        return SVF_ERR_ARG;
+    ChunkArgs a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.row_offsets = row_offsets;
+    a.B = B;
+    a.rows = rows;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.dtype = dtype;
+    a.sm_scale = sm_scale;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    a.status = status;
+    return launch_chunk(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int svf_debug_set_chunk_wait_ns(long long ns) {
+    chunk_set_wait_ns(ns);
+    return SVF_OK;
 }
 
 }  // extern "C"

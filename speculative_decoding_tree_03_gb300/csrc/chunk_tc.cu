@@ -1,0 +1,861 @@
+// chunk_tc.cu -- attention of chunks of new tokens over the paged cache (bf16, head_dim 128,
+// 5th-generation tensor cores).
+//
+//     out[r] = sum_{t <= L + i} p_t V_t / sum p_t,   p_t = 2^(scale log2(e) q_r . K_t - m_r)
+//
+// for row i of a sequence, in one pass over its keys. A CTA goes through the tiles of its
+// share of the call (chunk.cuh): up to two halves of 128 rows (token, head) against 128 tokens.
+// S = Q K^T and O += P V run on the tensor cores, S, P (bf16) and O in tensor memory:
+//     columns 0..127 S, 128..191 P of half 0, 192..255 P of half 1, 256 + 128 h.. O of half h.
+// One S serves both halves in turn: the softmax warps of a half take it into registers at
+// once and give it back, so that the next product never waits for their arithmetic. In the
+// steady state one thread issues
+//     QK_0(j)  PV_1(j-1)  QK_1(j)  PV_0(j)  QK_0(j+1) ...
+// and each half has the time of two products of the other one for its softmax. A thread sustains
+// N = 128 products at the tensor cores' full rate (64 cycles for M = N = 128, K = 16), so one
+// issuing thread is enough; N = 64 takes nearly as long (59), hence 128 tokens to a tile.
+//
+// Warps: K producer, V producer, the issuer, the planner (which lays out the CTA's parts ahead of the
+// others, in a ring in shared memory, and loads their Q), and four softmax warps per half,
+// which also write the results. A part of at most 128 rows uses half 0 alone.
+//
+// The running maximum m moves only when it grows by more than 2^8 (O is rescaled then); sums
+// and O are fp32. P is rounded to bf16 for the second product, at most half a step each.
+//
+// A token that a row does not see has p = 0, but 0 * V is no zero where V holds an infinity or
+// a NaN. Rows behind the block's last token are zeroed in shared memory; tokens inside the block can
+// only be masked. So a row that comes out with a value that is not finite, and that has masked tokens
+// among its tiles, is computed again from its visible tokens alone, by its warp in fp32.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "attn_tc_common.cuh"
+#include "chunk.cuh"
+
+namespace svf {
+
+namespace {
+
+namespace ct {
+constexpr int BN = 128;                  // tokens per tile
+constexpr int HD = 128;                  // head_dim
+constexpr int COL = 128 * 128;           // one 64-dim block of 128 rows (bytes)
+constexpr int TILE = 2 * COL;            // 128 rows of Q, K or V
+constexpr int KS = 2, VS = 3;            // ring stages
+constexpr int NR = 4;                    // parts in the planner's ring
+constexpr int NT = 384;
+constexpr int SW0 = 4;                   // first softmax warp
+constexpr uint32_t tS = 0, tP = 128, tO = 256;
+constexpr unsigned long long kLongWaitNs = 60000000000ull;  // waits as long as a part may take
+constexpr int kBarBoth = 1, kBarHalf = 2;  // named barriers: all softmax warps, half 0's
+}  // namespace ct
+
+struct TcPart {
+    int b, head, row, tok0, ntok;  // row: q row of the block's first token
+    int L;
+    int x0, n, t;                  // first tile, tiles of the part, tiles of the unit
+    int cf, cl, slot;              // groups that share the unit; this part's place in the workspace
+    int first_slot;                // piece 0's: 1 if the unit is not the first of its group
+    int two;                       // both halves have rows
+    int bad;                       // first token whose page is not in the cache
+    int pad;
+};
+
+struct TcSmem {
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + 2 * ct::TILE;
+    static constexpr int kV = kK + ct::KS * ct::TILE;
+    static constexpr int kBar = kV + ct::VS * ct::TILE;
+    static constexpr int kNumBars = 2 * ct::KS + 2 * ct::VS + 2 * ct::NR + 2 + 1 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kMisc = kBar + ((kNumBars * 8 + 127) / 128) * 128;
+    static constexpr int kSpace = kMisc + 64;
+    static constexpr int kParts = kSpace + 64;
+    static constexpr int kJoin = kParts + ct::NR * (int)sizeof(TcPart);
+    static constexpr int kBytes = kJoin + 256 * 4;
+    static constexpr int kDynamic = kBytes + 1024;  // slack to align the base to 1 KB
+    static_assert(sizeof(ChunkSpace) <= 64, "space");
+    static_assert(kDynamic <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ int bar_or(int id, int n, int pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(pred), "r"(id), "r"(n)
+        : "memory");
+    return (int)r;
+}
+
+// Eight floats (as bits) as bf16.
+__device__ __forceinline__ uint4 eight_bf16(const uint32_t *o) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The row of a part again, from its visible tokens in [t0, t1) alone, by a warp: 4 of the head's
+// elements per lane. Sums in fp32; returns the normalised elements and the log2-sum-exp.
+__device__ __noinline__ float4 row_again(const ChunkParams &p, int b, int head, size_t qrow, int t0,
+                                         int t1, float *lse2) {
+    const int lane = threadIdx.x & 31;
+    auto four = [&](const void *base, size_t row) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(
+                                  static_cast<const __nv_bfloat16 *>(base) + row * ct::HD) + lane);
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                           __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+    };
+    const float4 q = four(p.q, qrow);
+    const int32_t *table = p.page_table + (size_t)b * p.max_pages;
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int t = t0; t < t1; ++t) {
+        const int id = __ldg(table + t / p.ps);
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+        if (id >= 0 && id < p.num_pages) {
+            const size_t at = ((size_t)id * p.ps + t % p.ps) * p.Hkv + head;
+            k = four(p.k_cache, at);
+            v = four(p.v_cache, at);
+        }
+        const float s = warp_sum(fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)))) *
+                        p.scale_log2;
+        const float nm = fmaxf(m, s);
+        const float base = nm == -INFINITY ? 0.0f : nm;
+        const float a = ex2_approx(m - base), e = ex2_approx(s - base);
+        m = nm;
+        l = fmaf(l, a, e);
+        o.x = fmaf(e, v.x, o.x * a);
+        o.y = fmaf(e, v.y, o.y * a);
+        o.z = fmaf(e, v.z, o.z * a);
+        o.w = fmaf(e, v.w, o.w * a);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *lse2 = l == 0.0f ? -INFINITY : m + __log2f(l);
+    return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+__global__ void __launch_bounds__(ct::NT, 1)
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                    const __grid_constant__ CUtensorMap tmq, ChunkParams p) {
+    using namespace ct;
+    using S = TcSmem;
+    constexpr unsigned FULL = 0xffffffffu;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *sQ = smem + S::kQ, *sK = smem + S::kK, *sV = smem + S::kV;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBar);
+    uint64_t *k_full = bars, *k_empty = k_full + KS;
+    uint64_t *v_full = k_empty + KS, *v_empty = v_full + VS;
+    uint64_t *part_full = v_empty + VS;       // [NR] the planner wrote the part
+    uint64_t *part_empty = part_full + NR;    // [NR] everybody is through with it
+    uint64_t *q_full = part_empty + NR;       // the part's Q landed
+    uint64_t *q_free = q_full + 1;            // its products are done: Q may be replaced
+    uint64_t *s_free = q_free + 1;            // S was taken into registers
+    uint64_t *s_full = s_free + 1;            // [2] Q K^T of the half is in S
+    uint64_t *p_full = s_full + 2;            // [2] P of the half is written
+    uint64_t *o_done = p_full + 2;            // [2] P V of the half is done
+    uint64_t *o_free = o_done + 2;            // [2] O of the half was read out
+    uint64_t *drain = o_free + 2;             // the issuer's products done, after an abort
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kMisc + 4);
+    int *s_last = reinterpret_cast<int *>(smem + S::kMisc + 8);
+    ChunkSpace *space = reinterpret_cast<ChunkSpace *>(smem + S::kSpace);
+    TcPart *parts = reinterpret_cast<TcPart *>(smem + S::kParts);
+    float *join = reinterpret_cast<float *>(smem + S::kJoin);  // [256] the rows' joined log2-sum-exp
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hl = blockIdx.x % p.S;  // this CTA's head of a head block
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < KS; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < VS; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&part_full[i], 1);
+            mbar_init(&part_empty[i], 3 + 8);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_free, 1);
+        mbar_init(s_free, 128);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&s_full[h], 1);
+            mbar_init(&p_full[h], 128);
+            mbar_init(&o_done[h], 1);
+            mbar_init(&o_free[h], 128);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1 && lane == 0) {
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+        tma_prefetch_desc(&tmq);
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    chunk_layout<BN, NT>(p, space, reinterpret_cast<long long *>(join));
+    const uint32_t tmem = *tmem_slot;
+    tc_fence_after();
+
+    // Waits of the ring of parts: they go on after an abort, when every role still goes through
+    // the parts (without work), so that the pieces of split units are all counted.
+    volatile int never = 0;
+    auto ring_wait = [&](uint64_t *bar, int use) {
+        return __all_sync(FULL, mbar_wait_for(bar, (uint32_t)(use & 1), &never, kLongWaitNs));
+    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return warp_wait(bar, parity, abort_flag, p.wait_ns);
+    };
+    auto wait_long = [&](uint64_t *bar, uint32_t parity) {
+        return warp_wait(bar, parity, abort_flag, p.wait_ns < kWaitDeadlineNs ? p.wait_ns : kLongWaitNs);
+    };
+
+    if (warp < SW0) {
+        regs_dec<72>();
+        if (warp <= 1) {
+            // -------------------------------------------------------- producers of K and V
+            const bool is_k = warp == 0;
+            const CUtensorMap *map = is_k ? &tmk : &tmv;
+            uint8_t *ring = is_k ? sK : sV;
+            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+            const int stages = is_k ? KS : VS;
+            const int ps = p.ps, box = ps < BN ? ps : BN, bpt = BN / box;
+            const int oob = p.num_pages * ps;  // a slot past the cache: TMA fills zeros
+            constexpr int LA = 4;  // page-table entries are read this many tiles ahead
+            int st = 0, issued = 0;
+            uint32_t ph = 1;  // parity of the stage's last release; the first round passes
+            bool ok = true;
+            for (int i = 0; ring_wait(&part_full[i % NR], i / NR); ++i) {
+                TcPart *pt = &parts[i % NR];
+                const int n = pt->n;
+                if (n == 0) break;
+                const int end = pt->L + pt->tok0 + pt->ntok, head = pt->head, x0 = pt->x0;
+                const int32_t *table = p.page_table + (size_t)pt->b * p.max_pages;
+                // page id and slot offset of this lane's box of tile x (id -1: no token)
+                auto fetch = [&](int x, int &id, int &off) {
+                    const long long tok = (long long)(x0 + x) * BN + lane * box;
+                    id = -1;
+                    off = 0;
+                    if (lane < bpt && x < n && tok < end) {
+                        const int page = (int)(tok / ps);
+                        off = (int)(tok - (long long)page * ps);
+                        id = __ldg(table + page);
+                        if (is_k && (id < 0 || id >= p.num_pages)) atomicMin(&pt->bad, (int)tok);
+                    }
+                };
+                int id[LA], off[LA];
+#pragma unroll
+                for (int q = 0; q < LA; ++q) fetch(q, id[q], off[q]);
+                for (int j0 = 0; ok && j0 < n; j0 += LA) {
+#pragma unroll
+                    for (int q = 0; q < LA; ++q) {
+                        if (!ok || j0 + q >= n) break;
+                        if (!(ok = wait_long(&empty[st], ph))) break;
+                        const int at = id[q] < 0 || id[q] >= p.num_pages ? oob : id[q] * ps + off[q];
+                        if (lane == 0) mbar_arrive_expect_tx(&full[st], TILE);
+                        if (lane < bpt) {
+#pragma unroll
+                            for (int dh = 0; dh < 2; ++dh)
+                                tma_load_3d(ring + st * TILE + dh * COL + lane * box * 128, map, dh * 64,
+                                            head, at, &full[st]);
+                        }
+                        __syncwarp();
+                        ++issued;
+                        if (++st == stages) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                        fetch(j0 + q + LA, id[q], off[q]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&part_empty[i % NR]);
+            }
+            if (lane == 0) {
+                // never leave with copies in flight: the last fill of every stage
+                for (int s = 0; s < stages && s < issued; ++s)
+                    mbar_wait_for(&full[s], (uint32_t)(((issued - 1 - s) / stages) & 1), &never,
+                                  kWaitDeadlineNs);
+            }
+        } else if (warp == 2) {
+            // -------------------------------------------------------- the issuer
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, false, false);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD, false, true);
+            const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+            int ks = 0, vs = 0;              // stages of the next QK and the next PV
+            uint32_t kph = 0, vph = 0;
+            int s_uses = 0;                  // products into S so far
+            int pv[2] = {0, 0};              // PVs of each half so far
+            int blocks[2] = {0, 0};          // parts whose O each half began
+            bool ok = true;
+            // a PV that is still to be issued: of half 0 (single-half tiles) or half 1
+            int pend = -1, pend_first = 0, pend_zero = 0;
+            auto issue_pv = [&](int h, int first, int zero) {
+                // V is there; P is written; O may restart
+                if (!(ok = ok && wait(&v_full[vs], vph))) return;
+                if (zero > 0) {
+                    // the block's last tile: rows from its end to the end of their page
+                    // may hold anything
+                    const int ps = p.ps, box = ps < BN ? ps : BN, r0 = BN - zero;
+                    const int r1 = (r0 + box - 1) / box * box;
+                    uint8_t *vsm = sV + vs * TILE;
+                    for (int i = r0 * 16 + lane; i < r1 * 16; i += 32)
+                        *reinterpret_cast<uint4 *>(vsm + ((i & 15) >> 3) * COL + (i >> 4) * 128 +
+                                                   (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (first) {
+                    if (blocks[h] > 0 &&
+                        !(ok = wait_long(&o_free[h], (uint32_t)((blocks[h] - 1) & 1))))
+                        return;
+                    ++blocks[h];
+                }
+                if (!(ok = wait(&p_full[h], (uint32_t)(pv[h] & 1)))) return;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t d = tmem + tO + h * 128, a = tmem + tP + h * 64;
+                    const uint32_t v = aV + (uint32_t)vs * TILE;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts(d, a + kk * 8, smem_desc_sw128(v + kk * 2048, COL, 1024), idesc_pv,
+                                (!first || kk > 0) ? 1u : 0u);
+                    umma_commit(&o_done[h]);
+                }
+                __syncwarp();
+                ++pv[h];
+            };
+            auto v_through = [&] {  // the tile's last PV is issued
+                if (lane == 0) umma_commit(&v_empty[vs]);
+                __syncwarp();
+                if (++vs == VS) {
+                    vs = 0;
+                    vph ^= 1;
+                }
+            };
+            auto flush = [&] {
+                if (pend >= 0 && ok) {
+                    issue_pv(pend, pend_first, pend == 1 ? 0 : pend_zero);
+                    if (ok) v_through();
+                }
+                pend = -1;
+            };
+            auto issue_qk = [&](int h) {
+                if (s_uses > 0 && !(ok = ok && wait(s_free, (uint32_t)((s_uses - 1) & 1)))) return;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t q = aQ + h * TILE, k = aK + (uint32_t)ks * TILE;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t o = (kk >> 2) * COL + (kk & 3) * 32;
+                        umma_ss(tmem + tS, smem_desc_sw128(q + o, 16, 1024),
+                                smem_desc_sw128(k + o, 16, 1024), idesc_qk, kk > 0);
+                    }
+                    umma_commit(&s_full[h]);
+                }
+                __syncwarp();
+                ++s_uses;
+            };
+            for (int i = 0; ring_wait(&part_full[i % NR], i / NR); ++i) {
+                const TcPart *pt = &parts[i % NR];
+                const int n = pt->n, two = pt->two;
+                if (n == 0) break;
+                // tokens of the unit's last tile that the block does not see
+                const int over = (int)((long long)pt->t * BN - (pt->L + pt->tok0 + pt->ntok));
+                const bool ends = pt->x0 + n == pt->t;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&part_empty[i % NR]);
+                if (!ok) continue;
+                flush();
+                ok = ok && wait_long(q_full, (uint32_t)(i & 1));
+                for (int j = 0; ok && j < n; ++j) {
+                    const int first = j == 0, zero = ends && j == n - 1 ? over : 0;
+                    if (!(ok = wait(&k_full[ks], kph))) break;
+                    auto k_through = [&] {  // the tile's last QK is issued
+                        if (lane == 0) {
+                            umma_commit(&k_empty[ks]);
+                            if (j == n - 1) umma_commit(q_free);
+                        }
+                        __syncwarp();
+                        if (++ks == KS) {
+                            ks = 0;
+                            kph ^= 1;
+                        }
+                    };
+                    issue_qk(0);
+                    if (!ok) break;
+                    if (!two) k_through();
+                    flush();
+                    if (!ok) break;
+                    if (two) {
+                        issue_qk(1);
+                        if (!ok) break;
+                        k_through();
+                        issue_pv(0, first, zero);
+                        if (!ok) break;
+                    }
+                    pend = two;
+                    pend_first = first;
+                    pend_zero = zero;
+                }
+            }
+            flush();
+            if (*abort_flag && lane == 0) {
+                umma_commit(drain);
+                mbar_wait_for(drain, 0, &never, kWaitDeadlineNs);
+            }
+            __syncwarp();
+        } else {
+            // -------------------------------------------------------- the planner
+            ChunkSeg g;
+            bool more = chunk_first<BN>(p, *space, g), ended = false, ok = true;
+            int posted = 0, loaded = 0, q_loads = 0;
+            const ChunkSpace sp = *space;
+            for (;;) {
+                while (!ended && posted < loaded + NR - 1) {
+                    TcPart *pt = &parts[posted % NR];
+                    if (posted >= NR && !ring_wait(&part_empty[posted % NR], posted / NR - 1)) {
+                        ended = true;
+                        break;
+                    }
+                    if (lane == 0) {
+                        TcPart w = {};
+                        if (more) {
+                            w.b = g.b;
+                            w.head = g.hb * p.S + hl;
+                            w.tok0 = g.k * p.TB;
+                            w.row = g.row0 + w.tok0;
+                            w.ntok = min(p.TB, g.n - w.tok0);
+                            w.L = g.L;
+                            w.x0 = (int)(g.x0 - g.pu);
+                            w.n = (int)(g.x1 - g.x0);
+                            w.t = g.t;
+                            w.cf = chunk_group_of(g.pu, sp.T, sp.C);
+                            w.cl = chunk_group_of(g.pu + g.t - 1, sp.T, sp.C);
+                            w.slot = 2 * blockIdx.x + (g.x0 == sp.s ? 0 : 1);
+                            w.first_slot = chunk_start(w.cf, sp.T, sp.C) < g.pu ? 1 : 0;
+                            w.two = w.ntok > p.TB / 2;
+                            w.bad = kPieceFine;
+                        }
+                        *pt = w;
+                        mbar_arrive(&part_full[posted % NR]);
+                    }
+                    __syncwarp();
+                    ++posted;
+                    if (!more) ended = true;
+                    else more = chunk_next<BN>(p, sp, g);
+                }
+                if (loaded >= posted - (ended ? 1 : 0)) break;
+                const TcPart *pt = &parts[loaded % NR];
+                if (ok && loaded > 0) ok = wait_long(q_free, (uint32_t)((loaded - 1) & 1));
+                if (ok && lane == 0) {
+                    const int half = p.TB / 2;
+                    mbar_arrive_expect_tx(q_full, (pt->two ? 2u : 1u) * 2u * 128u * (uint32_t)(half * p.G));
+                    for (int h = 0; h <= pt->two; ++h)
+#pragma unroll
+                        for (int dh = 0; dh < 2; ++dh)
+                            tma_load_3d(sQ + h * TILE + dh * COL, &tmq, dh * 64, pt->head * p.G,
+                                        pt->row + h * half, q_full);
+                }
+                __syncwarp();
+                q_loads += ok;
+                ++loaded;
+            }
+            // (after an abort nobody may have waited for the last Q)
+            if (q_loads > 0 && lane == 0)
+                mbar_wait_for(q_full, (uint32_t)((q_loads - 1) & 1), &never, kWaitDeadlineNs);
+            __syncwarp();
+        }
+    } else {
+        regs_inc<216>();
+        // ------------------------------------------------------------ softmax
+        const int h = (warp - SW0) >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;           // row of the half
+        const int st = threadIdx.x - 32 * SW0;       // 0 .. 255
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t aS = tmem + lane_off + tS, aP = tmem + lane_off + tP + h * 64;
+        const uint32_t aO = tmem + lane_off + tO + h * 128;
+        const float sl2 = p.scale_log2;
+        const int half_tok = p.TB / 2, half_rows = half_tok * p.G;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+
+        chunk_status<HD, __nv_bfloat16>(p, st, 256,
+                                        [&](bool v) { return bar_or(kBarBoth, 256, v) != 0; });
+
+        bool ok = true;
+        int cnt = 0;    // tiles of this half so far
+        for (int i = 0; ring_wait(&part_full[i % NR], i / NR); ++i) {
+            const volatile TcPart *pt = &parts[i % NR];
+            const int n = pt->n;
+            if (n == 0) break;
+            const int two = pt->two;
+            if (h == 1 && !two) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&part_empty[i % NR]);
+                continue;
+            }
+            const int L = pt->L, x0 = pt->x0, tok0 = pt->tok0, ntok = pt->ntok;
+            const int ltok = r / p.G;                // token of the row in its half
+            const int tok = h * half_tok + ltok;     // and in the block
+            const bool row_valid = r < half_rows && tok < ntok;
+            const int see = row_valid ? L + tok0 + tok : 0x7fffffff;
+            const bool live = __any_sync(FULL, row_valid);
+            float m_ref = -INFINITY, l = 0.0f;
+            for (int jl = 0; ok && jl < n; ++jl, ++cnt) {
+                if (!(ok = wait(&s_full[h], (uint32_t)(cnt & 1)))) break;
+                if (!live) {  // padding of the half: its rows are not looked at
+                    mbar_arrive(s_free);
+                    if (cnt > 0 && !(ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1)))) break;
+                    mbar_arrive(&p_full[h]);
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t v[BN];
+                tmem_ld32(aS, v);
+                tmem_ld32(aS + 32, v + 32);
+                tmem_ld32(aS + 64, v + 64);
+                tmem_ld32(aS + 96, v + 96);
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive(s_free);
+                const int lim = see - (x0 + jl) * BN;  // columns up to it are visible
+                if (__any_sync(FULL, lim < BN - 1)) {
+#pragma unroll
+                    for (int c = 0; c < BN; ++c) v[c] = c <= lim ? v[c] : 0xff800000u;
+                }
+                float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < BN; c += 8) {
+                    m0 = fmax3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                    m1 = fmax3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+                    m2 = fmax3(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+                    m3 = fmax3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
+                }
+                const float mx = fmax3(m0, m1, fmaxf(m2, m3)) * sl2;
+                // P of the tile before was read, O is final up to it
+                if (cnt > 0 && !(ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1)))) break;
+                // lazy rescale: move the reference only when the maximum grows by > 2^8
+                const bool need = mx > m_ref + tc::kRescaleThreshold;
+                if (__any_sync(FULL, need)) {
+                    const float alpha = need ? ex2_approx(m_ref - mx) : 1.0f;
+                    if (need) {
+                        l *= alpha;
+                        m_ref = mx;
+                    }
+                    if (jl > 0) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(aO + c * 16, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st16(aO + c * 16, o);
+                        }
+                    }
+                }
+                const float mneg = m_ref == -INFINITY ? 0.0f : -m_ref;
+                const float2 sc2 = make_float2(sl2, sl2), mn2 = make_float2(mneg, mneg);
+                float2 rs = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c4 = 0; c4 < 4; ++c4) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const int e = c4 * 32 + 2 * c;
+                        const float2 y = ffma2(make_float2(__uint_as_float(v[e]),
+                                                           __uint_as_float(v[e + 1])), sc2, mn2);
+                        const float2 pp = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        rs = fadd2(rs, pp);
+                        pk[c] = pack_bf16x2(pp.x, pp.y);
+                    }
+                    tmem_st16(aP + c4 * 16, pk);
+                }
+                tmem_wait_st();
+                l += rs.x + rs.y;
+                tc_fence_before();
+                mbar_arrive(&p_full[h]);
+            }
+            // ---- the end of the part: O after its last PV
+            if (ok) ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1));
+            tc_fence_after();
+            const int head = pt->head, cf = pt->cf, cl = pt->cl, slot = pt->slot;
+            const int first_slot = pt->first_slot, bad = pt->bad, b = pt->b, qrow0 = pt->row;
+            const bool split = cf != cl;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float ls = l == 0.0f ? -INFINITY : m_ref + __log2f(l);
+            const size_t row = ((size_t)(qrow0 + tok)) * p.Hq + (size_t)head * p.G + r % p.G;
+            const int lr = h * 128 + r;
+            // tokens of this part that the row does not see?
+            const int seen_to = (int)min((long long)(x0 + n) * BN, (long long)L + tok0 + ntok);
+            const bool masked = row_valid && seen_to > see + 1;
+            float odd = 0.0f;  // NaN if the row holds a value that is not finite
+            if (!split) {
+                const bool zero = !ok || see >= bad;
+#pragma unroll 1
+                for (int c64 = 0; c64 < 2; ++c64) {
+                    uint32_t o[64];
+                    if (ok) {
+                        tmem_ld32(aO + c64 * 64, o);
+                        tmem_ld32(aO + c64 * 64 + 32, o + 32);
+                        tmem_wait_ld();
+                    }
+                    if (zero) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) o[e] = 0;
+                    }
+                    if (row_valid) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) {
+                            odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+                        }
+                        uint4 *op = reinterpret_cast<uint4 *>(out + row * HD + c64 * 64);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            op[k] = eight_bf16(o + 8 * k);
+                    }
+                }
+                if (row_valid && p.lse) p.lse[row] = zero ? 0.0f : ls * 0.69314718055994531f;
+            } else {
+                float4 *dst = p.part + (size_t)slot * (HD / 4) * p.slot_rows;
+#pragma unroll 1
+                for (int c32 = 0; c32 < 4; ++c32) {
+                    uint32_t o[32];
+                    if (ok) {
+                        tmem_ld32(aO + c32 * 32, o);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+                    if (row_valid) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float f[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                f[e] = __uint_as_float(o[4 * k + e]);
+                                odd = fmaf(f[e], 0.0f, odd);
+                                f[e] *= inv;
+                            }
+                            __stcg(dst + (size_t)(c32 * 8 + k) * p.slot_rows + lr,
+                                   make_float4(f[0], f[1], f[2], f[3]));
+                        }
+                    }
+                }
+                if (row_valid) __stcg(p.part_lse + (size_t)slot * p.slot_rows + lr, ok ? ls : -INFINITY);
+            }
+            // O may restart
+            tc_fence_before();
+            mbar_arrive(&o_free[h]);
+            // rows that a masked token may have reached: again, without it
+            unsigned again = __ballot_sync(FULL, ok && masked && odd != 0.0f && see < bad);
+            __syncwarp();
+            while (again) {
+                const int rl = __ffs(again) - 1;
+                again &= again - 1;
+                const size_t at = __shfl_sync(FULL, (unsigned long long)row, rl);
+                const int last = __shfl_sync(FULL, see, rl);
+                float lse2;
+                const float4 o = row_again(p, b, head, at, x0 * BN, min(seen_to, last + 1), &lse2);
+                if (!split) {
+                    *reinterpret_cast<uint2 *>(out + at * HD + lane * 4) =
+                        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                    if (lane == 0 && p.lse) p.lse[at] = lse2 * 0.69314718055994531f;
+                } else {
+                    const int lr2 = h * 128 + quarter * 32 + rl;
+                    __stcg(p.part + ((size_t)slot * (HD / 4) + lane) * p.slot_rows + lr2, o);
+                    if (lane == 0) __stcg(p.part_lse + (size_t)slot * p.slot_rows + lr2, lse2);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&part_empty[i % NR]);
+            if (!split) continue;
+            // ---- a piece: count it, and join the unit's pieces if it was the last
+            const int nthr = two ? 256 : 128, id = two ? kBarBoth : kBarHalf;
+            const int F = cl - cf + 1;
+            __threadfence();
+            const int lost_here = bar_or(id, nthr, !ok);
+            if (st == 0) {
+                __stcg(p.part_bad + slot, lost_here ? kPieceLost : bad);
+                __threadfence();
+                int *counter = p.counters + cf * p.S + hl;
+                const int before = atomicAdd(counter, 1);
+                if (before == F - 1) *counter = 0;
+                *s_last = before == F - 1;
+                __threadfence();
+            }
+            const int mine = bar_or(id, nthr, st == 0 && *s_last);
+            if (!mine) continue;
+            auto slot_of = [&](int f) {
+                return 2 * ((cf + f) * p.S + hl) + (f == 0 ? first_slot : 0);
+            };
+            int lost = kPieceFine;
+            for (int f = 0; f < F; ++f) lost = min(lost, __ldcg(p.part_bad + slot_of(f)));
+            const int M = ntok * p.G;  // rows of the block
+            auto place = [&](int m) {  // where row m of the block is in a piece
+                return m < half_rows ? m : 128 + m - half_rows;
+            };
+            for (int m = st; m < M; m += nthr) {
+                const int at = place(m);
+                float mx = -INFINITY, sum = 0.0f;
+                for (int f = 0; f < F; ++f)
+                    mx = fmaxf(mx, __ldcg(p.part_lse + (size_t)slot_of(f) * p.slot_rows + at));
+                for (int f = 0; f < F; ++f) {
+                    const float v = __ldcg(p.part_lse + (size_t)slot_of(f) * p.slot_rows + at);
+                    sum += v == -INFINITY ? 0.0f : ex2_approx(v - mx);
+                }
+                const float all = mx + __log2f(sum);
+                join[m] = all;
+                const bool zero = L + tok0 + m / p.G >= lost;
+                if (p.lse)
+                    p.lse[(size_t)(qrow0 + m / p.G) * p.Hq + (size_t)head * p.G + m % p.G] =
+                        zero ? 0.0f : all * 0.69314718055994531f;
+            }
+            bar_or(id, nthr, 0);
+            for (int it = st; it < M * (HD / 4); it += nthr) {
+                const int m = it % M, c = it / M, at = place(m);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (L + tok0 + m / p.G < lost) {
+                    const float all = join[m];
+                    for (int f0 = 0; f0 < F; f0 += 4) {
+                        float w[4];
+                        float4 a[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            w[u] = -INFINITY;
+                            a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (f0 + u < F) {
+                                const int sl = slot_of(f0 + u);
+                                w[u] = __ldcg(p.part_lse + (size_t)sl * p.slot_rows + at);
+                                a[u] = __ldcg(p.part + ((size_t)sl * (HD / 4) + c) * p.slot_rows + at);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if (w[u] == -INFINITY) continue;
+                            const float e = ex2_approx(w[u] - all);
+                            acc.x = fmaf(e, a[u].x, acc.x);
+                            acc.y = fmaf(e, a[u].y, acc.y);
+                            acc.z = fmaf(e, a[u].z, acc.z);
+                            acc.w = fmaf(e, a[u].w, acc.w);
+                        }
+                    }
+                }
+                const size_t orow = (size_t)(qrow0 + m / p.G) * p.Hq + (size_t)head * p.G + m % p.G;
+                *reinterpret_cast<uint2 *>(out + orow * HD + c * 4) =
+                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+            }
+            bar_or(id, nthr, 0);  // join[] is used again
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    // ---- CTAs that gave up: the last CTA of the call, to which every status word is visible,
+    // adds the bit for the sequences they had tiles of
+    if (threadIdx.x == 0) {
+        if (*abort_flag && space->s < space->e) {
+            ChunkSeg g;
+            chunk_first<BN>(p, *space, g);
+            const int b0 = g.b;
+            while (chunk_next<BN>(p, *space, g)) {}
+            p.gave_up[2 * blockIdx.x] = b0;
+            p.gave_up[2 * blockIdx.x + 1] = g.b < p.B ? g.b : p.B - 1;
+            atomicOr(p.done + 2 + blockIdx.x / 32, 1 << (blockIdx.x & 31));
+            atomicOr(p.done + 1, 1);
+        }
+        __threadfence();
+        if (atomicAdd(p.done, 1) == (int)gridDim.x - 1) {
+            __threadfence();
+            p.done[0] = 0;
+            if (atomicExch(p.done + 1, 0)) {
+                for (int c = 0; c < (int)gridDim.x; ++c)
+                    if (atomicAnd(p.done + 2 + c / 32, ~(1 << (c & 31))) >> (c & 31) & 1)
+                        for (int b = __ldcg(p.gave_up + 2 * c); b <= __ldcg(p.gave_up + 2 * c + 1); ++b)
+                            atomicOr(p.status + b, SVF_DEV_TIMEOUT);
+            }
+        }
+    }
+}
+
+// K or V cache [num_pages * page_size tokens][Hkv][128] as a 3-D map; boxes of 64 dims x 1 head
+// x one page (at most 128 tokens), 128-byte swizzle.
+bool make_cache_map(CUtensorMap *map, const void *base, int num_pages, int page_size, int Hkv) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)ct::HD, (cuuint64_t)Hkv,
+                          (cuuint64_t)num_pages * (cuuint64_t)page_size};
+    cuuint64_t strides[2] = {(cuuint64_t)ct::HD * 2, (cuuint64_t)Hkv * ct::HD * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)(page_size < ct::BN ? page_size : ct::BN)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q [rows][Hq][128]: boxes of 64 dims x G heads x floor(128 / G) tokens, the rows (token, head) of
+// a half.
+bool make_rows_map(CUtensorMap *map, const void *q, int rows, int Hq, int G) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)ct::HD, (cuuint64_t)Hq, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)ct::HD * 2, (cuuint64_t)Hq * ct::HD * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkParams &p, int ctas, cudaStream_t stream) {
+    CUtensorMap tmk, tmv, tmq;
+    if (!make_cache_map(&tmk, p.k_cache, p.num_pages, p.ps, p.Hkv) ||
+        !make_cache_map(&tmv, p.v_cache, p.num_pages, p.ps, p.Hkv) ||
+        !make_rows_map(&tmq, p.q, p.rows, p.Hq, p.G))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(
+        chunk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem::kDynamic);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(chunk_tc_kernel, dim3((unsigned)ctas), dim3(ct::NT), (size_t)TcSmem::kDynamic,
+                      stream, 0u, tmk, tmv, tmq, p);
+}
+
+}  // namespace svf

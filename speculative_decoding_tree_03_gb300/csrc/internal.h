@@ -132,6 +132,65 @@ struct RopeKvArgs {
 bool rope_kv_supported(int T, int Hq, int Hkv, int D, int rot, int elem_size);
 cudaError_t launch_rope_kv(const RopeKvArgs &a, cudaStream_t stream);
 
+// Sequences that share pages (pages_shared.cu).
+struct PageForkArgs {
+    int32_t *page_table;
+    const int32_t *free_pages;
+    int32_t *pool_state, *shares, *seq_lens;
+    const int32_t *src, *dst;
+    int32_t *copy_src, *copy_dst, *copy_len, *status;
+    int B, F, max_pages, page_size, num_pages;
+};
+struct PageCopyArgs {
+    void *k_cache, *v_cache;
+    int num_layers;
+    long long layer_stride;  // elements
+    int num_pages, page_size, Hkv, D, elem_size, n;
+    const int32_t *src, *dst, *lens;
+    int32_t *status;
+};
+cudaError_t launch_page_fork(const PageForkArgs &a, cudaStream_t stream);
+cudaError_t launch_page_copy(const PageCopyArgs &a, cudaStream_t stream);
+cudaError_t launch_page_release_shared(const PageReleaseArgs &a, int32_t *shares,
+                                       cudaStream_t stream);
+
+// Per-head norms, rotary positions on several axes and the K/V write (norm_rope.cu).
+struct NormRopeArgs {
+    RopeKvArgs rope;
+    const void *q_norm, *k_norm;
+    const int32_t *pair_axis;
+    int axes;
+    float eps;
+};
+bool norm_rope_supported(int T, int Hq, int Hkv, int D, int rot, int axes, int elem_size);
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
+
+// Attention of chunks of new tokens over the paged cache (chunk.cu; fp32 in
+// chunk_simt.cu, bf16 in chunk_tc.cu). launch_chunk returns an svf_status.
+struct ChunkArgs {
+    const void *q, *k_cache, *v_cache;
+    int num_pages, page_size;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *seq_lens, *row_offsets;
+    int B, rows, Hq, Hkv, D, dtype;
+    float sm_scale;
+    void *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t *status;
+};
+struct ChunkParams;
+bool chunk_supported(int rows, int B, int Hq, int Hkv, int D, int dtype, int page_size);
+size_t chunk_workspace_bytes(int rows, int Hq, int Hkv, int D, int dtype);
+int launch_chunk(const ChunkArgs &a, cudaStream_t stream);
+cudaError_t launch_chunk_simt(const ChunkParams &p, int D, int ctas, cudaStream_t stream);
+cudaError_t launch_chunk_tc(const ChunkParams &p, int ctas, cudaStream_t stream);
+// Test hook: the deadline of the bf16 kernel's waits (ns; 0 or less restores
+// the default of 2 s).
+void chunk_set_wait_ns(long long ns);
+
 // Arguments of one tree-attention call, shared by both attention kernels.
 struct AttnArgs {
     const void *q;

@@ -23,6 +23,7 @@
 // 4 us, 1024 9 us, 4096 50 us, 8192, the most, 167 us).
 #include "common.cuh"
 #include "internal.h"
+#include "page_math.cuh"
 
 namespace svf {
 
@@ -34,15 +35,6 @@ constexpr int kKept = 4;  // ids that a thread of a release keeps in registers
 
 // state[0] free pages; state[1] tickets and state[2] the largest served I_b of
 // the call in flight (both zero between calls).
-__device__ __forceinline__ int sat_add(int a, int b, int cap) {
-    // 0 <= a, b <= cap < 2^30: associative, so the order of a sum does not matter
-    return min(a + b, cap);
-}
-
-__device__ __forceinline__ int pages_of(int tokens, int ps) {
-    return tokens / ps + (tokens % ps != 0);
-}
-
 struct ReserveArgs {
     int32_t *table;
     const int32_t *seq_lens, *new_lens, *depth;

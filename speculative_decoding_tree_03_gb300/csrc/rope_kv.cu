@@ -22,6 +22,7 @@
 // 1984 rows of 64 + 8 + 8 heads (82 MB) 14.1 us, 86 % of a copy.
 #include "common.cuh"
 #include "internal.h"
+#include "vec16.cuh"
 
 namespace svf {
 
@@ -41,39 +42,6 @@ struct RopeArgs {
     int J;           // items of a head: two 16-byte vectors each
     int pairs;       // the first `pairs` of them are rotated
     int HG;          // heads that a block covers at once
-};
-
-template <typename T>
-struct Vec;
-template <>
-struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void load(uint4 r, float *f) {
-        f[0] = __uint_as_float(r.x);
-        f[1] = __uint_as_float(r.y);
-        f[2] = __uint_as_float(r.z);
-        f[3] = __uint_as_float(r.w);
-    }
-    static __device__ __forceinline__ uint4 store(const float *f) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
-    }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void load(uint4 r, float *f) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-    static __device__ __forceinline__ uint4 store(const float *f) {
-        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                          pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-    }
 };
 
 // block: J * HG threads, thread (j, hs) = item j of heads hs, hs + HG, ...;
