@@ -10,8 +10,8 @@
 // One S serves both halves in turn: the softmax warps of a half take it into registers at
 // once and give it back, so that the next product never waits for their arithmetic. In the
 // steady state one thread issues
-//     QK_0(j)  PV_1(j-1)  QK_1(j)  PV_0(j)  QK_0(j+1) ...
-// and each half has the time of two products of the other one for its softmax. A thread sustains
+//     QK_1(j)  PV_0(j-1)  QK_0(j+1)  PV_1(j-1) ...
+// so that a half finds its next scores ready when it is through with a tile. A thread sustains
 // N = 128 products at the tensor cores' full rate (64 cycles for M = N = 128, K = 16), so one
 // issuing thread is enough; N = 64 takes nearly as long (59), hence 128 tokens to a tile.
 //
@@ -59,7 +59,7 @@ struct TcPart {
     int first_slot;                // piece 0's: 1 if the unit is not the first of its group
     int two;                       // both halves have rows
     int bad;                       // first token whose page is not in the cache
-    int pad;
+    int clear;                     // the last tile reaches behind the block's last token
 };
 
 struct TcSmem {
@@ -67,7 +67,7 @@ struct TcSmem {
     static constexpr int kK = kQ + 2 * ct::TILE;
     static constexpr int kV = kK + ct::KS * ct::TILE;
     static constexpr int kBar = kV + ct::VS * ct::TILE;
-    static constexpr int kNumBars = 2 * ct::KS + 2 * ct::VS + 2 * ct::NR + 2 + 1 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kNumBars = 2 * ct::KS + 2 * ct::VS + 2 * ct::NR + 3 + 4 * 2 + ct::VS + 1;
     static constexpr int kMisc = kBar + ((kNumBars * 8 + 127) / 128) * 128;
     static constexpr int kSpace = kMisc + 64;
     static constexpr int kParts = kSpace + 64;
@@ -98,6 +98,16 @@ __device__ __forceinline__ uint4 eight_bf16(const uint32_t *o) {
     for (int i = 0; i < 4; ++i)
         w[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 template <int N>
@@ -171,7 +181,8 @@ __global__ void __launch_bounds__(ct::NT, 1)
     uint64_t *p_full = s_full + 2;            // [2] P of the half is written
     uint64_t *o_done = p_full + 2;            // [2] P V of the half is done
     uint64_t *o_free = o_done + 2;            // [2] O of the half was read out
-    uint64_t *drain = o_free + 2;             // the issuer's products done, after an abort
+    uint64_t *v_clear = o_free + 2;           // [VS] rows of the stage behind a block's last token are cleared
+    uint64_t *drain = v_clear + VS;           // the issuer's products done, after an abort
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kMisc + 4);
     int *s_last = reinterpret_cast<int *>(smem + S::kMisc + 8);
@@ -190,6 +201,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
         for (int i = 0; i < VS; ++i) {
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
+            mbar_init(&v_clear[i], 1);
         }
         for (int i = 0; i < NR; ++i) {
             mbar_init(&part_full[i], 1);
@@ -232,8 +244,9 @@ __global__ void __launch_bounds__(ct::NT, 1)
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return warp_wait(bar, parity, abort_flag, p.wait_ns);
     };
+    const unsigned long long long_ns = p.wait_ns < kWaitDeadlineNs ? p.wait_ns : kLongWaitNs;
     auto wait_long = [&](uint64_t *bar, uint32_t parity) {
-        return warp_wait(bar, parity, abort_flag, p.wait_ns < kWaitDeadlineNs ? p.wait_ns : kLongWaitNs);
+        return warp_wait(bar, parity, abort_flag, long_ns);
     };
 
     if (warp < SW0) {
@@ -305,137 +318,140 @@ __global__ void __launch_bounds__(ct::NT, 1)
             }
         } else if (warp == 2) {
             // -------------------------------------------------------- the issuer
-            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, false, false);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD, false, true);
-            const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
-            int ks = 0, vs = 0;              // stages of the next QK and the next PV
-            uint32_t kph = 0, vph = 0;
-            int s_uses = 0;                  // products into S so far
-            int pv[2] = {0, 0};              // PVs of each half so far
-            int blocks[2] = {0, 0};          // parts whose O each half began
-            bool ok = true;
-            // a PV that is still to be issued: of half 0 (single-half tiles) or half 1
-            int pend = -1, pend_first = 0, pend_zero = 0;
-            auto issue_pv = [&](int h, int first, int zero) {
-                // V is there; P is written; O may restart
-                if (!(ok = ok && wait(&v_full[vs], vph))) return;
-                if (zero > 0) {
-                    // the block's last tile: rows from its end to the end of their page
-                    // may hold anything
-                    const int ps = p.ps, box = ps < BN ? ps : BN, r0 = BN - zero;
-                    const int r1 = (r0 + box - 1) / box * box;
-                    uint8_t *vsm = sV + vs * TILE;
-                    for (int i = r0 * 16 + lane; i < r1 * 16; i += 32)
-                        *reinterpret_cast<uint4 *>(vsm + ((i & 15) >> 3) * COL + (i >> 4) * 128 +
-                                                   (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (first) {
-                    if (blocks[h] > 0 &&
-                        !(ok = wait_long(&o_free[h], (uint32_t)((blocks[h] - 1) & 1))))
-                        return;
-                    ++blocks[h];
-                }
-                if (!(ok = wait(&p_full[h], (uint32_t)(pv[h] & 1)))) return;
-                tc_fence_after();
-                if (lane == 0) {
+            // one elected thread: the compiler sees that it is alone and issues a product in
+            // 64 cycles (under `lane == 0` each takes about 100, whatever its size)
+            if (elect_one()) {
+                constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, false, false);
+                constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD, false, true);
+                const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+                const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
+                const uint64_t dV = smem_desc_sw128(smem_u32(sV), COL, 1024);
+                int ks = 0, vs = 0;              // stages of the next QK and the next PV
+                uint32_t kph = 0, vph = 0, sph = 1;
+                uint32_t zph = 0;                // bit s: parity of the stage's next clearing
+                uint32_t pvph = 0;               // bit h: parity of the half's next PV
+                uint32_t began = 0, oph = 3;     // bit h: the half had a part; parity of O's release
+                bool ok = true, s_used = false;
+                auto one = [&](uint64_t *bar, uint32_t parity) {
+                    return mbar_wait_for(bar, parity, abort_flag, p.wait_ns);
+                };
+                auto one_long = [&](uint64_t *bar, uint32_t parity) {
+                    return mbar_wait_for(bar, parity, abort_flag, long_ns);
+                };
+                // PVs that are still to be issued, oldest lowest: half, first of its part, last
+                // of its tile, rows of V to wait for
+                constexpr int kEntry = 4;
+                uint32_t queue = 0;
+                int waiting = 0;
+                auto issue_pv = [&] {
+                    const uint32_t e = queue & ((1u << kEntry) - 1);
+                    queue >>= kEntry;
+                    --waiting;
+                    const uint32_t h = e & 1;
+                    const bool first = e >> 1 & 1;
+                    if (!(ok = ok && one(&v_full[vs], vph))) return;
+                    if (e >> 3 & 1) {  // rows behind the block's end are cleared
+                        if (!(ok = one(&v_clear[vs], zph >> vs & 1))) return;
+                        zph ^= 1u << vs;
+                    }
+                    if (first) {  // O of the half's last part was read out
+                        if ((began >> h & 1) && !(ok = one_long(&o_free[h], oph >> h & 1))) return;
+                        began |= 1u << h;
+                        oph ^= 1u << h;
+                    }
+                    if (!(ok = one(&p_full[h], pvph >> h & 1))) return;
+                    pvph ^= 1u << h;
+                    tc_fence_after();
                     const uint32_t d = tmem + tO + h * 128, a = tmem + tP + h * 64;
-                    const uint32_t v = aV + (uint32_t)vs * TILE;
+                    const uint64_t v = dV + (uint64_t)(vs * (TILE >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(d, a + kk * 8, smem_desc_sw128(v + kk * 2048, COL, 1024), idesc_pv,
-                                (!first || kk > 0) ? 1u : 0u);
+                        umma_ts(d, a + kk * 8, v + (kk * 2048 >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
                     umma_commit(&o_done[h]);
-                }
-                __syncwarp();
-                ++pv[h];
-            };
-            auto v_through = [&] {  // the tile's last PV is issued
-                if (lane == 0) umma_commit(&v_empty[vs]);
-                __syncwarp();
-                if (++vs == VS) {
-                    vs = 0;
-                    vph ^= 1;
-                }
-            };
-            auto flush = [&] {
-                if (pend >= 0 && ok) {
-                    issue_pv(pend, pend_first, pend == 1 ? 0 : pend_zero);
-                    if (ok) v_through();
-                }
-                pend = -1;
-            };
-            auto issue_qk = [&](int h) {
-                if (s_uses > 0 && !(ok = ok && wait(s_free, (uint32_t)((s_uses - 1) & 1)))) return;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t q = aQ + h * TILE, k = aK + (uint32_t)ks * TILE;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t o = (kk >> 2) * COL + (kk & 3) * 32;
-                        umma_ss(tmem + tS, smem_desc_sw128(q + o, 16, 1024),
-                                smem_desc_sw128(k + o, 16, 1024), idesc_qk, kk > 0);
-                    }
-                    umma_commit(&s_full[h]);
-                }
-                __syncwarp();
-                ++s_uses;
-            };
-            for (int i = 0; ring_wait(&part_full[i % NR], i / NR); ++i) {
-                const TcPart *pt = &parts[i % NR];
-                const int n = pt->n, two = pt->two;
-                if (n == 0) break;
-                // tokens of the unit's last tile that the block does not see
-                const int over = (int)((long long)pt->t * BN - (pt->L + pt->tok0 + pt->ntok));
-                const bool ends = pt->x0 + n == pt->t;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&part_empty[i % NR]);
-                if (!ok) continue;
-                flush();
-                ok = ok && wait_long(q_full, (uint32_t)(i & 1));
-                for (int j = 0; ok && j < n; ++j) {
-                    const int first = j == 0, zero = ends && j == n - 1 ? over : 0;
-                    if (!(ok = wait(&k_full[ks], kph))) break;
-                    auto k_through = [&] {  // the tile's last QK is issued
-                        if (lane == 0) {
-                            umma_commit(&k_empty[ks]);
-                            if (j == n - 1) umma_commit(q_free);
+                    if (e >> 2 & 1) {
+                        umma_commit(&v_empty[vs]);
+                        if (++vs == VS) {
+                            vs = 0;
+                            vph ^= 1;
                         }
-                        __syncwarp();
+                    }
+                };
+                for (int i = 0; mbar_wait_for(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs);
+                     ++i) {
+                    const TcPart *pt = &parts[i % NR];
+                    const int n = pt->n, two = pt->two;
+                    if (n == 0) break;
+                    const uint32_t clear = pt->clear;
+                    mbar_arrive(&part_empty[i % NR]);
+                    while (ok && waiting > 0) issue_pv();
+                    if (!(ok = ok && one_long(q_full, (uint32_t)(i & 1)))) continue;
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (!(ok = one(&k_full[ks], kph))) break;
+                        for (int h = 0; h <= two; ++h) {
+                            if (s_used && !(ok = one(s_free, sph))) break;
+                            s_used = true;
+                            sph ^= 1;
+                            tc_fence_after();
+                            const uint64_t q = dQ + (uint64_t)(h * (TILE >> 4));
+                            const uint64_t k = dK + (uint64_t)(ks * (TILE >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const uint32_t o = ((kk >> 2) * COL + (kk & 3) * 32) >> 4;
+                                umma_ss(tmem + tS, q + o, k + o, idesc_qk, kk > 0);
+                            }
+                            umma_commit(&s_full[h]);
+                            if (h == two) {
+                                umma_commit(&k_empty[ks]);
+                                if (j == n - 1) umma_commit(q_free);
+                            }
+                            // a half that takes its next S has written P: the PV of that tile,
+                            // now that the other half has its next product on the way
+                            if (waiting == 2 + two) issue_pv();
+                            if (!ok) break;
+                            const uint32_t e = (uint32_t)h | (j == 0 ? 2u : 0u) | (h == two ? 4u : 0u) |
+                                               (h == 0 && j == n - 1 ? clear << 3 : 0u);
+                            queue |= e << (kEntry * waiting);
+                            ++waiting;
+                        }
                         if (++ks == KS) {
                             ks = 0;
                             kph ^= 1;
                         }
-                    };
-                    issue_qk(0);
-                    if (!ok) break;
-                    if (!two) k_through();
-                    flush();
-                    if (!ok) break;
-                    if (two) {
-                        issue_qk(1);
-                        if (!ok) break;
-                        k_through();
-                        issue_pv(0, first, zero);
-                        if (!ok) break;
                     }
-                    pend = two;
-                    pend_first = first;
-                    pend_zero = zero;
                 }
-            }
-            flush();
-            if (*abort_flag && lane == 0) {
-                umma_commit(drain);
-                mbar_wait_for(drain, 0, &never, kWaitDeadlineNs);
+                while (ok && waiting > 0) issue_pv();
+                if (*abort_flag) {
+                    umma_commit(drain);
+                    mbar_wait_for(drain, 0, &never, kWaitDeadlineNs);
+                }
             }
             __syncwarp();
         } else {
             // -------------------------------------------------------- the planner
             ChunkSeg g;
             bool more = chunk_first<BN>(p, *space, g), ended = false, ok = true;
-            int posted = 0, loaded = 0, q_loads = 0;
+            int posted = 0, loaded = 0, q_loads = 0, tiles = 0;
+            // The rows of V behind the last token of a part, whose last tile is the tiles-th: up
+            // to the end of their page they may hold anything. Called when the part's QKs
+            // are done: then the softmax has taken the scores of the tile before, after the PV
+            // of the tile VS before the last, so v_full's phase is that tile's or the last's.
+            auto clear = [&](const TcPart *pt) {
+                tiles += pt->n;
+                if (!pt->clear) return;
+                const int vs = (tiles - 1) % VS, use = (tiles - 1) / VS;
+                if (ok && (ok = wait_long(&v_full[vs], (uint32_t)(use & 1)))) {
+                    const int ps = p.ps, box = ps < BN ? ps : BN;
+                    const int r0 = (int)((long long)pt->L + pt->tok0 + pt->ntok - (long long)(pt->t - 1) * BN);
+                    const int r1 = (r0 + box - 1) / box * box;
+                    uint8_t *vsm = sV + vs * TILE;
+                    for (int i = r0 * 16 + lane; i < r1 * 16; i += 32)
+                        *reinterpret_cast<uint4 *>(vsm + ((i & 15) >> 3) * COL + (i >> 4) * 128 +
+                                                   (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_clear[vs]);
+            };
             const ChunkSpace sp = *space;
             for (;;) {
                 while (!ended && posted < loaded + NR - 1) {
@@ -462,6 +478,8 @@ __global__ void __launch_bounds__(ct::NT, 1)
                             w.first_slot = chunk_start(w.cf, sp.T, sp.C) < g.pu ? 1 : 0;
                             w.two = w.ntok > p.TB / 2;
                             w.bad = kPieceFine;
+                            w.clear = w.x0 + w.n == w.t &&
+                                      (long long)w.t * BN > (long long)w.L + w.tok0 + w.ntok;
                         }
                         *pt = w;
                         mbar_arrive(&part_full[posted % NR]);
@@ -485,7 +503,13 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 }
                 __syncwarp();
                 q_loads += ok;
+                // (the part before is still in the ring: at most NR - 1 are ahead of it)
+                if (loaded > 0) clear(&parts[(loaded - 1) % NR]);
                 ++loaded;
+            }
+            if (loaded > 0) {
+                if (ok) ok = wait_long(q_free, (uint32_t)((loaded - 1) & 1));
+                clear(&parts[(loaded - 1) % NR]);
             }
             // (after an abort nobody may have waited for the last Q)
             if (q_loads > 0 && lane == 0)
@@ -558,49 +582,44 @@ __global__ void __launch_bounds__(ct::NT, 1)
                     m3 = fmax3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
                 }
                 const float mx = fmax3(m0, m1, fmaxf(m2, m3)) * sl2;
-                // P of the tile before was read, O is final up to it
-                if (cnt > 0 && !(ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1)))) break;
                 // lazy rescale: move the reference only when the maximum grows by > 2^8
                 const bool need = mx > m_ref + tc::kRescaleThreshold;
-                if (__any_sync(FULL, need)) {
-                    const float alpha = need ? ex2_approx(m_ref - mx) : 1.0f;
-                    if (need) {
-                        l *= alpha;
-                        m_ref = mx;
-                    }
-                    if (jl > 0) {
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(aO + c * 16, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st16(aO + c * 16, o);
-                        }
-                    }
+                const float alpha = need ? ex2_approx(m_ref - mx) : 1.0f;
+                if (need) {
+                    l *= alpha;
+                    m_ref = mx;
                 }
                 const float mneg = m_ref == -INFINITY ? 0.0f : -m_ref;
                 const float2 sc2 = make_float2(sl2, sl2), mn2 = make_float2(mneg, mneg);
                 float2 rs = make_float2(0.0f, 0.0f);
+                uint32_t pk[BN / 2];
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int e = c4 * 32 + 2 * c;
-                        const float2 y = ffma2(make_float2(__uint_as_float(v[e]),
-                                                           __uint_as_float(v[e + 1])), sc2, mn2);
-                        const float2 pp = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                        rs = fadd2(rs, pp);
-                        pk[c] = pack_bf16x2(pp.x, pp.y);
-                    }
-                    tmem_st16(aP + c4 * 16, pk);
+                for (int c = 0; c < BN / 2; ++c) {
+                    const float2 y = ffma2(make_float2(__uint_as_float(v[2 * c]),
+                                                       __uint_as_float(v[2 * c + 1])), sc2, mn2);
+                    const float2 pp = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                    rs = fadd2(rs, pp);
+                    pk[c] = pack_bf16x2(pp.x, pp.y);
                 }
-                tmem_wait_st();
                 l += rs.x + rs.y;
+                // P of the tile before was read, O is final up to it
+                if (cnt > 0 && !(ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1)))) break;
+                if (jl > 0 && __any_sync(FULL, need)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(aO + c * 16, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st16(aO + c * 16, o);
+                    }
+                }
+                tmem_st32(aP, pk);
+                tmem_st32(aP + 32, pk + 32);
+                tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&p_full[h]);
             }
