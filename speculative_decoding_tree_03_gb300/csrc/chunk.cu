@@ -13,7 +13,7 @@ namespace {
 std::atomic<long long> g_wait_ns{0};
 
 struct Plan {
-    int ctas, S, rows_per_block, TB, min_tiles, slot_rows;
+    int ctas, S, rows_per_block, TB, min_tiles, lead, slot_rows;
     size_t done, gave_up, part_bad, part_lse, part, total;
 };
 
@@ -38,11 +38,13 @@ Plan plan_of(int rows, int Hq, int Hkv, int D, int dtype) {
         c.TB = 2 * (128 / G);
         c.rows_per_block = 256;
         c.min_tiles = 1;
+        c.lead = 6;
     } else {
         most = num_sms() * (D == 64 ? 3 : 1);  // CTAs whose shared memory fits an SM
         c.TB = 64 / G;
         c.rows_per_block = 64;
         c.min_tiles = 2;
+        c.lead = 1;
     }
     if (most > kChunkMaxCtas) most = kChunkMaxCtas;
     c.S = group_heads(Hkv, most);
@@ -104,6 +106,7 @@ int launch_chunk(const ChunkArgs &a, cudaStream_t stream) {
     p.NHB = a.Hkv / c.S;
     p.groups = c.ctas / c.S;
     p.min_tiles = c.min_tiles;
+    p.lead = c.lead;
     const float scale = a.sm_scale > 0.0f ? a.sm_scale : 1.0f / sqrtf((float)a.D);
     p.scale_log2 = scale * 1.4426950408889634f;
     const long long ns = g_wait_ns.load();

@@ -6,16 +6,18 @@
 //     tiles(b, k) = ceil((L_b + min((k + 1) TB, n_b)) / BN).
 // A unit is (sequence, KV head, block). The CTAs form groups of S, one CTA per KV head of a
 // head block (S = Hkv where that fills the GPU), whose CTAs go through the same token ranges
-// side by side: a token's row of the cache holds all heads. The units' tiles are laid end to
+// side by side: a token's row of the cache holds all heads. The units' tiles, with `lead` more in
+// front of each for what a unit costs besides (its Q, its output), are laid end to
 // end, sequence by sequence (its head blocks, their row blocks), T in all, and group c of C
-// takes tiles [cT/C, (c+1)T/C): every CTA the same number of tiles, whether the call is one
-// token after a long context or a prompt of thousands. The lengths are on the device only, so
+// takes [cT/C, (c+1)T/C): every CTA the same work, whether the call is one token after a long
+// context or a prompt of thousands. The lengths are on the device only, so
 // every CTA lays the space out by itself: the sum over a sequence's blocks has the closed
 // form floor_sum, and sequences are summed by all threads.
 //
 // A unit inside one group is written as final output. Of a unit split between groups each
 // piece is written as normalised fp32 rows with their log2-sum-exp to the workspace and
-// counted; whoever counts last joins the pieces in their order,
+// counted (a piece has tiles: one that ends in the lead is none); whoever counts last joins the
+// pieces in their order,
 //     out = sum_f w_f O_f,  w_f = 2^(lse_f - max) / sum,
 // so nobody waits for another CTA, and the result does not depend on who it was. A split unit
 // is the last of the group that holds its first tile, so one counter per CTA is enough;
@@ -41,6 +43,7 @@ struct ChunkParams {
     int S, NHB;    // heads of a group; head blocks (S * NHB = Hkv)
     int groups;    // groups of the grid
     int min_tiles; // a group has at least this many tiles, or there are fewer groups
+    int lead;      // tiles that a unit's beginning and end are worth
     float scale_log2;
     unsigned long long wait_ns;
     int *counters;     // [kChunkMaxCtas] zero between calls
@@ -101,14 +104,14 @@ __device__ __forceinline__ int chunk_tiles(const ChunkParams &p, const ChunkSeq 
     return (int)((end + BN - 1) / BN);
 }
 
-// Tiles of the first k row blocks of a sequence, for one head.
+// Length of the first k row blocks of a sequence in the tile space, for one head.
 template <int BN>
 __device__ __forceinline__ long long chunk_tiles_before(const ChunkParams &p, const ChunkSeq &s,
                                                         int k) {
     const int full = min(k, s.n / p.TB);
-    long long t = 0;
+    long long t = (long long)k * p.lead;
     if (full > 0)
-        t = floor_sum(full, BN, (unsigned)p.TB,
+        t += floor_sum(full, BN, (unsigned)p.TB,
                       (unsigned long long)s.L + (unsigned)p.TB + (unsigned)(BN - 1));
     if (k > full) t += ((long long)s.L + s.n + BN - 1) / BN;
     return t;
@@ -128,10 +131,10 @@ struct ChunkSpace {
     int b, hb, k;       // that unit
 };
 
-// A part [x0, x1) of one unit's tiles, the unit beginning at pu.
+// A part [x0, x1) of one unit's length, the unit beginning at pu: `lead` and then its t tiles.
 struct ChunkSeg {
     long long pu, x0, x1;
-    int b, hb, k, t;  // t: tiles of the unit
+    int b, hb, k, t;
     int L, n, row0;
 };
 
@@ -141,6 +144,20 @@ __device__ __forceinline__ long long chunk_start(int c, long long T, int C) {
 }
 __device__ __forceinline__ int chunk_group_of(long long x, long long T, int C) {
     return (int)(((x + 1) * (long long)C - 1) / T);
+}
+
+// The part's first tile, and how many it has (0: it ends in the unit's lead, nothing to do).
+__device__ __forceinline__ int chunk_part(const ChunkParams &p, const ChunkSeg &g, int &first) {
+    const long long at = g.pu + p.lead;
+    first = (int)max(g.x0 - at, 0ll);
+    return (int)max(g.x1 - at, 0ll) - first;
+}
+
+// The groups with the first and the last tile of a unit.
+__device__ __forceinline__ void chunk_groups(const ChunkParams &p, const ChunkSpace &sp,
+                                             const ChunkSeg &g, int &cf, int &cl) {
+    cf = chunk_group_of(g.pu + p.lead, sp.T, sp.C);
+    cl = chunk_group_of(g.pu + p.lead + g.t - 1, sp.T, sp.C);
 }
 
 // Lays out the tile space; all NT threads of the CTA, which meet in it. `wsum` is
@@ -247,7 +264,7 @@ __device__ __forceinline__ bool chunk_first(const ChunkParams &p, const ChunkSpa
     g.pu = sp.pu;
     g.t = chunk_tiles<BN>(p, q, g.k);
     g.x0 = sp.s;
-    g.x1 = min(g.pu + g.t, sp.e);
+    g.x1 = min(g.pu + p.lead + g.t, sp.e);
     return true;
 }
 
@@ -275,7 +292,7 @@ __device__ __forceinline__ bool chunk_next(const ChunkParams &p, const ChunkSpac
     g.pu = g.x1;
     g.x0 = g.x1;
     g.t = chunk_tiles<BN>(p, q, g.k);
-    g.x1 = min(g.pu + g.t, sp.e);
+    g.x1 = min(g.pu + p.lead + g.t, sp.e);
     return true;
 }
 

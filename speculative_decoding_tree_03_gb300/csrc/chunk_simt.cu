@@ -56,9 +56,11 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
     const float *V = static_cast<const float *>(p.v_cache);
     float *out = static_cast<float *>(p.out);
     ChunkSeg g;
-    int segi = 0;
     for (bool more = chunk_first<BN>(p, sm.space, g); more;
-         more = chunk_next<BN>(p, sm.space, g), ++segi) {
+         more = chunk_next<BN>(p, sm.space, g)) {
+        int x0;
+        const int tiles = chunk_part(p, g, x0);
+        if (tiles == 0) continue;
         const int head = g.hb * p.S + blockIdx.x % p.S;
         const int tok0 = g.k * p.TB, ntok = min(p.TB, g.n - tok0);
         const int M = ntok * p.G;  // rows of the block
@@ -85,8 +87,8 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
 #pragma unroll
             for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.0f;
         }
-        for (long long xt = g.x0; xt < g.x1; ++xt) {
-            const int t0 = (int)(xt - g.pu) * BN;
+        for (int xt = x0; xt < x0 + tiles; ++xt) {
+            const int t0 = xt * BN;
             const int tend = g.L + tok0 + ntok;  // tokens that the block sees
             __syncthreads();
             if (tid < BN) {
@@ -196,7 +198,8 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
             ls[i] = l[i] == 0.0f ? -INFINITY : m[i] + log2f(l[i]);
         }
         const ChunkSpace &sp = sm.space;
-        const int cf = chunk_group_of(g.pu, sp.T, sp.C), cl = chunk_group_of(g.pu + g.t - 1, sp.T, sp.C);
+        int cf, cl;
+        chunk_groups(p, sp, g, cf, cl);
         auto row_at = [&](int r) {
             return (size_t)(g.row0 + tok0 + r / p.G) * p.Hq + head * p.G + r % p.G;
         };

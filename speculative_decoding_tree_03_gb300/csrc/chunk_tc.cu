@@ -100,6 +100,13 @@ __device__ __forceinline__ uint4 eight_bf16(const uint32_t *o) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 32 bytes in one store: a lane of a warp that writes a row each fills whole sectors.
+__device__ __forceinline__ void store32(void *p, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile(
@@ -157,6 +164,70 @@ __device__ __noinline__ float4 row_again(const ChunkParams &p, int b, int head, 
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *lse2 = l == 0.0f ? -INFINITY : m + __log2f(l);
     return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+// The thread that fills the ring of K or of V.
+struct Producer {
+    const CUtensorMap *map;
+    uint8_t *ring;
+    uint64_t *full, *empty;
+    int stages, st, issued;
+    uint32_t ph;  // parity of the stage's last release; the first round passes
+    unsigned long long ns;
+    volatile int *abort;
+    bool ok;
+};
+
+// The tiles of a part, BPT boxes each: pages of 128 / BPT tokens, or (1) of a multiple of 128.
+// Page-table entries are read two tiles ahead. `bad` gets the first token of the part whose
+// page is not in the cache.
+template <int BPT>
+__device__ __forceinline__ void load_part(const ChunkParams &p, Producer &w, const TcPart &pt, int *bad) {
+    using namespace ct;
+    constexpr int BOX = BN / BPT;
+    const int n = pt.n, x0 = pt.x0, head = pt.head, end = pt.L + pt.tok0 + pt.ntok;
+    const int32_t *table = p.page_table + (size_t)pt.b * p.max_pages;
+    const int oob = p.num_pages * p.ps;  // a slot past the cache: TMA fills zeros
+    // slots of tile x's boxes
+    auto fetch = [&](int x, int *slot) {
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) {
+            const unsigned tok = (unsigned)(x0 + x) * BN + i * BOX;
+            slot[i] = oob;
+            if (x < n && tok < (unsigned)end) {
+                const unsigned page = tok / (BPT == 1 ? (unsigned)p.ps : (unsigned)BOX);
+                const int id = __ldg(table + page);
+                if (id >= 0 && id < p.num_pages)
+                    slot[i] = id * p.ps + (BPT == 1 ? (int)(tok - page * (unsigned)p.ps) : 0);
+                else if (bad)
+                    atomicMin(bad, (int)tok);
+            }
+        }
+    };
+    int slot[2][BPT];
+    fetch(0, slot[0]);
+    fetch(1, slot[1]);
+    for (int j0 = 0; w.ok && j0 < n; j0 += 2) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (!w.ok || j0 + q >= n) break;
+            if (!(w.ok = mbar_wait_for(&w.empty[w.st], w.ph, w.abort, w.ns))) break;
+            uint64_t *full = &w.full[w.st];
+            uint8_t *stage = w.ring + w.st * TILE;
+            mbar_arrive_expect_tx(full, TILE);
+#pragma unroll
+            for (int i = 0; i < BPT; ++i) {
+                tma_load_3d(stage + i * BOX * 128, w.map, 0, head, slot[q][i], full);
+                tma_load_3d(stage + COL + i * BOX * 128, w.map, 64, head, slot[q][i], full);
+            }
+            ++w.issued;
+            if (++w.st == w.stages) {
+                w.st = 0;
+                w.ph ^= 1;
+            }
+            fetch(j0 + q + 2, slot[q]);
+        }
+    }
 }
 
 __global__ void __launch_bounds__(ct::NT, 1)
@@ -253,69 +324,30 @@ __global__ void __launch_bounds__(ct::NT, 1)
         regs_dec<72>();
         if (warp <= 1) {
             // -------------------------------------------------------- producers of K and V
-            const bool is_k = warp == 0;
-            const CUtensorMap *map = is_k ? &tmk : &tmv;
-            uint8_t *ring = is_k ? sK : sV;
-            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
-            const int stages = is_k ? KS : VS;
-            const int ps = p.ps, box = ps < BN ? ps : BN, bpt = BN / box;
-            const int oob = p.num_pages * ps;  // a slot past the cache: TMA fills zeros
-            constexpr int LA = 4;  // page-table entries are read this many tiles ahead
-            int st = 0, issued = 0;
-            uint32_t ph = 1;  // parity of the stage's last release; the first round passes
-            bool ok = true;
-            for (int i = 0; ring_wait(&part_full[i % NR], i / NR); ++i) {
-                TcPart *pt = &parts[i % NR];
-                const int n = pt->n;
-                if (n == 0) break;
-                const int end = pt->L + pt->tok0 + pt->ntok, head = pt->head, x0 = pt->x0;
-                const int32_t *table = p.page_table + (size_t)pt->b * p.max_pages;
-                // page id and slot offset of this lane's box of tile x (id -1: no token)
-                auto fetch = [&](int x, int &id, int &off) {
-                    const long long tok = (long long)(x0 + x) * BN + lane * box;
-                    id = -1;
-                    off = 0;
-                    if (lane < bpt && x < n && tok < end) {
-                        const int page = (int)(tok / ps);
-                        off = (int)(tok - (long long)page * ps);
-                        id = __ldg(table + page);
-                        if (is_k && (id < 0 || id >= p.num_pages)) atomicMin(&pt->bad, (int)tok);
-                    }
-                };
-                int id[LA], off[LA];
-#pragma unroll
-                for (int q = 0; q < LA; ++q) fetch(q, id[q], off[q]);
-                for (int j0 = 0; ok && j0 < n; j0 += LA) {
-#pragma unroll
-                    for (int q = 0; q < LA; ++q) {
-                        if (!ok || j0 + q >= n) break;
-                        if (!(ok = wait_long(&empty[st], ph))) break;
-                        const int at = id[q] < 0 || id[q] >= p.num_pages ? oob : id[q] * ps + off[q];
-                        if (lane == 0) mbar_arrive_expect_tx(&full[st], TILE);
-                        if (lane < bpt) {
-#pragma unroll
-                            for (int dh = 0; dh < 2; ++dh)
-                                tma_load_3d(ring + st * TILE + dh * COL + lane * box * 128, map, dh * 64,
-                                            head, at, &full[st]);
-                        }
-                        __syncwarp();
-                        ++issued;
-                        if (++st == stages) {
-                            st = 0;
-                            ph ^= 1;
-                        }
-                        fetch(j0 + q + LA, id[q], off[q]);
-                    }
+            // one elected thread each, as for the issuer: a box takes a third of what it
+            // takes a lane of several
+            if (elect_one()) {
+                const bool is_k = warp == 0;
+                Producer w = {is_k ? &tmk : &tmv, is_k ? sK : sV, is_k ? k_full : v_full,
+                              is_k ? k_empty : v_empty, is_k ? KS : VS, 0, 0, 1u, long_ns, abort_flag, true};
+                const int bpt = p.ps < BN ? BN / p.ps : 1;
+                for (int i = 0; mbar_wait_for(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs);
+                     ++i) {
+                    TcPart *pt = &parts[i % NR];
+                    if (pt->n == 0) break;
+                    int *bad = is_k ? &pt->bad : nullptr;
+                    if (bpt == 8) load_part<8>(p, w, *pt, bad);
+                    else if (bpt == 4) load_part<4>(p, w, *pt, bad);
+                    else if (bpt == 2) load_part<2>(p, w, *pt, bad);
+                    else load_part<1>(p, w, *pt, bad);
+                    mbar_arrive(&part_empty[i % NR]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&part_empty[i % NR]);
-            }
-            if (lane == 0) {
                 // never leave with copies in flight: the last fill of every stage
-                for (int s = 0; s < stages && s < issued; ++s)
-                    mbar_wait_for(&full[s], (uint32_t)(((issued - 1 - s) / stages) & 1), &never,
+                for (int s = 0; s < w.stages && s < w.issued; ++s)
+                    mbar_wait_for(&w.full[s], (uint32_t)(((w.issued - 1 - s) / w.stages) & 1), &never,
                                   kWaitDeadlineNs);
             }
+            __syncwarp();
         } else if (warp == 2) {
             // -------------------------------------------------------- the issuer
             // one elected thread: the compiler sees that it is alone and issues a product in
@@ -326,100 +358,104 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
                 const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
                 const uint64_t dV = smem_desc_sw128(smem_u32(sV), COL, 1024);
-                int ks = 0, vs = 0;              // stages of the next QK and the next PV
+                uint32_t ks = 0, vs = 0;              // stages of the next QK and the next PV
                 uint32_t kph = 0, vph = 0, sph = 1;
                 uint32_t zph = 0;                // bit s: parity of the stage's next clearing
-                uint32_t pvph = 0;               // bit h: parity of the half's next PV
-                uint32_t began = 0, oph = 3;     // bit h: the half had a part; parity of O's release
-                bool ok = true, s_used = false;
+                uint32_t pph = 0;
+                uint32_t oph = 3;     // bit h: the half had a part; parity of O's release
+                bool ok = true;
                 auto one = [&](uint64_t *bar, uint32_t parity) {
                     return mbar_wait_for(bar, parity, abort_flag, p.wait_ns);
                 };
                 auto one_long = [&](uint64_t *bar, uint32_t parity) {
                     return mbar_wait_for(bar, parity, abort_flag, long_ns);
                 };
-                // PVs that are still to be issued, oldest lowest: half, first of its part, last
-                // of its tile, rows of V to wait for
-                constexpr int kEntry = 4;
-                uint32_t queue = 0;
-                int waiting = 0;
-                auto issue_pv = [&] {
-                    const uint32_t e = queue & ((1u << kEntry) - 1);
-                    queue >>= kEntry;
-                    --waiting;
-                    const uint32_t h = e & 1;
-                    const bool first = e >> 1 & 1;
+            // S = Q_h K^T of the tile in K's stage ks, once S was taken
+            auto issue_qk = [&](const uint32_t h, bool last_of_tile, bool last_of_part) {
+                if (!(ok = ok && one(s_free, sph))) return;
+                sph ^= 1;
+                tc_fence_after();
+                const uint64_t q = dQ + h * (TILE >> 4), k = dK + ks * (TILE >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t o = ((kk >> 2) * COL + (kk & 3) * 32) >> 4;
+                    umma_ss(tmem + tS, q + o, k + o, idesc_qk, kk > 0);
+                }
+                umma_commit(&s_full[h]);
+                if (last_of_tile) {
+                    umma_commit(&k_empty[ks]);
+                    if (last_of_part) umma_commit(q_free);
+                    if (++ks == KS) {
+                        ks = 0;
+                        kph ^= 1;
+                    }
+                }
+            };
+            // O_h (+)= P_h V of the tile in V's stage vs, once P is written; `cleared`: once the
+            // rows behind the block's end are cleared too
+            auto issue_pv = [&](const uint32_t h, bool first, bool last_of_tile, bool cleared, bool last) {
+                if (h == 0) {
                     if (!(ok = ok && one(&v_full[vs], vph))) return;
-                    if (e >> 3 & 1) {  // rows behind the block's end are cleared
+                    if (cleared) {
                         if (!(ok = one(&v_clear[vs], zph >> vs & 1))) return;
                         zph ^= 1u << vs;
                     }
-                    if (first) {  // O of the half's last part was read out
-                        if ((began >> h & 1) && !(ok = one_long(&o_free[h], oph >> h & 1))) return;
-                        began |= 1u << h;
-                        oph ^= 1u << h;
-                    }
-                    if (!(ok = one(&p_full[h], pvph >> h & 1))) return;
-                    pvph ^= 1u << h;
-                    tc_fence_after();
-                    const uint32_t d = tmem + tO + h * 128, a = tmem + tP + h * 64;
-                    const uint64_t v = dV + (uint64_t)(vs * (TILE >> 4));
+                }
+                if (first) {  // O of the half's last part was read out
+                    if (!(ok = ok && one(&o_free[h], oph >> h & 1))) return;
+                    oph ^= 1u << h;
+                }
+                // (the half gave back S of its next tile after it wrote P)
+                if (!(ok = ok && (!last || one(&p_full[h], pph >> h & 1)))) return;
+                pph ^= 1u << h;
+                tc_fence_after();
+                const uint32_t d = tmem + tO + h * 128, a = tmem + tP + h * 64;
+                const uint64_t v = dV + vs * (TILE >> 4);
+                umma_ts(d, a, v, idesc_pv, first ? 0u : 1u);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(d, a + kk * 8, v + (kk * 2048 >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
-                    umma_commit(&o_done[h]);
-                    if (e >> 2 & 1) {
-                        umma_commit(&v_empty[vs]);
-                        if (++vs == VS) {
-                            vs = 0;
-                            vph ^= 1;
-                        }
-                    }
-                };
-                for (int i = 0; mbar_wait_for(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs);
-                     ++i) {
-                    const TcPart *pt = &parts[i % NR];
-                    const int n = pt->n, two = pt->two;
-                    if (n == 0) break;
-                    const uint32_t clear = pt->clear;
-                    mbar_arrive(&part_empty[i % NR]);
-                    while (ok && waiting > 0) issue_pv();
-                    if (!(ok = ok && one_long(q_full, (uint32_t)(i & 1)))) continue;
-                    for (int j = 0; ok && j < n; ++j) {
-                        if (!(ok = one(&k_full[ks], kph))) break;
-                        for (int h = 0; h <= two; ++h) {
-                            if (s_used && !(ok = one(s_free, sph))) break;
-                            s_used = true;
-                            sph ^= 1;
-                            tc_fence_after();
-                            const uint64_t q = dQ + (uint64_t)(h * (TILE >> 4));
-                            const uint64_t k = dK + (uint64_t)(ks * (TILE >> 4));
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t o = ((kk >> 2) * COL + (kk & 3) * 32) >> 4;
-                                umma_ss(tmem + tS, q + o, k + o, idesc_qk, kk > 0);
-                            }
-                            umma_commit(&s_full[h]);
-                            if (h == two) {
-                                umma_commit(&k_empty[ks]);
-                                if (j == n - 1) umma_commit(q_free);
-                            }
-                            // a half that takes its next S has written P: the PV of that tile,
-                            // now that the other half has its next product on the way
-                            if (waiting == 2 + two) issue_pv();
-                            if (!ok) break;
-                            const uint32_t e = (uint32_t)h | (j == 0 ? 2u : 0u) | (h == two ? 4u : 0u) |
-                                               (h == 0 && j == n - 1 ? clear << 3 : 0u);
-                            queue |= e << (kEntry * waiting);
-                            ++waiting;
-                        }
-                        if (++ks == KS) {
-                            ks = 0;
-                            kph ^= 1;
-                        }
+                for (int kk = 1; kk < 8; ++kk)
+                    umma_ts(d, a + kk * 8, v + (kk * 2048 >> 4), idesc_pv, 1u);
+                umma_commit(&o_done[h]);
+                if (last_of_tile) {
+                    umma_commit(&v_empty[vs]);
+                    if (++vs == VS) {
+                        vs = 0;
+                        vph ^= 1;
                     }
                 }
-                while (ok && waiting > 0) issue_pv();
+            };
+            for (int i = 0; mbar_wait_for(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs); ++i) {
+                const int n = parts[i % NR].n, two = parts[i % NR].two;
+                const bool clear = parts[i % NR].clear;
+                if (n == 0) break;
+                mbar_arrive(&part_empty[i % NR]);
+                if (!(ok = ok && one(q_full, (uint32_t)(i & 1)))) continue;
+                // A half that takes its next S has written P: the PV of that tile follows, behind
+                // the other half's next product.
+                if (two) {
+                    ok = one(&k_full[ks], kph);
+                    issue_qk(0, false, false);
+                    for (int j = 0; ok && j < n; ++j) {
+                        issue_qk(1, true, j == n - 1);
+                        if (j > 0) issue_pv(0, j == 1, false, false, false);
+                        if (j + 1 < n) {
+                            ok = ok && one(&k_full[ks], kph);
+                            issue_qk(0, false, false);
+                        }
+                        if (j > 0) issue_pv(1, j == 1, true, false, j + 1 == n);
+                    }
+                    issue_pv(0, n == 1, false, clear, true);
+                    issue_pv(1, n == 1, true, false, true);
+                } else {
+                    for (int j = 0; ok && j < n + 2; ++j) {
+                        if (j < n) {
+                            ok = one(&k_full[ks], kph);
+                            issue_qk(0, true, j == n - 1);
+                        }
+                        if (j > 1) issue_pv(0, j == 2, true, clear && j == n + 1, j >= n);
+                    }
+                }
+            }
                 if (*abort_flag) {
                     umma_commit(drain);
                     mbar_wait_for(drain, 0, &never, kWaitDeadlineNs);
@@ -429,7 +465,13 @@ __global__ void __launch_bounds__(ct::NT, 1)
         } else {
             // -------------------------------------------------------- the planner
             ChunkSeg g;
-            bool more = chunk_first<BN>(p, *space, g), ended = false, ok = true;
+            // (a part that ends in its unit's lead has no tiles and is none)
+            auto with_tiles = [&](bool more) {
+                int first;
+                while (more && chunk_part(p, g, first) == 0) more = chunk_next<BN>(p, *space, g);
+                return more;
+            };
+            bool more = with_tiles(chunk_first<BN>(p, *space, g)), ended = false, ok = true;
             int posted = 0, loaded = 0, q_loads = 0, tiles = 0;
             // The rows of V behind the last token of a part, whose last tile is the tiles-th: up
             // to the end of their page they may hold anything. Called when the part's QKs
@@ -469,11 +511,9 @@ __global__ void __launch_bounds__(ct::NT, 1)
                             w.row = g.row0 + w.tok0;
                             w.ntok = min(p.TB, g.n - w.tok0);
                             w.L = g.L;
-                            w.x0 = (int)(g.x0 - g.pu);
-                            w.n = (int)(g.x1 - g.x0);
+                            w.n = chunk_part(p, g, w.x0);
                             w.t = g.t;
-                            w.cf = chunk_group_of(g.pu, sp.T, sp.C);
-                            w.cl = chunk_group_of(g.pu + g.t - 1, sp.T, sp.C);
+                            chunk_groups(p, sp, g, w.cf, w.cl);
                             w.slot = 2 * blockIdx.x + (g.x0 == sp.s ? 0 : 1);
                             w.first_slot = chunk_start(w.cf, sp.T, sp.C) < g.pu ? 1 : 0;
                             w.two = w.ntok > p.TB / 2;
@@ -487,7 +527,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
                     __syncwarp();
                     ++posted;
                     if (!more) ended = true;
-                    else more = chunk_next<BN>(p, sp, g);
+                    else more = with_tiles(chunk_next<BN>(p, sp, g));
                 }
                 if (loaded >= posted - (ended ? 1 : 0)) break;
                 const TcPart *pt = &parts[loaded % NR];
@@ -528,6 +568,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
         const float sl2 = p.scale_log2;
         const int half_tok = p.TB / 2, half_rows = half_tok * p.G;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+        const bool wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 
         chunk_status<HD, __nv_bfloat16>(p, st, 256,
                                         [&](bool v) { return bar_or(kBarBoth, 256, v) != 0; });
@@ -657,10 +698,16 @@ __global__ void __launch_bounds__(ct::NT, 1)
                             odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
                         }
-                        uint4 *op = reinterpret_cast<uint4 *>(out + row * HD + c64 * 64);
+                        __nv_bfloat16 *op = out + row * HD + c64 * 64;
+                        if (wide_out) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            op[k] = eight_bf16(o + 8 * k);
+                            for (int k = 0; k < 4; ++k)
+                                store32(op + 16 * k, eight_bf16(o + 16 * k), eight_bf16(o + 16 * k + 8));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                reinterpret_cast<uint4 *>(op)[k] = eight_bf16(o + 8 * k);
+                        }
                     }
                 }
                 if (row_valid && p.lse) p.lse[row] = zero ? 0.0f : ls * 0.69314718055994531f;
