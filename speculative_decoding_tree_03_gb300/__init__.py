@@ -206,7 +206,8 @@ def _load_fastcall(lib) -> None:
         return
     mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in
                (lib.svf_page_reserve, lib.svf_page_release, lib.svf_rope_kv_write,
-                lib.svf_lora_proj)))
+                lib.svf_lora_proj, lib.svf_page_release_shared, lib.svf_page_fork,
+                lib.svf_page_copy, lib.svf_norm_rope_kv_write, lib.svf_chunk_attn)))
     _fast = mod
 
 
@@ -931,10 +932,11 @@ def page_release(pool: dict, page_table: torch.Tensor, old_lens: torch.Tensor,
     when its last holder leaves it. Returns n_released [B], status [B]."""
     lib = _lib or load_library()
     shares = pool.get("shares")
-    if _fast is not None and outputs is not None and shares is None:
-        rc = _fast.page_release(pool, page_table, old_lens, keep_lens, page_size, outputs, stream)
+    if _fast is not None and outputs is not None:
+        fn = _fast.page_release if shares is None else _fast.page_release_shared
+        rc = fn(pool, page_table, old_lens, keep_lens, page_size, outputs, stream)
         if rc is not None:
-            _check(rc, "svf_page_release")
+            _check(rc, "svf_page_release" if shares is None else "svf_page_release_shared")
             return outputs
     dev, B, max_pages = _page_args(pool, page_table, old_lens, "old_lens", keep_lens, "keep_lens")
     free, i32 = pool["free"], torch.int32
@@ -972,6 +974,11 @@ def page_fork(pool: dict, page_table: torch.Tensor, seq_lens: torch.Tensor, src:
     (page_pool(..., shared=True)); page_table, seq_lens and the pool are updated in
     place. Returns device tensors copy_src, copy_dst, copy_len, status [F]."""
     lib = _lib or load_library()
+    if _fast is not None and outputs is not None:
+        rc = _fast.page_fork(pool, page_table, seq_lens, src, dst, page_size, outputs, stream)
+        if rc is not None:
+            _check(rc, "svf_page_fork")
+            return outputs
     if "shares" not in pool:
         raise SpecVerifyError("the pool has no 'shares': make it with page_pool(..., shared=True)")
     dev, B, max_pages = _page_args(pool, page_table, seq_lens, "seq_lens", seq_lens, "seq_lens")
@@ -1020,6 +1027,11 @@ def page_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor, d
     k_cache and v_cache [layers, num_pages, page_size, Hkv, D] (or without the layer
     axis). Returns status [n]."""
     lib = _lib or load_library()
+    if _fast is not None and status is not None:
+        rc = _fast.page_copy(k_cache, v_cache, src, dst, lens, status, stream)
+        if rc is not None:
+            _check(rc, "svf_page_copy")
+            return status
     dev, layers, stride, num_pages, page_size, Hkv, D = _layered(k_cache, v_cache)
     i32 = torch.int32
     n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
@@ -1127,6 +1139,12 @@ def norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     ``pair_axis`` [rot / 2] int32, the axis that turns each pair. The other arguments,
     the results and the rows that are left out are rope_kv_write's."""
     lib = _lib or load_library()
+    if _fast is not None and q_out is not None:
+        rc = _fast.norm_rope_kv_write(q, k, v, q_norm, k_norm, rope, positions, slots, k_cache,
+                                      v_cache, eps, pair_axis, q_out, interleaved, status, stream)
+        if rc is not None:
+            _check(rc, "svf_norm_rope_kv_write")
+            return q_out, status
     dev = _device_of(q, "q")
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4 or rope.dim() != 2:
         raise SpecVerifyError("q and k must be [T, heads, D], the caches [pages, page_size, Hkv, "
@@ -1188,6 +1206,12 @@ def chunk_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     D], lse [rows, Hq] float32 or None, status [B] int32); rows behind the last sequence
     keep what out and lse held (new ones: undefined)."""
     lib = _lib or load_library()
+    if _fast is not None and workspace is not None and (lse is not None or not want_lse):
+        rc = _fast.chunk_attn(q, k_cache, v_cache, page_table, seq_lens, row_offsets, sm_scale, out,
+                              lse, workspace, status, stream)
+        if rc is not None:
+            _check(rc, "svf_chunk_attn")
+            return out, lse, status
     dev = _device_of(q, "q")
     if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
         raise SpecVerifyError("q must be [rows, Hq, D], k_cache [pages, page_size, Hkv, D], "
