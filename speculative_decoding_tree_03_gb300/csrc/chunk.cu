@@ -56,7 +56,7 @@ Plan plan_of(int rows, int Hq, int Hkv, int D, int dtype) {
     c.done = kChunkMaxCtas * sizeof(int);  // the counters, and what else begins at zero, stay in place
     c.gave_up = kChunkHeadBytes;
     c.part_bad = up(c.gave_up + slots * sizeof(int), 256);
-    c.part_lse = up(c.part_bad + slots * sizeof(int), 256);
+    c.part_lse = up(c.part_bad + 2 * slots * sizeof(int), 256);
     c.part = up(c.part_lse + slots * c.slot_rows * sizeof(float), 256);
     c.total = c.part + slots * c.slot_rows * (size_t)D * sizeof(float);
     return c;

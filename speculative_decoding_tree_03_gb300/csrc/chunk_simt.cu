@@ -30,12 +30,12 @@ struct ChunkSmem {
     float k[BN][LDK];
     float v[BN][LDK];
     float p[BN][LDP];  // P transposed: [token][row]
-    float w[2][BM];    // the join: a row's maximum and 1 / sum
+    float w[BM];       // the join: a row's log2-sum-exp
     int page[BN];      // slot of each token of the tile, -1 without one
     int bad;           // first token of the part whose page is not in the cache
     int last;
     ChunkSpace space;
-    long long wsum[NT / 32];
+    ChunkCount sums[NT / 32];
 };
 
 __device__ __forceinline__ float ex2(float x) { return exp2f(x); }
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
     pdl_wait();
     pdl_launch_dependents();
     chunk_status<D, float>(p, tid, NT, [](bool v) { return __syncthreads_or(v) != 0; });
-    chunk_layout<BN, NT>(p, &sm.space, sm.wsum);
+    chunk_layout<BN, NT>(p, &sm.space, sm.sums);
     const float *Q = static_cast<const float *>(p.q);
     const float *K = static_cast<const float *>(p.k_cache);
     const float *V = static_cast<const float *>(p.v_cache);
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
     for (bool more = chunk_first<BN>(p, sm.space, g); more;
          more = chunk_next<BN>(p, sm.space, g)) {
         int x0;
-        const int tiles = chunk_part(p, g, x0);
+        const int tiles = chunk_part(sm.space, g, x0);
         if (tiles == 0) continue;
         const int head = g.hb * p.S + blockIdx.x % p.S;
         const int tok0 = g.k * p.TB, ntok = min(p.TB, g.n - tok0);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
         }
         const ChunkSpace &sp = sm.space;
         int cf, cl;
-        chunk_groups(p, sp, g, cf, cl);
+        chunk_groups(sp, g, cf, cl);
         auto row_at = [&](int r) {
             return (size_t)(g.row0 + tok0 + r / p.G) * p.Hq + head * p.G + r % p.G;
         };
@@ -233,12 +233,12 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
                                    o[i][4 * c + 2] * inv[i], o[i][4 * c + 3] * inv[i]));
             if (x == 0) __stcg(p.part_lse + (size_t)slot * p.slot_rows + r, ls[i]);
         }
-        if (tid == 0) __stcg(p.part_bad + slot, first_bad);
-        __threadfence();
+        if (tid == 0) __stcg(p.part_bad + 2 * slot, first_bad);
         __syncthreads();
         int *counter = p.counters + cf * p.S + blockIdx.x % p.S;
         const int F = cl - cf + 1;
         if (tid == 0) {
+            __threadfence();  // what the barrier made visible to this thread, too
             const int before = atomicAdd(counter, 1);
             sm.last = before == F - 1;
             if (before == F - 1) *counter = 0;
@@ -246,45 +246,9 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
         }
         __syncthreads();
         if (!sm.last) continue;
-        // ---- join the pieces
-        auto slot_of = [&](int f) {
-            return 2 * ((cf + f) * p.S + (int)(blockIdx.x % p.S)) +
-                   ((f == 0 && chunk_start(cf, sp.T, sp.C) < g.pu) ? 1 : 0);
-        };
-        int lost = kPieceFine;
-        for (int f = 0; f < F; ++f) lost = min(lost, __ldcg(p.part_bad + slot_of(f)));
-        if (tid < M) {
-            float mx = -INFINITY, sum = 0.0f;
-            for (int f = 0; f < F; ++f)
-                mx = fmaxf(mx, __ldcg(p.part_lse + (size_t)slot_of(f) * p.slot_rows + tid));
-            for (int f = 0; f < F; ++f) {
-                const float v = __ldcg(p.part_lse + (size_t)slot_of(f) * p.slot_rows + tid);
-                sum += v == -INFINITY ? 0.0f : ex2(v - mx);
-            }
-            sm.w[0][tid] = mx;
-            sm.w[1][tid] = 1.0f / sum;
-            const bool zero = g.L + tok0 + tid / p.G >= lost;
-            if (p.lse) p.lse[row_at(tid)] = zero ? 0.0f : (mx + log2f(sum)) * 0.69314718055994531f;
-        }
-        __syncthreads();
-        for (int i = tid; i < M * (D / 4); i += NT) {
-            const int r = i % M, c = i / M;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (g.L + tok0 + r / p.G < lost) {
-                for (int f = 0; f < F; ++f) {
-                    const int sl = slot_of(f);
-                    const float v = __ldcg(p.part_lse + (size_t)sl * p.slot_rows + r);
-                    if (v == -INFINITY) continue;
-                    const float w = ex2(v - sm.w[0][r]) * sm.w[1][r];
-                    const float4 a = __ldcg(p.part + ((size_t)sl * (D / 4) + c) * p.slot_rows + r);
-                    acc.x = fmaf(w, a.x, acc.x);
-                    acc.y = fmaf(w, a.y, acc.y);
-                    acc.z = fmaf(w, a.z, acc.z);
-                    acc.w = fmaf(w, a.w, acc.w);
-                }
-            }
-            *reinterpret_cast<float4 *>(out + row_at(r) * D + 4 * c) = acc;
-        }
+        const ChunkJoin jn = {F, cf, (int)(blockIdx.x % p.S), chunk_start(cf, sp.T, sp.C) < g.pu ? 1 : 0,
+                              M, M, 1, g.row0 + tok0, head, g.L + tok0, tid, NT, 0};
+        chunk_join<D, float>(p, jn, sm.w);
     }
 }
 

@@ -91,6 +91,12 @@ __device__ __forceinline__ int bar_or(int id, int n, int pred) {
     return (int)r;
 }
 
+// A wait of the roles that need few registers (not inlined: there are many).
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                       unsigned long long ns) {
+    return mbar_wait_for(bar, parity, abort, ns);
+}
+
 // Eight floats (as bits) as bf16.
 __device__ __forceinline__ uint4 eight_bf16(const uint32_t *o) {
     uint32_t w[4];
@@ -178,54 +184,50 @@ struct Producer {
     bool ok;
 };
 
-// The tiles of a part, BPT boxes each: pages of 128 / BPT tokens, or (1) of a multiple of 128.
-// Page-table entries are read two tiles ahead. `bad` gets the first token of the part whose
-// page is not in the cache.
-template <int BPT>
+// The tiles of a part, each in boxes of a page (at most 128 tokens). Page-table entries are read a
+// tile ahead. `bad` gets the first token of the part whose page is not in the cache.
 __device__ __forceinline__ void load_part(const ChunkParams &p, Producer &w, const TcPart &pt, int *bad) {
     using namespace ct;
-    constexpr int BOX = BN / BPT;
-    const int n = pt.n, x0 = pt.x0, head = pt.head, end = pt.L + pt.tok0 + pt.ntok;
+    constexpr int MAXB = BN / 16;
+    const int n = pt.n, x0 = pt.x0, head = pt.head, end = pt.L + pt.tok0 + pt.ntok, ps = p.ps;
+    const int box = ps < BN ? ps : BN, bpt = BN / box;
     const int32_t *table = p.page_table + (size_t)pt.b * p.max_pages;
-    const int oob = p.num_pages * p.ps;  // a slot past the cache: TMA fills zeros
+    const int oob = p.num_pages * ps;  // a slot past the cache: TMA fills zeros
     // slots of tile x's boxes
     auto fetch = [&](int x, int *slot) {
+        const unsigned t0 = (unsigned)(x0 + x) * BN;
+        const unsigned page = bpt > 1 ? (unsigned)(x0 + x) * bpt : t0 / (unsigned)ps;
+        const int off = bpt > 1 ? 0 : (int)(t0 - page * (unsigned)ps);
 #pragma unroll
-        for (int i = 0; i < BPT; ++i) {
-            const unsigned tok = (unsigned)(x0 + x) * BN + i * BOX;
+        for (int i = 0; i < MAXB; ++i) {
             slot[i] = oob;
-            if (x < n && tok < (unsigned)end) {
-                const unsigned page = tok / (BPT == 1 ? (unsigned)p.ps : (unsigned)BOX);
-                const int id = __ldg(table + page);
-                if (id >= 0 && id < p.num_pages)
-                    slot[i] = id * p.ps + (BPT == 1 ? (int)(tok - page * (unsigned)p.ps) : 0);
-                else if (bad)
-                    atomicMin(bad, (int)tok);
+            if (i < bpt && x < n && t0 + i * box < (unsigned)end) {
+                const int id = __ldg(table + page + i);
+                if (id >= 0 && id < p.num_pages) slot[i] = id * ps + off;
+                else if (bad) atomicMin(bad, (int)(t0 + i * box));
             }
         }
     };
-    int slot[2][BPT];
-    fetch(0, slot[0]);
-    fetch(1, slot[1]);
-    for (int j0 = 0; w.ok && j0 < n; j0 += 2) {
+    int slot[MAXB], next[MAXB];
+    fetch(0, slot);
+    for (int j = 0; w.ok && j < n; ++j) {
+        fetch(j + 1, next);
+        if (!(w.ok = mbar_wait_for(&w.empty[w.st], w.ph, w.abort, w.ns))) break;
+        uint64_t *full = &w.full[w.st];
+        uint8_t *stage = w.ring + w.st * TILE;
+        mbar_arrive_expect_tx(full, TILE);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (!w.ok || j0 + q >= n) break;
-            if (!(w.ok = mbar_wait_for(&w.empty[w.st], w.ph, w.abort, w.ns))) break;
-            uint64_t *full = &w.full[w.st];
-            uint8_t *stage = w.ring + w.st * TILE;
-            mbar_arrive_expect_tx(full, TILE);
-#pragma unroll
-            for (int i = 0; i < BPT; ++i) {
-                tma_load_3d(stage + i * BOX * 128, w.map, 0, head, slot[q][i], full);
-                tma_load_3d(stage + COL + i * BOX * 128, w.map, 64, head, slot[q][i], full);
+        for (int i = 0; i < MAXB; ++i) {
+            if (i < bpt) {
+                tma_load_3d(stage + i * box * 128, w.map, 0, head, slot[i], full);
+                tma_load_3d(stage + COL + i * box * 128, w.map, 64, head, slot[i], full);
             }
-            ++w.issued;
-            if (++w.st == w.stages) {
-                w.st = 0;
-                w.ph ^= 1;
-            }
-            fetch(j0 + q + 2, slot[q]);
+            slot[i] = next[i];
+        }
+        ++w.issued;
+        if (++w.st == w.stages) {
+            w.st = 0;
+            w.ph ^= 1;
         }
     }
 }
@@ -300,11 +302,13 @@ __global__ void __launch_bounds__(ct::NT, 1)
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    pdl_wait();
-    pdl_launch_dependents();
-    chunk_layout<BN, NT>(p, space, reinterpret_cast<long long *>(join));
+    tc_fence_before();
+    __syncthreads();
     const uint32_t tmem = *tmem_slot;
     tc_fence_after();
+    pdl_wait();
+    pdl_launch_dependents();
+    if (p.B > kChunkWarpBatch) chunk_layout<BN, NT>(p, space, reinterpret_cast<ChunkCount *>(join));
 
     // Waits of the ring of parts: they go on after an abort, when every role still goes through
     // the parts (without work), so that the pieces of split units are all counted.
@@ -316,12 +320,15 @@ __global__ void __launch_bounds__(ct::NT, 1)
         return warp_wait(bar, parity, abort_flag, p.wait_ns);
     };
     const unsigned long long long_ns = p.wait_ns < kWaitDeadlineNs ? p.wait_ns : kLongWaitNs;
-    auto wait_long = [&](uint64_t *bar, uint32_t parity) {
-        return warp_wait(bar, parity, abort_flag, long_ns);
-    };
 
     if (warp < SW0) {
         regs_dec<72>();
+        auto role_ring_wait = [&](uint64_t *bar, int use) {
+            return __all_sync(FULL, role_wait(bar, (uint32_t)(use & 1), &never, kLongWaitNs));
+        };
+        auto role_wait_long = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(FULL, role_wait(bar, parity, abort_flag, long_ns));
+        };
         if (warp <= 1) {
             // -------------------------------------------------------- producers of K and V
             // one elected thread each, as for the issuer: a box takes a third of what it
@@ -330,21 +337,16 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 const bool is_k = warp == 0;
                 Producer w = {is_k ? &tmk : &tmv, is_k ? sK : sV, is_k ? k_full : v_full,
                               is_k ? k_empty : v_empty, is_k ? KS : VS, 0, 0, 1u, long_ns, abort_flag, true};
-                const int bpt = p.ps < BN ? BN / p.ps : 1;
-                for (int i = 0; mbar_wait_for(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs);
+                for (int i = 0; role_wait(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs);
                      ++i) {
                     TcPart *pt = &parts[i % NR];
                     if (pt->n == 0) break;
-                    int *bad = is_k ? &pt->bad : nullptr;
-                    if (bpt == 8) load_part<8>(p, w, *pt, bad);
-                    else if (bpt == 4) load_part<4>(p, w, *pt, bad);
-                    else if (bpt == 2) load_part<2>(p, w, *pt, bad);
-                    else load_part<1>(p, w, *pt, bad);
+                    load_part(p, w, *pt, is_k ? &pt->bad : nullptr);
                     mbar_arrive(&part_empty[i % NR]);
                 }
                 // never leave with copies in flight: the last fill of every stage
                 for (int s = 0; s < w.stages && s < w.issued; ++s)
-                    mbar_wait_for(&w.full[s], (uint32_t)(((w.issued - 1 - s) / w.stages) & 1), &never,
+                    role_wait(&w.full[s], (uint32_t)(((w.issued - 1 - s) / w.stages) & 1), &never,
                                   kWaitDeadlineNs);
             }
             __syncwarp();
@@ -365,10 +367,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 uint32_t oph = 3;     // bit h: the half had a part; parity of O's release
                 bool ok = true;
                 auto one = [&](uint64_t *bar, uint32_t parity) {
-                    return mbar_wait_for(bar, parity, abort_flag, p.wait_ns);
-                };
-                auto one_long = [&](uint64_t *bar, uint32_t parity) {
-                    return mbar_wait_for(bar, parity, abort_flag, long_ns);
+                    return role_wait(bar, parity, abort_flag, long_ns);
                 };
             // S = Q_h K^T of the tile in K's stage ks, once S was taken
             auto issue_qk = [&](const uint32_t h, bool last_of_tile, bool last_of_part) {
@@ -424,7 +423,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
                     }
                 }
             };
-            for (int i = 0; mbar_wait_for(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs); ++i) {
+            for (int i = 0; role_wait(&part_full[i % NR], (uint32_t)(i / NR & 1), &never, kLongWaitNs); ++i) {
                 const int n = parts[i % NR].n, two = parts[i % NR].two;
                 const bool clear = parts[i % NR].clear;
                 if (n == 0) break;
@@ -458,20 +457,23 @@ __global__ void __launch_bounds__(ct::NT, 1)
             }
                 if (*abort_flag) {
                     umma_commit(drain);
-                    mbar_wait_for(drain, 0, &never, kWaitDeadlineNs);
+                    role_wait(drain, 0, &never, kWaitDeadlineNs);
                 }
             }
             __syncwarp();
         } else {
             // -------------------------------------------------------- the planner
+            // a batch that one warp can lay out the others need not wait for
+            const ChunkSpace sp = p.B > kChunkWarpBatch ? *space : chunk_layout_warp<BN>(p, lane);
+            if (lane == 0 && p.B <= kChunkWarpBatch) *space = sp;
             ChunkSeg g;
             // (a part that ends in its unit's lead has no tiles and is none)
             auto with_tiles = [&](bool more) {
                 int first;
-                while (more && chunk_part(p, g, first) == 0) more = chunk_next<BN>(p, *space, g);
+                while (more && chunk_part(sp, g, first) == 0) more = chunk_next<BN>(p, sp, g);
                 return more;
             };
-            bool more = with_tiles(chunk_first<BN>(p, *space, g)), ended = false, ok = true;
+            bool more = with_tiles(chunk_first<BN>(p, sp, g)), ended = false, ok = true;
             int posted = 0, loaded = 0, q_loads = 0, tiles = 0;
             // The rows of V behind the last token of a part, whose last tile is the tiles-th: up
             // to the end of their page they may hold anything. Called when the part's QKs
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 tiles += pt->n;
                 if (!pt->clear) return;
                 const int vs = (tiles - 1) % VS, use = (tiles - 1) / VS;
-                if (ok && (ok = wait_long(&v_full[vs], (uint32_t)(use & 1)))) {
+                if (ok && (ok = role_wait_long(&v_full[vs], (uint32_t)(use & 1)))) {
                     const int ps = p.ps, box = ps < BN ? ps : BN;
                     const int r0 = (int)((long long)pt->L + pt->tok0 + pt->ntok - (long long)(pt->t - 1) * BN);
                     const int r1 = (r0 + box - 1) / box * box;
@@ -494,11 +496,10 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&v_clear[vs]);
             };
-            const ChunkSpace sp = *space;
             for (;;) {
                 while (!ended && posted < loaded + NR - 1) {
                     TcPart *pt = &parts[posted % NR];
-                    if (posted >= NR && !ring_wait(&part_empty[posted % NR], posted / NR - 1)) {
+                    if (posted >= NR && !role_ring_wait(&part_empty[posted % NR], posted / NR - 1)) {
                         ended = true;
                         break;
                     }
@@ -511,9 +512,9 @@ __global__ void __launch_bounds__(ct::NT, 1)
                             w.row = g.row0 + w.tok0;
                             w.ntok = min(p.TB, g.n - w.tok0);
                             w.L = g.L;
-                            w.n = chunk_part(p, g, w.x0);
+                            w.n = chunk_part(sp, g, w.x0);
                             w.t = g.t;
-                            chunk_groups(p, sp, g, w.cf, w.cl);
+                            chunk_groups(sp, g, w.cf, w.cl);
                             w.slot = 2 * blockIdx.x + (g.x0 == sp.s ? 0 : 1);
                             w.first_slot = chunk_start(w.cf, sp.T, sp.C) < g.pu ? 1 : 0;
                             w.two = w.ntok > p.TB / 2;
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 }
                 if (loaded >= posted - (ended ? 1 : 0)) break;
                 const TcPart *pt = &parts[loaded % NR];
-                if (ok && loaded > 0) ok = wait_long(q_free, (uint32_t)((loaded - 1) & 1));
+                if (ok && loaded > 0) ok = role_wait_long(q_free, (uint32_t)((loaded - 1) & 1));
                 if (ok && lane == 0) {
                     const int half = p.TB / 2;
                     mbar_arrive_expect_tx(q_full, (pt->two ? 2u : 1u) * 2u * 128u * (uint32_t)(half * p.G));
@@ -548,12 +549,12 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 ++loaded;
             }
             if (loaded > 0) {
-                if (ok) ok = wait_long(q_free, (uint32_t)((loaded - 1) & 1));
+                if (ok) ok = role_wait_long(q_free, (uint32_t)((loaded - 1) & 1));
                 clear(&parts[(loaded - 1) % NR]);
             }
             // (after an abort nobody may have waited for the last Q)
             if (q_loads > 0 && lane == 0)
-                mbar_wait_for(q_full, (uint32_t)((q_loads - 1) & 1), &never, kWaitDeadlineNs);
+                role_wait(q_full, (uint32_t)((q_loads - 1) & 1), &never, kWaitDeadlineNs);
             __syncwarp();
         }
     } else {
@@ -769,79 +770,20 @@ __global__ void __launch_bounds__(ct::NT, 1)
             // ---- a piece: count it, and join the unit's pieces if it was the last
             const int nthr = two ? 256 : 128, id = two ? kBarBoth : kBarHalf;
             const int F = cl - cf + 1;
-            __threadfence();
-            const int lost_here = bar_or(id, nthr, !ok);
+            if (r == 0) __stcg(p.part_bad + 2 * slot + h, ok ? bad : kPieceLost);
+            bar_or(id, nthr, 0);
             if (st == 0) {
-                __stcg(p.part_bad + slot, lost_here ? kPieceLost : bad);
-                __threadfence();
+                __threadfence();  // what the barrier made visible to this thread, too
                 int *counter = p.counters + cf * p.S + hl;
                 const int before = atomicAdd(counter, 1);
                 if (before == F - 1) *counter = 0;
                 *s_last = before == F - 1;
                 __threadfence();
             }
-            const int mine = bar_or(id, nthr, st == 0 && *s_last);
-            if (!mine) continue;
-            auto slot_of = [&](int f) {
-                return 2 * ((cf + f) * p.S + hl) + (f == 0 ? first_slot : 0);
-            };
-            int lost = kPieceFine;
-            for (int f = 0; f < F; ++f) lost = min(lost, __ldcg(p.part_bad + slot_of(f)));
-            const int M = ntok * p.G;  // rows of the block
-            auto place = [&](int m) {  // where row m of the block is in a piece
-                return m < half_rows ? m : 128 + m - half_rows;
-            };
-            for (int m = st; m < M; m += nthr) {
-                const int at = place(m);
-                float mx = -INFINITY, sum = 0.0f;
-                for (int f = 0; f < F; ++f)
-                    mx = fmaxf(mx, __ldcg(p.part_lse + (size_t)slot_of(f) * p.slot_rows + at));
-                for (int f = 0; f < F; ++f) {
-                    const float v = __ldcg(p.part_lse + (size_t)slot_of(f) * p.slot_rows + at);
-                    sum += v == -INFINITY ? 0.0f : ex2_approx(v - mx);
-                }
-                const float all = mx + __log2f(sum);
-                join[m] = all;
-                const bool zero = L + tok0 + m / p.G >= lost;
-                if (p.lse)
-                    p.lse[(size_t)(qrow0 + m / p.G) * p.Hq + (size_t)head * p.G + m % p.G] =
-                        zero ? 0.0f : all * 0.69314718055994531f;
-            }
-            bar_or(id, nthr, 0);
-            for (int it = st; it < M * (HD / 4); it += nthr) {
-                const int m = it % M, c = it / M, at = place(m);
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (L + tok0 + m / p.G < lost) {
-                    const float all = join[m];
-                    for (int f0 = 0; f0 < F; f0 += 4) {
-                        float w[4];
-                        float4 a[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            w[u] = -INFINITY;
-                            a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (f0 + u < F) {
-                                const int sl = slot_of(f0 + u);
-                                w[u] = __ldcg(p.part_lse + (size_t)sl * p.slot_rows + at);
-                                a[u] = __ldcg(p.part + ((size_t)sl * (HD / 4) + c) * p.slot_rows + at);
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (w[u] == -INFINITY) continue;
-                            const float e = ex2_approx(w[u] - all);
-                            acc.x = fmaf(e, a[u].x, acc.x);
-                            acc.y = fmaf(e, a[u].y, acc.y);
-                            acc.z = fmaf(e, a[u].z, acc.z);
-                            acc.w = fmaf(e, a[u].w, acc.w);
-                        }
-                    }
-                }
-                const size_t orow = (size_t)(qrow0 + m / p.G) * p.Hq + (size_t)head * p.G + m % p.G;
-                *reinterpret_cast<uint2 *>(out + orow * HD + c * 4) =
-                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            }
-            bar_or(id, nthr, 0);  // join[] is used again
+            if (!bar_or(id, nthr, st == 0 && *s_last)) continue;
+            const ChunkJoin jn = {F, cf, hl, first_slot, ntok * p.G, half_rows, 1 + two,
+                                  qrow0, head, L + tok0, st, nthr, id};
+            chunk_join<HD, __nv_bfloat16>(p, jn, join);
         }
     }
 
