@@ -24,6 +24,7 @@ namespace svf {
 namespace {
 
 constexpr int kNormRopeThreads = 128;
+constexpr int kMostPairs = 128;  // D <= 256
 
 struct NormRopeDev {
     const uint8_t *q, *k, *v;
@@ -51,31 +52,25 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(NormRopeDev
     const int j = threadIdx.x % a.lanes, hs = threadIdx.x / a.lanes;
     pdl_wait();
     pdl_launch_dependents();
+    // what the addresses of a row depend on, in one round trip
     const int slot = a.slots[t];
+    int pos[MULTI ? 4 : 1];
+#pragma unroll
+    for (int x = 0; x < (MULTI ? 4 : 1); ++x)
+        pos[x] = x < a.axes ? a.positions[(size_t)x * a.T + t] : 0;
+    int axis = 0;
+    if (MULTI && threadIdx.x < a.rot / 2) axis = __ldg(a.pair_axis + threadIdx.x);
     int st = 0;
     if (slot != -1) {
         if (slot < 0 || slot >= a.num_slots) st |= SVF_DEV_BAD_PAGE;
-        for (int x = 0; x < a.axes; ++x) {
-            const int p = a.positions[(size_t)x * a.T + t];
-            if (p < 0 || p >= a.max_pos) st |= SVF_DEV_BAD_LENGTH;
-        }
+#pragma unroll
+        for (int x = 0; x < (MULTI ? 4 : 1); ++x)
+            if (x < a.axes && (pos[x] < 0 || pos[x] >= a.max_pos)) st |= SVF_DEV_BAD_LENGTH;
     }
     const bool turn = j < a.pairs;
-    int ax[N];  // the axis of each of this item's pairs
-    if (MULTI) {
-        bool bad = false;
-        if (turn) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                ax[i] = __ldg(a.pair_axis + j * N + i);
-                bad |= ax[i] < 0 || ax[i] >= a.axes;
-            }
-        }
-        // every block has lanes for all pairs, so all agree
-        if (__syncthreads_or(bad) && slot != -1) st |= SVF_DEV_BAD_LENGTH;
-    }
-    if (a.status && blockIdx.y == 0 && threadIdx.x == 0) a.status[t] = st;
-    if (slot == -1) return;  // a row behind the last sequence, or one without a page
+    __shared__ __align__(16) float s_cs[MULTI ? 2 * kMostPairs : 4];  // cosines, then sines
+    const int H = a.Hq + 2 * a.Hkv;
+    const int h0 = blockIdx.y * a.HG * HEADS + hs;
     const bool item = j < a.J;
     // byte offsets of the item's two vectors inside a head; the tail of an
     // odd number of vectors ends with a single one
@@ -83,35 +78,13 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(NormRopeDev
     const int vb = (INTER || !turn) ? va + 1 : j + a.pairs;
     const int oa = va * 16, ob = vb * 16;
     const bool has_b = item && ob < a.head_bytes;
-    float cs[N], sn[N];
-    if (turn && !st) {
-        if (MULTI) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int pos = __ldg(a.positions + (size_t)ax[i] * a.T + t);
-                const float *row = a.rope + (size_t)pos * a.rot + j * N + i;
-                cs[i] = __ldg(row);
-                sn[i] = __ldg(row + a.rot / 2);
-            }
-        } else {
-            const float *row = a.rope + (size_t)a.positions[t] * a.rot + j * N;
-#pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                *reinterpret_cast<float4 *>(cs + i) = __ldg(reinterpret_cast<const float4 *>(row + i));
-                *reinterpret_cast<float4 *>(sn + i) =
-                    __ldg(reinterpret_cast<const float4 *>(row + a.rot / 2 + i));
-            }
-        }
-    }
-    const int H = a.Hq + 2 * a.Hkv;
-    const int h0 = blockIdx.y * a.HG * HEADS + hs;
-    const size_t kv_row = (size_t)(st ? 0 : slot) * (size_t)(a.Hkv * a.head_bytes);
+    const bool left_out = slot == -1;  // a row behind the last sequence, or one without a page
     uint4 xa[HEADS], xb[HEADS];
 #pragma unroll
     for (int u = 0; u < HEADS; ++u) {
         const int h = h0 + u * a.HG;
         xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
-        if (item && h < H && !st) {
+        if (item && h < H && !st && !left_out) {
             const uint8_t *src =
                 h < a.Hq ? a.q + t * a.q_stride + (size_t)h * a.head_bytes
                 : h < a.Hq + a.Hkv
@@ -121,6 +94,40 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(NormRopeDev
             if (has_b) xb[u] = __ldcs(reinterpret_cast<const uint4 *>(src + ob));
         }
     }
+    if (MULTI) {
+        // the row's cosines and sines, each pair's by its own axis, once for all heads
+        bool bad = false;
+        for (int i = threadIdx.x; i < a.rot / 2; i += (int)blockDim.x) {
+            const int ax = i == threadIdx.x ? axis : __ldg(a.pair_axis + i);
+            if (ax < 0 || ax >= a.axes) {
+                bad = true;
+            } else if (!st && !left_out) {
+                const int at = ax == 0 ? pos[0] : ax == 1 ? pos[MULTI] : ax == 2 ? pos[2 * MULTI] : pos[3 * MULTI];
+                const float *row = a.rope + (size_t)at * a.rot + i;
+                s_cs[i] = __ldg(row);
+                s_cs[kMostPairs + i] = __ldg(row + a.rot / 2);
+            }
+        }
+        // (every block looks at all pairs, so all agree)
+        if (__syncthreads_or(bad) && !left_out) {
+            st |= SVF_DEV_BAD_LENGTH;
+#pragma unroll
+            for (int u = 0; u < HEADS; ++u) xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (a.status && blockIdx.y == 0 && threadIdx.x == 0) a.status[t] = st;
+    if (left_out) return;
+    float cs[N], sn[N];
+    if (turn && !st) {
+        const float *row = MULTI ? s_cs + j * N : a.rope + (size_t)pos[0] * a.rot + j * N;
+        const int sines = MULTI ? kMostPairs : a.rot / 2;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            *reinterpret_cast<float4 *>(cs + i) = *reinterpret_cast<const float4 *>(row + i);
+            *reinterpret_cast<float4 *>(sn + i) = *reinterpret_cast<const float4 *>(row + sines + i);
+        }
+    }
+    const size_t kv_row = (size_t)(st ? 0 : slot) * (size_t)(a.Hkv * a.head_bytes);
 #pragma unroll
     for (int u = 0; u < HEADS; ++u) {
         const int h = h0 + u * a.HG;
