@@ -46,7 +46,7 @@ struct NormRopeDev {
 // block: lanes * HG threads, thread (j, hs) = item j of heads hs, hs + HG, ...;
 // grid (rows, head blocks of HG * HEADS)
 template <typename T, bool INTER, bool MULTI, int HEADS>
-__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(NormRopeDev a) {
+__global__ void __launch_bounds__(kNormRopeThreads, 8) norm_rope_kernel(NormRopeDev a) {
     constexpr int N = Vec<T>::N;
     const int t = blockIdx.x;
     const int j = threadIdx.x % a.lanes, hs = threadIdx.x / a.lanes;
