@@ -455,10 +455,6 @@ __global__ void __launch_bounds__(ct::NT, 1)
                     }
                 }
             }
-                if (*abort_flag) {
-                    umma_commit(drain);
-                    role_wait(drain, 0, &never, kWaitDeadlineNs);
-                }
             }
             __syncwarp();
         } else {
@@ -789,6 +785,18 @@ __global__ void __launch_bounds__(ct::NT, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {
+        // Some role gave up, the issuer perhaps through before: its products finish before tensor
+        // memory and shared memory go. (elect.sync elects the same thread each time, the one
+        // that issued them.)
+        if (warp == 2 && elect_one()) {
+            umma_commit(drain);
+            mbar_wait_for(drain, 0, &never, kWaitDeadlineNs);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
