@@ -91,6 +91,74 @@ __device__ __forceinline__ int bar_or(int id, int n, int pred) {
     return (int)r;
 }
 
+// Products with the operands' descriptors as their low words (start address and leading offset; the
+// high word is the same for all: 1024 bytes between groups of eight rows, 128-byte swizzle):
+// the issuer has no register to spare either.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t start, uint32_t lbo) {
+    return start >> 4 | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
+        : "memory");
+}
+
+// Barriers by their 32-bit addresses: the softmax warps have no register to spare.
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool test_wait_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A warp's wait, as mbar_wait_for; the clock is read in units of 1.024 us, in 32 bits.
+__device__ __forceinline__ bool warp_wait_at(uint32_t bar, uint32_t parity, volatile int *abort,
+                                             unsigned long long ns) {
+    if (__all_sync(0xffffffffu, test_wait_at(bar, parity))) return true;
+    const bool quick = ns < 1000000ull;
+    const uint32_t t0 = (uint32_t)(globaltimer_ns() >> 10), limit = (uint32_t)(ns >> 10);
+    for (uint32_t it = 1;; ++it) {
+        const bool ok = quick ? test_wait_at(bar, parity) : try_wait_at(bar, parity);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (quick || (it & 63u) == 0) {
+            if ((uint32_t)(globaltimer_ns() >> 10) - t0 > limit) *abort = 1;
+            if (__any_sync(0xffffffffu, *abort)) return false;
+        }
+    }
+}
+
 // A wait of the roles that need few registers (not inlined: there are many).
 __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
                                        unsigned long long ns) {
@@ -316,13 +384,10 @@ __global__ void __launch_bounds__(ct::NT, 1)
     auto ring_wait = [&](uint64_t *bar, int use) {
         return __all_sync(FULL, mbar_wait_for(bar, (uint32_t)(use & 1), &never, kLongWaitNs));
     };
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return warp_wait(bar, parity, abort_flag, p.wait_ns);
-    };
     const unsigned long long long_ns = p.wait_ns < kWaitDeadlineNs ? p.wait_ns : kLongWaitNs;
 
     if (warp < SW0) {
-        regs_dec<72>();
+        regs_dec<56>();
         auto role_ring_wait = [&](uint64_t *bar, int use) {
             return __all_sync(FULL, role_wait(bar, (uint32_t)(use & 1), &never, kLongWaitNs));
         };
@@ -357,9 +422,8 @@ __global__ void __launch_bounds__(ct::NT, 1)
             if (elect_one()) {
                 constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, false, false);
                 constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD, false, true);
-                const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-                const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
-                const uint64_t dV = smem_desc_sw128(smem_u32(sV), COL, 1024);
+                const uint32_t dQ = desc_low(smem_u32(sQ), 16), dK = desc_low(smem_u32(sK), 16);
+                const uint32_t dV = desc_low(smem_u32(sV), COL);
                 uint32_t ks = 0, vs = 0;              // stages of the next QK and the next PV
                 uint32_t kph = 0, vph = 0, sph = 1;
                 uint32_t zph = 0;                // bit s: parity of the stage's next clearing
@@ -374,11 +438,11 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 if (!(ok = ok && one(s_free, sph))) return;
                 sph ^= 1;
                 tc_fence_after();
-                const uint64_t q = dQ + h * (TILE >> 4), k = dK + ks * (TILE >> 4);
+                const uint32_t q = dQ + h * (TILE >> 4), k = dK + ks * (TILE >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     const uint32_t o = ((kk >> 2) * COL + (kk & 3) * 32) >> 4;
-                    umma_ss(tmem + tS, q + o, k + o, idesc_qk, kk > 0);
+                    mma_ss(tmem + tS, q + o, k + o, idesc_qk, kk > 0);
                 }
                 umma_commit(&s_full[h]);
                 if (last_of_tile) {
@@ -409,11 +473,11 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 pph ^= 1u << h;
                 tc_fence_after();
                 const uint32_t d = tmem + tO + h * 128, a = tmem + tP + h * 64;
-                const uint64_t v = dV + vs * (TILE >> 4);
-                umma_ts(d, a, v, idesc_pv, first ? 0u : 1u);
+                const uint32_t v = dV + vs * (TILE >> 4);
+                mma_ts(d, a, v, idesc_pv, first ? 0u : 1u);
 #pragma unroll
                 for (int kk = 1; kk < 8; ++kk)
-                    umma_ts(d, a + kk * 8, v + (kk * 2048 >> 4), idesc_pv, 1u);
+                    mma_ts(d, a + kk * 8, v + (kk * 2048 >> 4), idesc_pv, 1u);
                 umma_commit(&o_done[h]);
                 if (last_of_tile) {
                     umma_commit(&v_empty[vs]);
@@ -554,7 +618,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
             __syncwarp();
         }
     } else {
-        regs_inc<216>();
+        regs_inc<224>();
         // ------------------------------------------------------------ softmax
         const int h = (warp - SW0) >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;           // row of the half
@@ -566,6 +630,14 @@ __global__ void __launch_bounds__(ct::NT, 1)
         const int half_tok = p.TB / 2, half_rows = half_tok * p.G;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
         const bool wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+        const int tok = h * half_tok + r / p.G;      // token of the row in its block
+        // the half's barriers
+        const uint32_t bH = smem_u32(bars) + h * 8;
+        constexpr int kSFree = (2 * KS + 2 * VS + 2 * NR + 2) * 8, kSFull = kSFree + 8,
+                      kPFull = kSFull + 16, kODone = kPFull + 16;
+        auto wait_at = [&](uint32_t bar, uint32_t parity) {
+            return warp_wait_at(bar, parity, abort_flag, p.wait_ns);
+        };
 
         chunk_status<HD, __nv_bfloat16>(p, st, 256,
                                         [&](bool v) { return bar_or(kBarBoth, 256, v) != 0; });
@@ -582,19 +654,17 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 if (lane == 0) mbar_arrive(&part_empty[i % NR]);
                 continue;
             }
-            const int L = pt->L, x0 = pt->x0, tok0 = pt->tok0, ntok = pt->ntok;
-            const int ltok = r / p.G;                // token of the row in its half
-            const int tok = h * half_tok + ltok;     // and in the block
-            const bool row_valid = r < half_rows && tok < ntok;
-            const int see = row_valid ? L + tok0 + tok : 0x7fffffff;
-            const bool live = __any_sync(FULL, row_valid);
+            // (what the tiles do not need is read again behind them)
+            const bool live = __any_sync(FULL, r < half_rows && tok < pt->ntok);
+            // columns of the part up to it are visible (rows of padding see them all)
+            int lim = r < half_rows && tok < pt->ntok ? pt->L + pt->tok0 + tok - pt->x0 * BN : 0x7fffffff;
             float m_ref = -INFINITY, l = 0.0f;
-            for (int jl = 0; ok && jl < n; ++jl, ++cnt) {
-                if (!(ok = wait(&s_full[h], (uint32_t)(cnt & 1)))) break;
+            for (int jl = 0; ok && jl < n; ++jl, ++cnt, lim -= BN) {
+                if (!(ok = wait_at(bH + kSFull, (uint32_t)(cnt & 1)))) break;
                 if (!live) {  // padding of the half: its rows are not looked at
-                    mbar_arrive(s_free);
-                    if (cnt > 0 && !(ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1)))) break;
-                    mbar_arrive(&p_full[h]);
+                    arrive_at(bH - h * 8 + kSFree);
+                    if (cnt > 0 && !(ok = wait_at(bH + kODone, (uint32_t)((cnt - 1) & 1)))) break;
+                    arrive_at(bH + kPFull);
                     continue;
                 }
                 tc_fence_after();
@@ -605,8 +675,7 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 tmem_ld32(aS + 96, v + 96);
                 tmem_wait_ld();
                 tc_fence_before();
-                mbar_arrive(s_free);
-                const int lim = see - (x0 + jl) * BN;  // columns up to it are visible
+                arrive_at(bH - h * 8 + kSFree);
                 if (__any_sync(FULL, lim < BN - 1)) {
 #pragma unroll
                     for (int c = 0; c < BN; ++c) v[c] = c <= lim ? v[c] : 0xff800000u;
@@ -630,18 +699,17 @@ __global__ void __launch_bounds__(ct::NT, 1)
                 const float mneg = m_ref == -INFINITY ? 0.0f : -m_ref;
                 const float2 sc2 = make_float2(sl2, sl2), mn2 = make_float2(mneg, mneg);
                 float2 rs = make_float2(0.0f, 0.0f);
-                uint32_t pk[BN / 2];
 #pragma unroll
-                for (int c = 0; c < BN / 2; ++c) {
+                for (int c = 0; c < BN / 2; ++c) {  // P takes the place of S
                     const float2 y = ffma2(make_float2(__uint_as_float(v[2 * c]),
                                                        __uint_as_float(v[2 * c + 1])), sc2, mn2);
                     const float2 pp = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                     rs = fadd2(rs, pp);
-                    pk[c] = pack_bf16x2(pp.x, pp.y);
+                    v[c] = pack_bf16x2(pp.x, pp.y);
                 }
                 l += rs.x + rs.y;
                 // P of the tile before was read, O is final up to it
-                if (cnt > 0 && !(ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1)))) break;
+                if (cnt > 0 && !(ok = wait_at(bH + kODone, (uint32_t)((cnt - 1) & 1)))) break;
                 if (jl > 0 && __any_sync(FULL, need)) {
                     tc_fence_after();
 #pragma unroll 1
@@ -655,15 +723,20 @@ __global__ void __launch_bounds__(ct::NT, 1)
                         tmem_st16(aO + c * 16, o);
                     }
                 }
-                tmem_st32(aP, pk);
-                tmem_st32(aP + 32, pk + 32);
+                tmem_st16(aP, v);
+                tmem_st16(aP + 16, v + 16);
+                tmem_st16(aP + 32, v + 32);
+                tmem_st16(aP + 48, v + 48);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&p_full[h]);
+                arrive_at(bH + kPFull);
             }
             // ---- the end of the part: O after its last PV
-            if (ok) ok = wait(&o_done[h], (uint32_t)((cnt - 1) & 1));
+            if (ok) ok = wait_at(bH + kODone, (uint32_t)((cnt - 1) & 1));
             tc_fence_after();
+            const int L = pt->L, x0 = pt->x0, tok0 = pt->tok0, ntok = pt->ntok;
+            const bool row_valid = r < half_rows && tok < ntok;
+            const int see = row_valid ? L + tok0 + tok : 0x7fffffff;
             const int head = pt->head, cf = pt->cf, cl = pt->cl, slot = pt->slot;
             const int first_slot = pt->first_slot, bad = pt->bad, b = pt->b, qrow0 = pt->row;
             const bool split = cf != cl;
