@@ -8,8 +8,8 @@
 // A CTA goes through the tiles of its share of the call (chunk.cuh): 64 rows (token, head)
 // against 64 tokens at a time. 256 threads as 16 x 16: thread (y, x) has rows 4 y .. + 3 and
 // tokens x, x + 16, .. of the scores, and the same rows of O with elements 4 x + 64 c ..; so a
-// row's sums stay inside 16 neighbouring lanes. K and V tiles share one buffer for the copies
-// of the next tile while the present one is used.
+// row's sums stay inside 16 neighbouring lanes. The next K comes while P is made and
+// multiplied with V, the next V while the next scores are made.
 //
 // Bound: fp32 FMA issue and shared-memory reads of the two products (2 D FMAs per score).
 #include <math.h>
@@ -31,7 +31,6 @@ struct ChunkSmem {
     float v[BN][LDK];
     float p[BN][LDP];  // P transposed: [token][row]
     float w[BM];       // the join: a row's log2-sum-exp
-    int page[BN];      // slot of each token of the tile, -1 without one
     int bad;           // first token of the part whose page is not in the cache
     int last;
     ChunkSpace space;
@@ -41,7 +40,7 @@ struct ChunkSmem {
 __device__ __forceinline__ float ex2(float x) { return exp2f(x); }
 
 template <int D>
-__global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
+__global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) chunk_simt_kernel(ChunkParams p) {
     using Sm = ChunkSmem<D>;
     extern __shared__ __align__(16) uint8_t raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
@@ -87,33 +86,43 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
 #pragma unroll
             for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.0f;
         }
+        // Tiles come by asynchronous copies: 16 bytes a lane, R rows of K or V a warp. A row without
+        // a token of the block, or without a page, is zeros.
+        constexpr int R = D / 16;
+        const int tend = g.L + tok0 + ntok;  // tokens that the block sees
+        const int crow = tid / (D / 4), cc = tid % (D / 4);  // rows crow + (NT / (D / 4)) q
+        int at[R];
+        auto lookup = [&](int xt) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                const unsigned t = (unsigned)xt * BN + crow + q * (NT / (D / 4));
+                at[q] = -1;
+                if (xt < x0 + tiles && t < (unsigned)tend) {
+                    const unsigned page = t / (unsigned)p.ps;
+                    const int id = __ldg(table + page);
+                    if (id >= 0 && id < p.num_pages) at[q] = id * p.ps + (int)(t - page * (unsigned)p.ps);
+                    else if (cc == 0) atomicMin(&sm.bad, (int)t);
+                }
+            }
+        };
+        auto copy = [&](float (*dst)[Sm::LDK], const float *base) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                const float *src = base + ((size_t)max(at[q], 0) * p.Hkv + head) * D + 4 * cc;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 smem_u32(&dst[crow + q * (NT / (D / 4))][4 * cc])),
+                             "l"(src), "r"(at[q] >= 0 ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        __syncthreads();  // sm.bad is set
+        lookup(x0);
+        copy(sm.k, K);
+        copy(sm.v, V);
         for (int xt = x0; xt < x0 + tiles; ++xt) {
             const int t0 = xt * BN;
-            const int tend = g.L + tok0 + ntok;  // tokens that the block sees
-            __syncthreads();
-            if (tid < BN) {
-                int slot = -1;
-                if (tid < tend - t0) {
-                    const int t = t0 + tid;
-                    const int id = __ldg(table + t / p.ps);
-                    if (id >= 0 && id < p.num_pages) slot = id * p.ps + t % p.ps;
-                    else atomicMin(&sm.bad, t);
-                }
-                sm.page[tid] = slot;
-            }
-            __syncthreads();
-            for (int i = tid; i < BN * (D / 4); i += NT) {
-                const int r = i / (D / 4), c = i % (D / 4);
-                const int slot = sm.page[r];
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-                if (slot >= 0) {
-                    const size_t at = ((size_t)slot * p.Hkv + head) * D + 4 * c;
-                    a = __ldg(reinterpret_cast<const float4 *>(K + at));
-                    b = __ldg(reinterpret_cast<const float4 *>(V + at));
-                }
-                *reinterpret_cast<float4 *>(&sm.k[r][4 * c]) = a;
-                *reinterpret_cast<float4 *>(&sm.v[r][4 * c]) = b;
-            }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // K is there
             __syncthreads();
             float s[4][4];  // rows 4 y + i, tokens x + 16 j
 #pragma unroll
@@ -137,6 +146,9 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
                         s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
                     }
             }
+            __syncthreads();  // K may be replaced, while P is made and multiplied
+            lookup(xt + 1);
+            copy(sm.k, K);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float mx = -INFINITY;
@@ -165,7 +177,8 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<float4 *>(&sm.p[x + 16 * j][4 * y]) =
                     make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-            __syncwarp();  // a warp reads the rows that it wrote
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // V is there
+            __syncthreads();
             const bool inner = BN - 1 <= g.L + tok0 - t0;  // every row sees the whole tile
 #pragma unroll 4
             for (int t = 0; t < BN; ++t) {
@@ -185,7 +198,10 @@ __global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
                     }
                 }
             }
+            __syncthreads();  // V may be replaced, while the next S is made
+            copy(sm.v, V);
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
         // ---- the end of the part
         const int first_bad = sm.bad;
