@@ -12,6 +12,9 @@
 // multiplied with V, the next V while the next scores are made.
 //
 // Bound: fp32 FMA issue and shared-memory reads of the two products (2 D FMAs per score).
+// Measured, 32/8 heads: 20 tokens over 20000 each of 20 sequences 2420 us (D = 128; 2970 with K and V
+// through registers, whose loads wait for one another); 2048 tokens over themselves 3240 us at
+// D = 128 (3035 through registers: the only case that loses) and 1490 at D = 64 (1510).
 #include <math.h>
 
 #include "chunk.cuh"
@@ -40,7 +43,7 @@ struct ChunkSmem {
 __device__ __forceinline__ float ex2(float x) { return exp2f(x); }
 
 template <int D>
-__global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) chunk_simt_kernel(ChunkParams p) {
+__global__ void __launch_bounds__(NT) chunk_simt_kernel(ChunkParams p) {
     using Sm = ChunkSmem<D>;
     extern __shared__ __align__(16) uint8_t raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
