@@ -759,7 +759,8 @@ int svf_norm_rope_kv_write(const void *q, const void *k, const void *v, long lon
  *   k_cache, v_cache, num_pages, page_size, page_table, max_pages, sm_scale
  *               as in svf_tree_verify_attn
  *   seq_lens    [B] int32      L_b, the tokens before the chunk
- *   row_offsets [B + 1] int32  rising; lengths of 0 are fine
+ *   row_offsets [B + 1] int32  rising; lengths of 0 are fine (a row that two
+ *               sequences claim, where offsets fall in between, is undefined)
  *   out         [rows, Hq, D] dtype; rows behind the last sequence are not
  *               written, nor read
  *   lse         [rows, Hq] float32, may be NULL (natural log)

@@ -242,14 +242,18 @@ _ZEROED_WS = {}
 def _zeroed_workspace(need: int, dev: torch.device, stream=None, of="tree") -> torch.Tensor:
     """The attention workspace used when the caller passes none: zero-filled
     once, on the stream of the call that makes it, and kept per device and
-    operator (every call leaves zero what has to be). Calls that may overlap on the GPU should pass
-    workspaces of their own. A captured call gets one of the graph's memory,
-    filled in every replay: the kept one goes when a larger shape comes, and
-    one made in a capture would begin at zero only in the replays."""
+    operator (every call leaves zero what has to be); the chunk attention's per
+    stream too, so that its calls on two streams never meet in one. Tree calls that may
+    overlap on the GPU should pass workspaces of their own. A captured call gets
+    one of the graph's memory, filled in every replay: the kept one goes when a
+    larger shape comes, and one made in a capture would begin at zero only in
+    the replays."""
     with _on(stream, dev):
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros((need,), dtype=torch.uint8, device=dev)
         key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device(), of)
+        if of == "chunk":
+            key += (torch.cuda.current_stream(dev).cuda_stream,)
         ws = _ZEROED_WS.get(key)
         if ws is None or ws.numel() < need:
             ws = torch.zeros((need,), dtype=torch.uint8, device=dev)
@@ -1202,9 +1206,10 @@ def chunk_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     seq_lens [B] (tokens before the chunk), row_offsets [B + 1] int32 (page_reserve's:
     sequence b's tokens are rows row_offsets[b] .. row_offsets[b + 1]). A row sees the
     tokens up to its own. ``workspace``: chunk_attn_workspace_size bytes, zero-filled
-    once; calls that may overlap need workspaces of their own. Returns (out [rows, Hq,
-    D], lse [rows, Hq] float32 or None, status [B] int32); rows behind the last sequence
-    keep what out and lse held (new ones: undefined)."""
+    once; calls that may overlap need workspaces of their own (without one, the binding
+    keeps one per stream). Returns (out [rows, Hq, D], lse [rows, Hq] float32 or None,
+    status [B] int32); rows behind the last sequence keep what out and lse held (new
+    ones: undefined)."""
     lib = _lib or load_library()
     if _fast is not None and workspace is not None and (lse is not None or not want_lse):
         rc = _fast.chunk_attn(q, k_cache, v_cache, page_table, seq_lens, row_offsets, sm_scale, out,

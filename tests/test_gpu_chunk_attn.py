@@ -329,6 +329,23 @@ def test_streams(sv, dt):
         assert all(torch.equal(x, y) for x, y in zip(res, want))
 
 
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_streams_without_a_workspace(sv, dt):
+    """Calls on two streams that pass no workspace do not meet in one, sizes that grow among them."""
+    cs = [case(33 + i, [3000 * (i // 2 + 1), 40], [300 * (i // 2 + 1), 7], 16, 4, 16, dt)
+          for i in range(4)]
+    want = [sv.chunk_attn(**c)[:2] for c, _ in cs]
+    for c, h in cs:
+        check(sv, c, h)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        res = [sv.chunk_attn(**c, stream=streams[i % 2])[:2] for i, (c, _) in enumerate(cs)]
+        torch.cuda.synchronize()
+        for x, y in zip(res, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 def test_offsets_past_32_bits(sv):
     """Pages whose elements lie beyond 2^31, and beyond 2^32 bytes."""
     ps, Hkv, D, pages = 16, 8, 128, 150000
