@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kForkThreads = 256;
 constexpr int kShareThreads = 1024;
-constexpr int kShareCtas = 8;
 constexpr int kCopyThreads = 256;
 constexpr int kClaim = -(1 << 30);  // below any count: at most 2^30 holders leave in a call
 constexpr int kMostGifts = (1 << 30) - 1;
@@ -207,9 +206,11 @@ struct SharedReleaseArgs {
 // leaves nothing), lower the counts, claim the pages that nobody holds, count them (per
 // warp, so that every page has its place), put them back. Up to kKeep ranks a thread stay
 // in registers, so that the ids are read once and a pass has all of its reads in
-// flight (56 forks of 2049 pages, with fork and copy: 63.5 us with every pass reading the
-// table again, 43.6 with 16 a thread; small tables take 1, whose code is shorter).
-template <int kKeep>
+// flight. Bound: the passes, each a round trip to the L2 and a meeting. 56 forks of 2049 pages, with
+// fork and copy: 31.8 us with 16 CTAs, 42.3 with 8 (63.5 with every pass reading the table again);
+// 34 where a thread goes through all 16 ranks though it has 7. Small tables take 8 CTAs and a rank
+// a thread, whose code is shorter.
+template <int kKeep, int kCtas>
 __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(SharedReleaseArgs a) {
     extern __shared__ int s_off[];   // [B + 1] the running sum of the pages
     int *s_first = s_off + a.B + 1;  // [B]
@@ -219,9 +220,9 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = blockIdx.x;
     constexpr unsigned FULL = 0xffffffffu;
-    if (!cluster_shape_is((uint32_t)kShareCtas, 1u, 1u)) {
+    if (!cluster_shape_is((uint32_t)kCtas, 1u, 1u)) {
         pdl_wait();
-        for (int b = rank * kShareThreads + tid; b < a.B; b += kShareCtas * kShareThreads) {
+        for (int b = rank * kShareThreads + tid; b < a.B; b += kCtas * kShareThreads) {
             a.n_released[b] = 0;
             a.status[b] = SVF_DEV_BAD_CLUSTER;
         }
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     cluster_wait();
     const bool many = total >= kMostGifts;  // more than can be counted: nothing is taken
     if (many) total = 0;
-    constexpr int kWarps = kShareCtas * kShareThreads / 32;
+    constexpr int kWarps = kCtas * kShareThreads / 32;
     const int per = ((total + kWarps - 1) / kWarps + 31) & ~31;
     const int k0 = (int)min((long long)(rank * (kShareThreads / 32) + warp) * per, (long long)total);
     const int k1 = min(k0 + per, total);
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     int seq[kKeep], id[kKeep];
     if (kept) {
 #pragma unroll
-        for (int u = 0; u < kKeep; ++u) {
+        for (int u = 0; u < kKeep && 32 * u < per; ++u) {
             const int k = k0 + lane + 32 * u;
             seq[u] = k < k1 ? owner(k) : -1;
             if (k < k1) id[u] = *entry(seq[u], k);
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     auto each = [&](auto f) {
         if (kept) {
 #pragma unroll
-            for (int u = 0; u < kKeep; ++u)
+            for (int u = 0; u < kKeep && 32 * u < per; ++u)
                 if (seq[u] >= 0) f(k0 + lane + 32 * u, seq[u], id[u]);
         } else {
             for (int k = k0 + lane; k < k1; k += 32) {
@@ -320,11 +321,11 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     };
     each([&](int, int b, int p) {
         if ((p < 0 || p >= a.num_pages) && !is_bad(b))
-            for (int c = 0; c < kShareCtas; ++c)
+            for (int c = 0; c < kCtas; ++c)
                 or_cluster(cluster_map(&s_bad[b >> 5], (uint32_t)c), 1u << (b & 31));
     });
     meet();
-    for (int b = rank * kShareThreads + tid; b < a.B; b += kShareCtas * kShareThreads) {
+    for (int b = rank * kShareThreads + tid; b < a.B; b += kCtas * kShareThreads) {
         int first, n;
         const bool ok = gift(b, first, n);
         a.n_released[b] = 0;
@@ -332,19 +333,21 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     }
     if (kept) {  // the ranks of sequences that leave nothing are out
 #pragma unroll
-        for (int u = 0; u < kKeep; ++u)
+        for (int u = 0; u < kKeep && 32 * u < per; ++u)
             if (seq[u] >= 0 && is_bad(seq[u])) seq[u] = -1;
     }
-    each([&](int, int b, int p) {
-        if (!is_bad(b)) atomicSub(&a.shares[p], 1);
+    each([&](int k, int b, int p) {
+        if (is_bad(b)) return;
+        atomicSub(&a.shares[p], 1);
+        if (kept) *entry(b, k) = -1;  // (else it is read again)
     });
     meet();
     int now[kKeep];
     if (kept) {
 #pragma unroll
-        for (int u = 0; u < kKeep; ++u) now[u] = seq[u] >= 0 ? __ldcg(&a.shares[id[u]]) : 0;
+        for (int u = 0; u < kKeep && 32 * u < per; ++u) now[u] = seq[u] >= 0 ? __ldcg(&a.shares[id[u]]) : 0;
 #pragma unroll
-        for (int u = 0; u < kKeep; ++u)
+        for (int u = 0; u < kKeep && 32 * u < per; ++u)
             if (now[u] < 0) atomicMin(&a.shares[id[u]], kClaim - seq[u]);
     } else {
         each([&](int, int b, int p) {
@@ -364,9 +367,9 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     unsigned mask = 0;  // bit u: the page of kept rank u goes back
     if (kept) {
 #pragma unroll
-        for (int u = 0; u < kKeep; ++u) now[u] = seq[u] >= 0 ? __ldcg(&a.shares[id[u]]) : 0;
+        for (int u = 0; u < kKeep && 32 * u < per; ++u) now[u] = seq[u] >= 0 ? __ldcg(&a.shares[id[u]]) : 0;
 #pragma unroll
-        for (int u = 0; u < kKeep; ++u) {
+        for (int u = 0; u < kKeep && 32 * u < per; ++u) {
             const bool yes = seq[u] >= 0 && now[u] == kClaim - seq[u];
             mask |= yes ? 1u << u : 0u;
             mine += __popc(__ballot_sync(FULL, yes));
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     if (tid == 31) s_total = incl;
     meet();  // (the counts above were read by everybody before a page goes back, too)
     int all = 0;
-    for (int c = 0; c < kShareCtas; ++c) {
+    for (int c = 0; c < kCtas; ++c) {
         const int t = ld_dsmem_s32(cluster_map(&s_total, (uint32_t)c));
         if (c < rank) at += t;
         all += t;
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
     };
     if (kept) {
 #pragma unroll
-        for (int u = 0; u < kKeep; ++u) put(mask >> u & 1u, seq[u], id[u]);
+        for (int u = 0; u < kKeep && 32 * u < per; ++u) put(mask >> u & 1u, seq[u], id[u]);
     } else {
         for (int k = k0 + lane; k - lane < k1; k += 32) {
             int b = -1, p = -1;
@@ -419,14 +422,27 @@ __global__ void __launch_bounds__(kShareThreads) page_release_shared_kernel(Shar
             put(yes, b, p);
         }
     }
-    each([&](int k, int b, int) {
-        if (!is_bad(b)) *entry(b, k) = -1;
-    });
+    if (!kept)
+        each([&](int k, int b, int) {
+            if (!is_bad(b)) *entry(b, k) = -1;
+        });
     // nobody leaves while another may read its count; every CTA read the old one at the start
     cluster_arrive();
     cluster_wait();
     if (rank == 0 && tid == 0)
         a.state[0] = (int)min((long long)F + all, (long long)a.num_pages);
+}
+
+template <int kKeep, int kCtas>
+cudaError_t launch_release(const SharedReleaseArgs &a, size_t bytes, cudaStream_t stream) {
+    auto kernel = page_release_shared_kernel<kKeep, kCtas>;
+    constexpr int kMost = (2 * kMaxPageSequences + 1 + (kMaxPageSequences + 31) / 32) * (int)sizeof(int);
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e == cudaSuccess && kCtas > 8)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(kCtas), dim3(kShareThreads), bytes, stream, (unsigned)kCtas, a);
 }
 
 }  // namespace
@@ -479,16 +495,14 @@ cudaError_t launch_page_release_shared(const PageReleaseArgs &p, int32_t *shares
     a.max_pages = p.max_pages;
     a.ps = p.page_size;
     a.num_pages = p.num_pages;
-    auto bytes = [](int B) { return (size_t)(2 * B + 1 + (B + 31) / 32) * sizeof(int); };
-    // a table whose every page fits one rank a thread
-    auto kernel = (long long)p.B * p.max_pages <= kShareCtas * kShareThreads
-                      ? page_release_shared_kernel<1>
-                      : page_release_shared_kernel<16>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)bytes(kMaxPageSequences));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(kShareCtas), dim3(kShareThreads), bytes(p.B), stream,
-                      (unsigned)kShareCtas, a);
+    const size_t bytes = (size_t)(2 * p.B + 1 + (p.B + 31) / 32) * sizeof(int);
+    // a table whose every page fits one rank a thread of 8 CTAs; larger ones 16, where such a
+    // cluster fits the device
+    if ((long long)p.B * p.max_pages > 8 * kShareThreads &&
+        resident_clusters(page_release_shared_kernel<16, 16>, kShareThreads, bytes, 16) > 0)
+        return launch_release<16, 16>(a, bytes, stream);
+    return (long long)p.B * p.max_pages > 8 * kShareThreads ? launch_release<16, 8>(a, bytes, stream)
+                                                            : launch_release<1, 8>(a, bytes, stream);
 }
 
 }  // namespace svf

@@ -270,6 +270,49 @@ def test_many_holders_leave_at_once(sv):
     assert set(before) <= set(d["pool"]["free"].tolist())
 
 
+@pytest.mark.parametrize("rows,top", [(60, 2000), (300, 1000)])
+def test_long_rows_leave_at_once(sv, rows, top):
+    """Releases of 120 and 300 thousand entries (a thread keeps its share, or reads it again), without
+    sharing as page_release does them, then of a third of rows and their forks, step by step."""
+    ps = 2
+    m = Model(rows * top + rows, rows, top, ps)
+    m.reserve([top * ps - 1] * rows)
+    d, e = device(m), device(m)
+    del e["pool"]["shares"]
+    keep = torch.zeros_like(d["lens"])
+    a = sv.page_release(d["pool"], d["table"], d["lens"], keep, ps)
+    b = sv.page_release(e["pool"], e["table"], e["lens"], keep, ps)
+    for k in a:
+        assert torch.equal(a[k], b[k])
+    assert torch.equal(d["table"], e["table"])
+    for k in ("free", "state"):
+        assert torch.equal(d["pool"][k], e["pool"][k])
+    assert not bool(d["pool"]["shares"].any())
+    third = rows // 3
+    m = Model(rows * top + rows, rows, top, ps)
+    m.reserve([top * ps - 1] * third + [0] * (rows - third))
+    d = device(m)
+    src = torch.arange(third, device="cuda", dtype=torch.int32)
+    for i in (1, 2):
+        f = sv.page_fork(d["pool"], d["table"], d["lens"], src, src + i * third, ps)
+        assert not bool(f["status"].any())
+    # the first third leaves what the others hold on to, the rest all but a page, then all
+    lens = d["lens"].clone()
+    keep = lens.clone()
+    keep[:third] = 0
+    r = sv.page_release(d["pool"], d["table"], lens, keep, ps)
+    assert r["n_released"].tolist() == [1] * third + [0] * (rows - third)  # its own last page
+    assert sorted(d["pool"]["shares"].unique().tolist()) == [0, 1]
+    lens, keep = keep.clone(), keep.clone()
+    keep[third:] = ps
+    r = sv.page_release(d["pool"], d["table"], lens, keep, ps)
+    assert r["n_released"].tolist() == [0] * third + [1] * third + [top - 1] * third
+    r = sv.page_release(d["pool"], d["table"], keep, torch.zeros_like(keep), ps)
+    assert r["n_released"].tolist() == [0] * 2 * third + [1] * third
+    assert not bool(d["pool"]["shares"].any()) and bool((d["table"] == -1).all())
+    assert sorted(d["pool"]["free"].tolist()) == list(range(rows * top + rows))
+
+
 def test_more_released_than_the_stack_holds(sv):
     """Pages given back twice: nothing is written behind the stack."""
     m = Model(6, 3, 4, 2)
