@@ -496,9 +496,11 @@ cudaError_t launch_page_release_shared(const PageReleaseArgs &p, int32_t *shares
     a.ps = p.page_size;
     a.num_pages = p.num_pages;
     const size_t bytes = (size_t)(2 * p.B + 1 + (p.B + 31) / 32) * sizeof(int);
-    // a table whose every page fits one rank a thread of 8 CTAs; larger ones 16, where such a
-    // cluster fits the device
-    if ((long long)p.B * p.max_pages > 8 * kShareThreads &&
+    // A table whose every page fits one rank a thread of 8 CTAs has the kernel for that; from 16
+    // thousand entries on 16 CTAs, where such a cluster fits the device. Forks, copies and release of
+    // 56 rows of 64, with 16 and with 8 CTAs (us): 145 entries a row 18.7 and 17.5, 252 20.0 and
+    // 20.1, 502 22.5 and 23.0, 1002 26.7 and 29.6, 2050 30.8 and 39.5.
+    if ((long long)p.B * p.max_pages > 16 * kShareThreads &&
         resident_clusters(page_release_shared_kernel<16, 16>, kShareThreads, bytes, 16) > 0)
         return launch_release<16, 16>(a, bytes, stream);
     return (long long)p.B * p.max_pages > 8 * kShareThreads ? launch_release<16, 8>(a, bytes, stream)
