@@ -31,8 +31,8 @@
 // TB/s, a copy's rate). With many the softmax warps: a tile of 256 rows by 128 tokens takes
 // them about 2700 cycles, of which the tensor cores have work for 2048, and a unit's end (the
 // last product, O out of tensor memory, the pieces that wait to be joined) 8 to 9 thousand.
-// A prompt of 8192 tokens, 32/8 heads: 437 us, 1258 TFLOP/s of its visible scores (66 % of the
-// measured burst rate); 8185 tokens after 24576, 64/8 heads: 4.9 to 5.4 ms (75 to 82 %), where the
+// A prompt of 8192 tokens, 32/8 heads: 424 to 433 us, 1280 TFLOP/s of its visible scores (67 %
+// of the measured burst rate); 8185 tokens after 24576, 64/8 heads: 4.9 to 5.4 ms (75 to 82 %), where the
 // power limit lowers the clock. One token over 2049: 21.5 us, all of it latency (layout 3.5, first
 // page numbers and K 2.2, tile 2, pieces 1.5, join 6).
 // Registers: 384 threads start with 168 each; the four warps of the first group keep 56 and the softmax
