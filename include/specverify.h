@@ -897,8 +897,8 @@ int svf_debug_lora_plan(int R, int rows_per_id, int H, int O, int adapters, int 
  * svf_debug_set_attn_wait_ns for the tree attention. A CTA whose wait runs out
  * leaves its loops, waits (with the default deadline) for its copies and
  * products in flight, releases its tensor memory, and the sequences that it had
- * tiles of get SVF_DEV_TIMEOUT. ns <= 0 restores the default of 2 s. Returns
- * SVF_OK.
+ * tiles of get SVF_DEV_TIMEOUT. ns <= 0 restores the default of 2 s (60 s for
+ * waits that may last as long as another role's work). Returns SVF_OK.
  * ---------------------------------------------------------------------- */
 int svf_debug_set_chunk_wait_ns(long long ns);
 
