@@ -313,6 +313,35 @@ def test_long_rows_leave_at_once(sv, rows, top):
     assert sorted(d["pool"]["free"].tolist()) == list(range(rows * top + rows))
 
 
+def test_a_captured_release_of_long_rows(sv):
+    """Forks of long rows and their release, replayed: everything is as before each time."""
+    B, top, ps = 40, 1500, 4
+    m = Model(B * 10 + 8 * top, B, top, ps)
+    m.reserve([top * ps - 1] * 5 + [0] * (B - 5))
+    d = device(m)
+    src = i32([i % 5 for i in range(B - 5)])
+    dst = torch.arange(5, B, device="cuda", dtype=torch.int32)
+    keep = d["lens"].clone()
+    torch.cuda.synchronize()
+    before = [d["table"].clone(), d["pool"]["free"].clone(), d["pool"]["state"].clone()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        f = sv.page_fork(d["pool"], d["table"], d["lens"], src, dst, ps)
+        held = d["lens"].clone()
+        r = sv.page_release(d["pool"], d["table"], held, keep, ps)
+        d["lens"].copy_(keep)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert not bool(f["status"].any()) and not bool(r["status"].any())
+        assert held.tolist() == [top * ps - 1] * B
+        assert r["n_released"].tolist() == [0] * 5 + [1] * (B - 5)
+        assert not bool(d["pool"]["shares"].any())
+        assert torch.equal(d["table"], before[0])
+        assert torch.equal(d["pool"]["state"], before[2])
+        assert sorted(d["pool"]["free"].tolist()) == sorted(before[1].tolist())
+
+
 def test_more_released_than_the_stack_holds(sv):
     """Pages given back twice: nothing is written behind the stack."""
     m = Model(6, 3, 4, 2)
